@@ -31,7 +31,8 @@
  *     ea_check_errors() reads back.
  *   - Every function returns an ea_status; no exception or abort crosses the ABI.
  *   - ea_route, ea_hybrid_attn_prefill, ea_hybrid_attn_prefill_varlen,
- *     ea_hybrid_attn_decode and ea_xa_estimate enqueue kernels only (no
+ *     ea_hybrid_attn_decode, ea_xa_estimate and the KV cache operators
+ *     (ea_cache_write, ea_evict_select, ea_cache_compact) enqueue kernels only (no
  *     allocation, no host synchronisation): after one call on the device
  *     (which raises the kernels' shared-memory limits), a call can be captured
  *     into a CUDA graph and replayed with new contents in the same buffers.
@@ -518,6 +519,127 @@ ea_status ea_xa_estimate(const void *Q, const void *K, const int64_t q_str[4],
                          const uint8_t *m, int stride, float threshold, int block_size,
                          int max_units, uint8_t *block_mask, float *block_scores, void *workspace,
                          size_t ws_bytes, void *stream);
+
+/*
+ * ------------------------------------------------------------------ KV caches
+ * A KV cache of one layer as the cache operators below read and write it: bf16
+ * rows, or 8-bit codes with one float scale per block of `scale_block`
+ * consecutive tokens and KV head (value = code * scale).  The pages have no
+ * counterpart: [EN] §08 leaves the cache of the decode phase open, and its
+ * size is what bounds batch and context there.
+ *
+ * A block's scale is a power of two, the least s = 2^e (e >= -64) with
+ * |x| <= qmax * s for every value x written to the block (qmax: 448 for E4M3,
+ * 127 for INT8), so that scaling is exact, a code is its value's correctly
+ * rounded one, and appended tokens seldom change the scale of the tokens
+ * before them.  A block that receives an infinity or a NaN gets a NaN scale:
+ * all of it reads as NaN until it is written again from its first token on.
+ *
+ *   K, V         device, codes (or bf16) at element strides kv_str[4]:
+ *                contiguous [outer = B][rows = Lmax][Hkv][d]; paged
+ *                [outer = num_pages][rows = page_size][Hkv][d]
+ *   k_scale, v_scale  device float [outer][Hkv][ceil(rows / scale_block)],
+ *                contiguous; NULL for EA_CACHE_BF16.  Scales of blocks that
+ *                hold no token are never used.
+ *   block_table  NULL for a contiguous cache; else device int32 [B][bt_stride]:
+ *                row p of sequence b is row p % rows of page
+ *                block_table[b][p / rows]; a sequence holds at most
+ *                max_pages * rows tokens
+ *   scale_block  16, 32, 64 or 128 (ignored for EA_CACHE_BF16); pages hold a
+ *                multiple of it
+ * Constraints: d == 128; K, V 16-byte aligned, the strides of the first three
+ * dimensions multiples of 16 bytes, head-dim stride 1; a paged sequence's
+ * capacity below 2^31.
+ */
+typedef enum {
+    EA_CACHE_BF16 = 0,
+    EA_CACHE_E4M3 = 1,   /* 8-bit float, 4 exponent and 3 fraction bits           */
+    EA_CACHE_INT8 = 2    /* -127 .. 127                                            */
+} ea_cache_format;
+
+typedef struct {
+    void *K;
+    void *V;
+    float *k_scale;
+    float *v_scale;
+    int64_t kv_str[4];
+    const int32_t *block_table;
+    int64_t bt_stride;
+    int outer;
+    int rows;
+    int max_pages;       /* of one sequence (paged); ignored without a table       */
+    int Hkv;
+    int d;
+    int format;          /* ea_cache_format                                        */
+    int scale_block;
+} ea_cache;
+
+/* Bytes of device workspace ea_cache_write, ea_evict_select and
+ * ea_cache_compact need (they only use its error word); 256-byte aligned. */
+size_t ea_cache_workspace_size(void);
+
+/*
+ * ea_cache_write - append new tokens to every sequence of a cache, quantising
+ * them (the prefill's keys and values, or one decode step's).
+ *
+ *   K_new, V_new device bf16 [B][T][Hkv][d], element strides n_str[4] (shared)
+ *   start        device int32 [B], the row of each sequence's first new token
+ *                (its length so far), or NULL: 0 for all
+ *   n_new        device int32 [B], new tokens of each sequence (0 .. T), or
+ *                NULL: T for all
+ * A block that already holds tokens below `start` keeps them: its scale is the
+ * larger of the stored one and the new tokens'; if it grows, the codes below
+ * `start` are rounded to it in the same launch.  Rows at or behind
+ * start + n_new stay as they are.  A sequence whose rows do not fit its
+ * capacity, or whose page is outside the cache, is reported by ea_check_errors
+ * and nothing is written for it (for a bad page: for the blocks in it).  Pages
+ * that receive tokens must belong to one sequence only.  B is c->outer for a
+ * contiguous cache.
+ */
+ea_status ea_cache_write(const ea_cache *c, const void *K_new, const void *V_new,
+                         const int64_t n_str[4], const int32_t *start, const int32_t *n_new, int B,
+                         int T, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * ea_evict_select - which tokens of each (sequence, KV head) stay when a cache
+ * is cut to `keep` tokens by accumulated attention weight: the first `sink`,
+ * the last `recent` and, of those between, the heaviest (equal weights: the
+ * earlier token; a NaN counts as less than every number), ascending.  A sequence of at most `keep`
+ * tokens keeps all of them.
+ *
+ *   weights      device float [B][Hkv][Lmax], contiguous
+ *   seqlens      device int32 [B], each in [0, Lmax]; one that is not is
+ *                reported by ea_check_errors and counts as 0
+ *   index        device int32 [B][Hkv][keep] (output); entries behind the kept
+ *                ones are -1
+ *   new_seqlens  device int32 [B] (output): min(seqlens, keep)
+ * Constraints: 1 <= keep, sink, recent >= 0, sink + recent <= keep,
+ * 1 <= Lmax <= 2^21 (more: EA_ERR_UNSUPPORTED).
+ */
+ea_status ea_evict_select(const float *weights, const int32_t *seqlens, int B, int Hkv, int Lmax,
+                          int keep, int sink, int recent, int32_t *index, int32_t *new_seqlens,
+                          void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * ea_cache_compact - gather kept tokens into another cache: row i < counts[b]
+ * of head h of sequence b of `dst` is row index[b][h][i] of `src`.  The formats
+ * may differ (a bf16 cache becomes an 8-bit one, or back); every block of an
+ * 8-bit dst is quantised anew from the values its tokens stand for.
+ *
+ *   index        device int32 [B][Hkv][keep]
+ *   counts       device int32 [B], each in [0, keep] (else reported and skipped)
+ *   weights, weights_out  device float [B][Hkv][src capacity] and
+ *                [B][Hkv][dst capacity], contiguous, or both NULL: the tokens'
+ *                accumulated weights move with them
+ * Rows of dst at or behind counts[b] stay as they are.  An index outside the
+ * source, or one whose page is outside it, is reported and reads zeros.  src
+ * and dst may share pages of one pool as long as no page is read and written;
+ * contiguous ones must not overlap (EA_ERR_INVALID_ARG).  keep is at most
+ * dst's capacity; src and dst have the same Hkv.
+ */
+ea_status ea_cache_compact(const ea_cache *src, const ea_cache *dst, const int32_t *index,
+                           const int32_t *counts, int B, int keep, const float *weights,
+                           float *weights_out, void *workspace, size_t ws_bytes, void *stream);
 
 /*
  * ea_sparsity_ratios - model sparsity ratio and effective sparsity ratio of one

@@ -13,6 +13,9 @@ present, the device entry points raise instead of computing anything else.
     ea_hybrid_attn_prefill_varlen  sequences of different lengths in one launch
     ea_hybrid_attn_decode    split-KV decode with the prefill-time routing
     ea_hybrid_attn_decode_paged  the same decode over a paged KV cache
+    ea_cache_write           new tokens into a KV cache of 8 bits (or bf16), quantised
+    ea_evict_select          which tokens stay when a cache is cut by those weights
+    ea_cache_compact         gathers them into another cache
     ea_sparsity_ratios       Omega_MSR / Omega_ESR (host)
     ea_check_errors          read back the device error word of a workspace
 """
@@ -40,7 +43,8 @@ EXPORTS = ("ea_status_string", "ea_route", "ea_route_layers", "ea_prefill_worksp
            "ea_prefill_layers_workspace_size", "ea_hybrid_attn_prefill_layers",
            "ea_decode_workspace_size",
            "ea_hybrid_attn_decode", "ea_hybrid_attn_decode_paged", "ea_xa_workspace_size",
-           "ea_xa_estimate", "ea_sparsity_ratios", "ea_check_errors")
+           "ea_xa_estimate", "ea_cache_workspace_size", "ea_cache_write", "ea_evict_select",
+           "ea_cache_compact", "ea_sparsity_ratios", "ea_check_errors")
 
 
 class EAError(RuntimeError):
@@ -58,6 +62,15 @@ class _PrefillLayer(ctypes.Structure):
     _fields_ = [("Q", ctypes.c_void_p), ("K", ctypes.c_void_p), ("V", ctypes.c_void_p),
                 ("O", ctypes.c_void_p), ("LSE", ctypes.c_void_p), ("m", ctypes.c_void_p),
                 ("block_mask", ctypes.c_void_p)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("kv_str", ctypes.c_int64 * 4),
+                ("block_table", ctypes.c_void_p), ("bt_stride", ctypes.c_int64),
+                ("outer", ctypes.c_int), ("rows", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("Hkv", ctypes.c_int), ("d", ctypes.c_int), ("format", ctypes.c_int),
+                ("scale_block", ctypes.c_int)]
 
 
 MAX_PREFILL_LAYERS = 48
@@ -130,11 +143,16 @@ def lib():
         L.ea_xa_estimate.argtypes = [P, P, P, P, i32, i32, i32, i32, i32, f32, P, i32, f32, i32,
                                      i32, P, P, P, sz, P]
         L.ea_xa_estimate.restype = ctypes.c_int
+        L.ea_cache_workspace_size.argtypes = []
+        L.ea_cache_workspace_size.restype = sz
+        L.ea_cache_write.argtypes = [P, P, P, P, P, P, i32, i32, P, sz, P]
+        L.ea_evict_select.argtypes = [P, P, i32, i32, i32, i32, i32, i32, P, P, P, sz, P]
+        L.ea_cache_compact.argtypes = [P, P, P, P, i32, i32, P, P, P, sz, P]
         L.ea_sparsity_ratios.argtypes = [P, P, i32, i32, i32, i32, i32, P, i32,
                                          ctypes.POINTER(f64), ctypes.POINTER(f64)]
         L.ea_check_errors.argtypes = [P, P]
         for f in ("ea_route", "ea_route_layers", "ea_hybrid_attn_prefill", "ea_prefill_plan", "ea_prefill_attend",
-                  "ea_hybrid_attn_decode",
+                  "ea_hybrid_attn_decode", "ea_cache_write", "ea_evict_select", "ea_cache_compact",
                   "ea_sparsity_ratios", "ea_check_errors"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
@@ -624,6 +642,219 @@ def ea_xa_estimate(Q, K, m, *, threshold=0.9, max_units=None, block_mask=None,
                               _ptr(workspace), workspace.numel(), _stream(stream))
     _check("ea_xa_estimate", st)
     return block_mask, block_scores
+
+
+CACHE_FORMATS = {torch.bfloat16: 0, torch.float8_e4m3fn: 1, torch.int8: 2}
+SCALE_BLOCKS = (16, 32, 64, 128)
+
+
+class KVCache:
+    """One layer's KV cache as the cache operators use it: a handle over the
+    caller's tensors, made once and kept as long as they are.
+
+    K, V: [B, Lmax, Hkv, 128], or with a block_table (int32 [B, max_pages])
+    pages [num_pages, page_size, Hkv, 128]; bfloat16, float8_e4m3fn or int8.
+    k_scale, v_scale (8-bit formats): float32 [B or num_pages, Hkv,
+    ceil(rows / scale_block)], one scale per block of scale_block tokens and
+    head.  ``kv_cache`` and ``kv_cache_paged`` allocate an empty one."""
+
+    def __init__(self, K, V, k_scale=None, v_scale=None, *, scale_block=64, block_table=None):
+        _dev(K, "K")
+        _dev(V, "V", K.dtype)
+        if K.dtype not in CACHE_FORMATS:
+            raise ValueError("K and V must be bfloat16, float8_e4m3fn or int8, got %s" % K.dtype)
+        if K.dim() != 4 or V.shape != K.shape or V.stride() != K.stride():
+            raise ValueError("K and V must share 4-dimensional shapes and strides")
+        outer, rows, Hkv, d = K.shape
+        if outer < 1 or rows < 1 or Hkv < 1:
+            raise ValueError("an empty cache")
+        self.quantized = K.dtype != torch.bfloat16
+        if self.quantized:
+            if scale_block not in SCALE_BLOCKS:
+                raise ValueError("scale_block must be one of %s" % (SCALE_BLOCKS,))
+            shape = (outer, Hkv, -(-rows // scale_block))
+            for t, nm in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                _dev(t, nm, torch.float32)
+                if tuple(t.shape) != shape or not t.is_contiguous():
+                    raise ValueError("%s must be a contiguous %s tensor" % (nm, list(shape)))
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        if block_table is not None:
+            _dev(block_table, "block_table", torch.int32)
+            if block_table.dim() != 2 or block_table.shape[1] < 1 or (
+                    block_table.shape[1] > 1 and block_table.stride(1) != 1):
+                raise ValueError("block_table must be [B, max_pages] with unit column stride")
+            if self.quantized and rows % scale_block:
+                raise ValueError("pages must hold a multiple of scale_block rows")
+        _one_device(K, V, k_scale, v_scale, block_table)
+        self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
+        self.scale_block, self.block_table = scale_block, block_table
+        self.B = outer if block_table is None else block_table.shape[0]
+        self.max_pages = 0 if block_table is None else block_table.shape[1]
+        self.capacity = rows * max(self.max_pages, 1)
+        self.Hkv, self.device = Hkv, K.device
+        self._c = _Cache(K.data_ptr(), V.data_ptr(), 0 if k_scale is None else k_scale.data_ptr(),
+                         0 if v_scale is None else v_scale.data_ptr(),
+                         (ctypes.c_int64 * 4)(*K.stride()),
+                         0 if block_table is None else block_table.data_ptr(),
+                         0 if block_table is None else max(block_table.stride(0), self.max_pages),
+                         outer, rows, self.max_pages, Hkv, d, CACHE_FORMATS[K.dtype], scale_block)
+        self._ref = ctypes.byref(self._c)
+
+
+def _alloc_cache(outer, rows, Hkv, dtype, scale_block, device, block_table):
+    K = torch.zeros(outer, rows, Hkv, 128, dtype=dtype, device=device)
+    scales = [None, None]
+    if dtype != torch.bfloat16:
+        scales = [torch.zeros(outer, Hkv, -(-rows // scale_block), device=device) for _ in range(2)]
+    return KVCache(K, torch.zeros_like(K), *scales, scale_block=scale_block, block_table=block_table)
+
+
+def kv_cache(B, Lmax, Hkv, *, dtype=torch.float8_e4m3fn, scale_block=64, device="cuda"):
+    """An empty contiguous cache [B, Lmax, Hkv, 128]."""
+    return _alloc_cache(B, Lmax, Hkv, dtype, scale_block, device, None)
+
+
+def kv_cache_paged(num_pages, page_size, Hkv, block_table, *, dtype=torch.float8_e4m3fn,
+                   scale_block=64):
+    """An empty pool of pages [num_pages, page_size, Hkv, 128] read through
+    block_table (int32 [B, max_pages], CUDA)."""
+    return _alloc_cache(num_pages, page_size, Hkv, dtype, scale_block, block_table.device, block_table)
+
+
+def _one_device(*tensors):
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) > 1:
+        raise ValueError("tensors on several devices: %s" % sorted(map(str, devs)))
+
+
+class _at:
+    """Runs a call on the device of its tensors and on the stream it names (the
+    device's current one if none), allocations included."""
+
+    def __init__(self, device, stream):
+        self.ctx = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def _i32_vec(t, name, B):
+    if t is not None:
+        _dev(t, name, torch.int32)
+        if tuple(t.shape) != (B,) or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous int32 [%d] tensor" % (name, B))
+    return t
+
+
+def _like(t, name, shape, dtype):
+    _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s %s tensor" % (name, dtype, list(shape)))
+    return t
+
+
+def ea_cache_workspace_size():
+    return int(lib().ea_cache_workspace_size())
+
+
+def cache_workspace(device="cuda"):
+    """A zeroed workspace of ea_cache_write, ea_evict_select and ea_cache_compact
+    (their error word)."""
+    return torch.zeros(ea_cache_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def ea_cache_write(cache, K, V, start=None, n_new=None, *, workspace=None, stream=None):
+    """Append K, V [B, T, Hkv, 128] (bf16, CUDA) to the sequences of a KVCache at
+    rows start[b] (int32 [B]; None: 0), the first n_new[b] (int32 [B]; None: T)
+    tokens of each, quantising them for an 8-bit cache."""
+    _dev(K, "K", torch.bfloat16)
+    _dev(V, "V", torch.bfloat16)
+    if K.dim() != 4 or V.shape != K.shape or V.stride() != K.stride():
+        raise ValueError("K and V must share 4-dimensional shapes and strides")
+    B, T, Hkv, d = K.shape
+    if (B, Hkv, d) != (cache.B, cache.Hkv, 128):
+        raise ValueError("K and V must be [%d, T, %d, 128]" % (cache.B, cache.Hkv))
+    _i32_vec(start, "start", B)
+    _i32_vec(n_new, "n_new", B)
+    _one_device(cache.K, K, V, start, n_new, workspace)
+    with _at(cache.device, stream) as st:
+        if workspace is None:
+            workspace = cache_workspace(cache.device)
+        _check("ea_cache_write", lib().ea_cache_write(
+            cache._ref, K.data_ptr(), V.data_ptr(), _strides(K), _ptr(start), _ptr(n_new), B, T,
+            workspace.data_ptr(), workspace.numel(), st))
+
+
+def ea_evict_select(weights, seqlens, *, keep, sink=0, recent=0, index=None, new_seqlens=None,
+                    workspace=None, stream=None):
+    """The tokens that stay when every sequence is cut to `keep`: the first
+    `sink`, the last `recent` and the heaviest of the others by weights (float32
+    [B, Hkv, Lmax]), per KV head, ascending.  Returns (index int32 [B, Hkv,
+    keep], -1 behind the kept ones; new_seqlens int32 [B])."""
+    _dev(weights, "weights", torch.float32)
+    if weights.dim() != 3 or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous [B, Hkv, Lmax] tensor")
+    B, Hkv, Lmax = weights.shape
+    if seqlens is None:
+        raise ValueError("seqlens is needed")
+    _i32_vec(seqlens, "seqlens", B)
+    _i32_vec(new_seqlens, "new_seqlens", B)
+    if index is not None:
+        _like(index, "index", (B, Hkv, keep), torch.int32)
+    _one_device(weights, seqlens, index, new_seqlens, workspace)
+    with _at(weights.device, stream) as st:
+        if index is None:
+            index = torch.empty(B, Hkv, max(int(keep), 0), dtype=torch.int32, device=weights.device)
+        if new_seqlens is None:
+            new_seqlens = torch.empty(B, dtype=torch.int32, device=weights.device)
+        if workspace is None:
+            workspace = cache_workspace(weights.device)
+        _check("ea_evict_select", lib().ea_evict_select(
+            weights.data_ptr(), seqlens.data_ptr(), B, Hkv, Lmax, int(keep), int(sink), int(recent),
+            index.data_ptr(), new_seqlens.data_ptr(), workspace.data_ptr(), workspace.numel(), st))
+    return index, new_seqlens
+
+
+def ea_cache_compact(src, dst, index, counts, *, weights=None, weights_out=None, workspace=None,
+                     stream=None):
+    """Gather rows index[b, h, i] (int32 [B, Hkv, keep]; i < counts[b], int32
+    [B]) of KVCache src into rows i of KVCache dst; the formats may differ.
+    weights / weights_out (float32 [B, Hkv, capacity]): the tokens' accumulated
+    weights move along."""
+    B, Hkv = dst.B, dst.Hkv
+    if (src.B, src.Hkv) != (B, Hkv):
+        raise ValueError("src and dst must have the same sequences and heads")
+    _dev(index, "index", torch.int32)
+    if index.dim() != 3 or index.shape[:2] != (B, Hkv) or not index.is_contiguous():
+        raise ValueError("index must be a contiguous [%d, %d, keep] tensor" % (B, Hkv))
+    if counts is None:
+        raise ValueError("counts is needed")
+    _i32_vec(counts, "counts", B)
+    if (weights is None) != (weights_out is None):
+        raise ValueError("weights and weights_out go together")
+    if weights is not None:
+        _like(weights, "weights", (B, Hkv, src.capacity), torch.float32)
+        _like(weights_out, "weights_out", (B, Hkv, dst.capacity), torch.float32)
+    _one_device(src.K, dst.K, index, counts, weights, weights_out, workspace)
+    with _at(dst.device, stream) as st:
+        if workspace is None:
+            workspace = cache_workspace(dst.device)
+        _check("ea_cache_compact", lib().ea_cache_compact(
+            src._ref, dst._ref, index.data_ptr(), counts.data_ptr(), B, index.shape[2], _ptr(weights),
+            _ptr(weights_out), workspace.data_ptr(), workspace.numel(), st))
 
 
 def ea_sparsity_ratios(r, m, S, *, sink, window, block_masks=None):

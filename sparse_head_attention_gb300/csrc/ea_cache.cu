@@ -1,0 +1,789 @@
+// ea_cache.cu - writing a KV cache (quantising to 8 bits with one scale per
+// block of tokens and KV head), choosing the tokens that stay when it is cut by
+// accumulated attention weight, and gathering those into another cache.
+//
+// All three only move data, so what bounds them is HBM for long inputs and the
+// latency of a launch and a few dependent loads for short ones.
+//   cache_write_kernel    one CTA per (block of tokens, KV head, sequence, K or
+//                         V).  A row of a head is 16 threads x 16 bytes, so 128
+//                         threads hold a whole block in registers: one read
+//                         finds the block's largest value, sets the scale, and
+//                         the same registers are rounded and stored.
+//   cache_compact_kernel  the same over gathered rows of another cache.
+//   evict_select_kernel   a cluster of CTAs per (sequence, KV head): a radix
+//                         search for the lightest weight that stays, then one
+//                         ordered pass that lists the tokens.
+#include <cuda_runtime.h>
+
+#include "ea_cache.cuh"
+#include "ea_internal.h"
+
+namespace ea {
+
+constexpr int kCacheThreads = 128;
+constexpr int kRowThreads = 16;                            // threads of one row: 8 elements each
+constexpr int kRowsPerPass = kCacheThreads / kRowThreads;  // 8
+
+// Row p of sequence b: the cache's outer index and row in it; false (reported)
+// if its page is outside the cache.
+__device__ __forceinline__ bool locate(const CacheDev &c, int b, int p, int &outer, int &row,
+                                       uint32_t *err)
+{
+    if (!c.table) {
+        outer = b;
+        row = p;
+        return true;
+    }
+    const int pg = p / c.rows;
+    row = p - pg * c.rows;
+    outer = c.table[b * c.bt_stride + pg];
+    if (outer >= 0 && outer < c.outer)
+        return true;
+    raise_error(err, EA_DEVERR_CHECK);
+    outer = 0;
+    return false;
+}
+
+// Maximum over the CTA (128 threads).
+__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t *red)
+{
+    v = __reduce_max_sync(0xffffffffu, v);
+    if ((threadIdx.x & 31) == 0)
+        red[threadIdx.x / 32] = v;
+    __syncthreads();
+    return max(max(red[0], red[1]), max(red[2], red[3]));
+}
+
+// Eight bf16 as floats.
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint32_t amax8(const float (&x)[8])
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    return m;
+}
+
+struct WriteArgs {
+    CacheDev c;
+    const __nv_bfloat16 *x[2];
+    int64_t n_sb, n_st, n_sh;
+    const int32_t *start, *n_new;
+    uint32_t *err;
+    int T, blocks;       // blocks: token blocks a sequence's new tokens can touch
+};
+
+template <int SB, int FMT>
+__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const WriteArgs a)
+{
+    constexpr bool kE4M3 = FMT == EA_CACHE_E4M3;
+    constexpr int kPasses = SB / kRowsPerPass;
+    __shared__ uint32_t red[4];
+    const int h = blockIdx.x % a.c.Hkv, blk = blockIdx.x / a.c.Hkv;
+    const int b = blockIdx.y, kv = blockIdx.z;
+    const int start = a.start ? a.start[b] : 0, n = a.n_new ? a.n_new[b] : a.T;
+    if (start < 0 || n < 0 || n > a.T || static_cast<int64_t>(start) + n > a.c.cap) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && kv == 0)
+            raise_error(a.err, EA_DEVERR_CHECK);
+        return;
+    }
+    const int p0 = (start / SB + blk) * SB;              // the block's first row
+    const int lo = max(start, p0), hi = min(start + n, p0 + SB);
+    if (lo >= hi)
+        return;
+    int outer, row0;
+    if (!locate(a.c, b, p0, outer, row0, a.err))
+        return;
+    const int r = threadIdx.x / kRowThreads, e0 = threadIdx.x % kRowThreads * 8;
+    const __nv_bfloat16 *src = a.x[kv] + b * a.n_sb + h * a.n_sh + e0;
+    const int64_t dst0 = outer * a.c.s_outer + row0 * a.c.s_row + h * a.c.s_head + e0;
+
+    uint4 raw[kPasses];
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int p = p0 + i * kRowsPerPass + r;
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (p >= lo && p < hi)
+            raw[i] = __ldg(reinterpret_cast<const uint4 *>(src + (p - start) * a.n_st));
+    }
+    if constexpr (FMT == EA_CACHE_BF16) {
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.c.code[kv]) + dst0;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int p = p0 + i * kRowsPerPass + r;
+            if (p >= lo && p < hi)
+                *reinterpret_cast<uint4 *>(dst + (p - p0) * a.c.s_row) = raw[i];
+        }
+    } else {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            unpack8(raw[i], x);
+            mx = max(mx, amax8(x));
+        }
+        float s = block_scale(cta_max(mx, red), kE4M3);
+        float *sp = a.c.scale[kv] + (static_cast<int64_t>(outer) * a.c.Hkv + h) * a.c.nsb + row0 / SB;
+        uint8_t *dst = static_cast<uint8_t *>(a.c.code[kv]) + dst0;
+        if (lo > p0) {
+            // the block already holds rows p0 .. lo - 1
+            const float was = *sp;
+            __syncthreads();                 // every thread has read it before it changes
+            if (!(was <= s)) {
+                s = isnan(s) ? s : was;      // larger, or NaN: it stays
+            } else if (was < s) {
+                const float f = was / s;
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const int k = i * kRowsPerPass + r;
+                    if (p0 + k < lo) {
+                        uint2 *w = reinterpret_cast<uint2 *>(dst + k * a.c.s_row);
+                        float u[4], v[4];
+                        decode4<kE4M3>(w->x, u);
+                        decode4<kE4M3>(w->y, v);
+                        *w = make_uint2(encode4<kE4M3>(u[0] * f, u[1] * f, u[2] * f, u[3] * f),
+                                        encode4<kE4M3>(v[0] * f, v[1] * f, v[2] * f, v[3] * f));
+                    }
+                }
+            }
+        }
+        if (threadIdx.x == 0)
+            *sp = s;
+        const float inv = isnan(s) ? 0.f : 1.f / s;          // a power of two: exact
+        const bool dead = isnan(s);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int p = p0 + i * kRowsPerPass + r;
+            if (p >= lo && p < hi) {
+                unpack8(raw[i], x);
+                uint2 w = make_uint2(0u, 0u);
+                if (!dead)
+                    w = make_uint2(encode4<kE4M3>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                                   encode4<kE4M3>(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+                *reinterpret_cast<uint2 *>(dst + (p - p0) * a.c.s_row) = w;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ compaction
+struct CompactArgs {
+    CacheDev src, dst;
+    const int32_t *index, *counts;
+    const float *w;
+    float *w_out;
+    uint32_t *err;
+    int keep;
+};
+
+// One row's eight elements of a cache, as stored.
+template <int FMT>
+struct Raw8 {
+    uint2 v;
+};
+template <>
+struct Raw8<EA_CACHE_BF16> {
+    uint4 v;
+};
+
+template <int FMT>
+__device__ __forceinline__ void values8(const Raw8<FMT> &raw, float s, float (&x)[8])
+{
+    if constexpr (FMT == EA_CACHE_BF16) {
+        unpack8(raw.v, x);
+    } else {
+        float u[4], v[4];
+        decode4<FMT == EA_CACHE_E4M3>(raw.v.x, u);
+        decode4<FMT == EA_CACHE_E4M3>(raw.v.y, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = u[i] * s;
+            x[4 + i] = v[i] * s;
+        }
+    }
+}
+
+template <int SB, int SRC, int DST>
+__global__ void __launch_bounds__(kCacheThreads) cache_compact_kernel(const CompactArgs a)
+{
+    constexpr bool kE4M3 = DST == EA_CACHE_E4M3;
+    constexpr int kPasses = SB / kRowsPerPass;
+    using Elem = typename std::conditional<SRC == EA_CACHE_BF16, uint16_t, uint8_t>::type;
+    __shared__ uint32_t red[4];
+    const int h = blockIdx.x % a.dst.Hkv, blk = blockIdx.x / a.dst.Hkv;
+    const int b = blockIdx.y, kv = blockIdx.z;
+    const int n = a.counts[b];
+    if (n < 0 || n > a.keep) {
+        if (threadIdx.x == 0 && blockIdx.x == 0 && kv == 0)
+            raise_error(a.err, EA_DEVERR_CHECK);
+        return;
+    }
+    const int p0 = blk * SB;
+    if (p0 >= n)
+        return;
+    int outer, row0;
+    if (!locate(a.dst, b, p0, outer, row0, a.err))
+        return;
+    const int r = threadIdx.x / kRowThreads, e0 = threadIdx.x % kRowThreads * 8;
+    const int64_t unit = static_cast<int64_t>(b) * a.dst.Hkv + h;
+    const int32_t *index = a.index + unit * a.keep;
+    const Elem *src = static_cast<const Elem *>(a.src.code[kv]) + h * a.src.s_head + e0;
+
+    // rows of this thread: index, then page, then data, each step's loads together
+    int at[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int p = p0 + i * kRowsPerPass + r;
+        at[i] = p < n ? __ldg(index + p) : -1;
+        if (p < n && (at[i] < 0 || at[i] >= a.src.cap)) {
+            raise_error(a.err, EA_DEVERR_CHECK);
+            at[i] = -1;
+        }
+    }
+    int so[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        so[i] = b;
+        if (a.src.table && at[i] >= 0) {
+            int row;
+            if (!locate(a.src, b, at[i], so[i], row, a.err))
+                row = -1;
+            at[i] = row;
+        }
+    }
+    Raw8<SRC> raw[kPasses];
+    float sc[kPasses];
+    const float *ssrc = a.src.scale[kv];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        raw[i] = Raw8<SRC>{};
+        sc[i] = 0.f;
+        if (at[i] >= 0) {
+            raw[i].v = __ldg(reinterpret_cast<const decltype(raw[i].v) *>(src + so[i] * a.src.s_outer +
+                                                                         at[i] * a.src.s_row));
+            if constexpr (SRC != EA_CACHE_BF16)
+                sc[i] = __ldg(ssrc + (static_cast<int64_t>(so[i]) * a.src.Hkv + h) * a.src.nsb +
+                              (at[i] >> a.src.log2sb));
+        }
+    }
+    const int64_t dst0 = outer * a.dst.s_outer + row0 * a.dst.s_row + h * a.dst.s_head + e0;
+    float x[8];
+    if constexpr (DST == EA_CACHE_BF16) {
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.dst.code[kv]) + dst0;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int k = i * kRowsPerPass + r;
+            if (p0 + k < n) {
+                values8<SRC>(raw[i], sc[i], x);
+                *reinterpret_cast<uint4 *>(dst + k * a.dst.s_row) =
+                    make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+            }
+        }
+    } else {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            values8<SRC>(raw[i], sc[i], x);
+            mx = max(mx, amax8(x));
+        }
+        const float s = block_scale(cta_max(mx, red), kE4M3);
+        if (threadIdx.x == 0)
+            a.dst.scale[kv][(static_cast<int64_t>(outer) * a.dst.Hkv + h) * a.dst.nsb + row0 / SB] = s;
+        const bool dead = isnan(s);
+        const float inv = 1.f / s;
+        uint8_t *dst = static_cast<uint8_t *>(a.dst.code[kv]) + dst0;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int k = i * kRowsPerPass + r;
+            if (p0 + k < n) {
+                values8<SRC>(raw[i], sc[i], x);
+                uint2 w = make_uint2(0u, 0u);
+                if (!dead)
+                    w = make_uint2(encode4<kE4M3>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                                   encode4<kE4M3>(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+                *reinterpret_cast<uint2 *>(dst + k * a.dst.s_row) = w;
+            }
+        }
+    }
+    if (kv == 0 && a.w) {
+        for (int k = threadIdx.x; k < SB && p0 + k < n; k += kCacheThreads) {
+            const int i = index[p0 + k];
+            a.w_out[unit * a.dst.cap + p0 + k] = i >= 0 && i < a.src.cap ? a.w[unit * a.src.cap + i] : 0.f;
+        }
+    }
+}
+
+// ------------------------------------------------------------ selection
+constexpr int kSelThreads = 1024;
+constexpr int kSelBits = 11;                 // digits: bits 31..21, 20..10, 9..0
+constexpr int kSelBins = 1 << kSelBits;
+constexpr int kSelMaxCluster = 8;
+
+struct SelectArgs {
+    const float *w;
+    const int32_t *seqlens;
+    int32_t *index, *new_seqlens;
+    uint32_t *err;
+    int Hkv, Lmax, keep, sink, recent;
+};
+
+struct SelSmem {
+    uint32_t hist[3][kSelBins];
+    uint32_t warp[32];
+    uint32_t digit, above;                   // result of one radix step
+    uint32_t n_above, n_equal;               // this CTA's tokens above / at the threshold
+};
+
+// Order-preserving bits of a weight: larger weight, larger key; -0 equals +0;
+// a NaN is below everything.
+__device__ __forceinline__ uint32_t weight_key(float f)
+{
+    if (isnan(f))
+        return 0u;
+    const uint32_t u = f == 0.f ? 0u : __float_as_uint(f);
+    return (u >> 31) ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cl_addr)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cl_addr) : "memory");
+    return v;
+}
+
+// Inclusive sum over the CTA (1024 threads); `total` is the whole sum.
+__device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t *warp_sums, uint32_t &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    __syncthreads();                          // warp_sums of the previous call have been read
+    if (lane == 31)
+        warp_sums[warp] = x;
+    __syncthreads();
+    uint32_t s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o)
+            s += y;
+    }
+    total = __shfl_sync(0xffffffffu, s, 31);
+    const uint32_t before = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+    return x + (warp > 0 ? before : 0u);
+}
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a)
+{
+    __shared__ SelSmem sm;
+    const int tid = threadIdx.x;
+    const int C = gridDim.x, rank = blockIdx.x;        // one cluster spans the x dimension
+    const int unit = blockIdx.y + gridDim.y * blockIdx.z;
+    const int b = unit / a.Hkv;
+    int L = a.seqlens[b];
+    if (L < 0 || L > a.Lmax) {
+        if (tid == 0 && rank == 0)
+            raise_error(a.err, EA_DEVERR_CHECK);
+        L = 0;
+    }
+    const int n_keep = min(L, a.keep);
+    int32_t *out = a.index + static_cast<int64_t>(unit) * a.keep;
+    if (tid == 0 && rank == 0 && unit % a.Hkv == 0)
+        a.new_seqlens[b] = n_keep;
+    // entries behind the kept ones
+    for (int i = n_keep + rank * kSelThreads + tid; i < a.keep; i += C * kSelThreads)
+        out[i] = -1;
+    if (L <= a.keep) {                                  // the same in every CTA of the cluster
+        for (int i = rank * kSelThreads + tid; i < L; i += C * kSelThreads)
+            out[i] = i;
+        return;
+    }
+    for (int i = tid; i < 3 * kSelBins; i += kSelThreads)
+        (&sm.hist[0][0])[i] = 0u;
+    __syncthreads();
+
+    // this CTA's share of the middle tokens [sink, L - recent)
+    const float *w = a.w + static_cast<int64_t>(unit) * a.Lmax;
+    const int m0 = a.sink, m1 = L - a.recent;
+    const int len = (m1 - m0 + C - 1) / C;
+    const int lo = min(m0 + rank * len, m1), hi = min(lo + len, m1);
+    uint32_t want = a.keep - a.sink - a.recent;         // tokens of the middle that stay (< m1 - m0)
+    uint32_t prefix = 0;                                // the threshold's digits found so far
+#pragma unroll 1
+    for (int step = 0; step < 3; ++step) {
+        const int shift = step == 0 ? 21 : step == 1 ? 10 : 0;
+        const uint32_t mask = step == 2 ? 0x3ffu : 0x7ffu;
+        const int up = shift + (step == 2 ? 10 : 11);
+#pragma unroll 4
+        for (int i = lo + tid; i < hi; i += kSelThreads) {
+            const uint32_t k = weight_key(__ldg(w + i));
+            if (step == 0 || (k >> up) == prefix)
+                atomicAdd(&sm.hist[step][(k >> shift) & mask], 1u);
+        }
+        cluster_sync_all();
+        // thread t sums bins from the top: 2047 - 2t and 2046 - 2t
+        uint32_t c0 = 0, c1 = 0;
+        const int top = kSelBins - 1 - 2 * tid;
+        for (int r = 0; r < C; ++r) {
+            c0 += ld_cluster_u32(mapa_shared(smem_u32(&sm.hist[step][top]), r));
+            c1 += ld_cluster_u32(mapa_shared(smem_u32(&sm.hist[step][top - 1]), r));
+        }
+        uint32_t total;
+        const uint32_t incl = cta_scan(c0 + c1, sm.warp, total), excl = incl - c0 - c1;
+        // the bin that holds the want-th largest (want 0: nothing of the middle stays)
+        if (want > excl && want <= excl + c0) {
+            sm.digit = top;
+            sm.above = excl;
+        } else if (want > excl + c0 && want <= incl) {
+            sm.digit = top - 1;
+            sm.above = excl + c0;
+        }
+        __syncthreads();
+        if (want == 0)
+            break;                                       // the same in every CTA
+        prefix = step == 0 ? sm.digit : prefix << (step == 2 ? 10 : 11) | sm.digit;
+        want -= sm.above;
+        __syncthreads();
+    }
+    // tokens with a key above `prefix` stay, and the first `want` of those equal to it
+    const bool none = a.keep == a.sink + a.recent;
+    const uint32_t thr = none ? 0xffffffffu : prefix;    // no key reaches 0xffffffff
+    if (tid == 0)
+        sm.n_above = sm.n_equal = 0u;
+    __syncthreads();
+    uint32_t na = 0, ne = 0;
+#pragma unroll 4
+    for (int i = lo + tid; i < hi; i += kSelThreads) {
+        const uint32_t k = weight_key(__ldg(w + i));
+        na += k > thr;
+        ne += k == thr;
+    }
+    na = __reduce_add_sync(0xffffffffu, na);
+    ne = __reduce_add_sync(0xffffffffu, ne);
+    if ((tid & 31) == 0) {
+        atomicAdd(&sm.n_above, na);
+        atomicAdd(&sm.n_equal, ne);
+    }
+    cluster_sync_all();
+    uint32_t above = 0, equal = 0;                       // in the CTAs before this one
+    for (int r = 0; r < rank; ++r) {
+        above += ld_cluster_u32(mapa_shared(smem_u32(&sm.n_above), r));
+        equal += ld_cluster_u32(mapa_shared(smem_u32(&sm.n_equal), r));
+    }
+    // ordered list: four consecutive tokens a thread
+    uint32_t pos = a.sink + above + min(equal, want);
+    for (int i0 = lo; i0 < hi; i0 += 4 * kSelThreads) {
+        uint32_t k[4], mine = 0;                         // tokens above << 16 | equal, of this thread
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + 4 * tid + j;
+            k[j] = i < hi ? weight_key(__ldg(w + i)) : 0u;
+            mine += i < hi ? (k[j] > thr ? 0x10000u : k[j] == thr ? 1u : 0u) : 0u;
+        }
+        uint32_t total;
+        const uint32_t before = cta_scan(mine, sm.warp, total) - mine;
+        uint32_t eq = equal + (before & 0xffffu);        // equal ones before this thread's
+        uint32_t at = pos + (before >> 16) + (min(eq, want) - min(equal, want));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + 4 * tid + j;
+            if (i >= hi)
+                break;
+            bool stay = k[j] > thr;
+            if (k[j] == thr)
+                stay = eq++ < want;
+            if (stay)
+                out[at++] = i;
+        }
+        pos += (total >> 16) + (min(equal + (total & 0xffffu), want) - min(equal, want));
+        equal += total & 0xffffu;
+    }
+    // the protected tokens on both sides
+    for (int i = rank * kSelThreads + tid; i < a.sink; i += C * kSelThreads)
+        out[i] = i;
+    for (int i = rank * kSelThreads + tid; i < a.recent; i += C * kSelThreads)
+        out[a.keep - a.recent + i] = m1 + i;
+    cluster_sync_all();                                  // no CTA leaves while its counts may be read
+}
+
+// ------------------------------------------------------------ launches
+bool cache_dev(const ea_cache *c, int B, CacheDev &d, ea_status &why)
+{
+    why = EA_ERR_INVALID_ARG;
+    if (!c || !c->K || !c->V || c->format < EA_CACHE_BF16 || c->format > EA_CACHE_INT8 || c->rows < 1 ||
+        c->outer < 1 || c->Hkv < 1 || B < 1)
+        return false;
+    const bool wide = c->format == EA_CACHE_BF16;
+    const int sb = wide ? 64 : c->scale_block;
+    if (!wide && (!c->k_scale || !c->v_scale))
+        return false;
+    if (c->d != EA_HEAD_DIM || (sb != 16 && sb != 32 && sb != 64 && sb != 128) || B > 65535 ||
+        c->Hkv > 65535) {
+        why = EA_ERR_UNSUPPORTED;
+        return false;
+    }
+    if (c->kv_str[3] != 1)
+        return false;
+    const int unit = wide ? 8 : 16;                     // elements of 16 bytes
+    for (int k = 0; k < 3; ++k)
+        if (c->kv_str[k] <= 0 || c->kv_str[k] % unit)
+            return false;
+    for (const void *p : {static_cast<const void *>(c->K), static_cast<const void *>(c->V)})
+        if (reinterpret_cast<uintptr_t>(p) & 15u)
+            return false;
+    int64_t cap = c->rows;
+    if (c->block_table) {
+        if (c->max_pages < 1 || c->bt_stride < c->max_pages)
+            return false;
+        if (!wide && c->rows % sb) {
+            why = EA_ERR_UNSUPPORTED;
+            return false;
+        }
+        cap = static_cast<int64_t>(c->rows) * c->max_pages;
+    } else if (c->outer != B) {
+        return false;
+    }
+    if (cap > (int64_t(1) << 31) - 256) {               // row numbers are 32-bit
+        why = EA_ERR_UNSUPPORTED;
+        return false;
+    }
+    d.code[0] = c->K;
+    d.code[1] = c->V;
+    d.scale[0] = c->k_scale;
+    d.scale[1] = c->v_scale;
+    d.s_outer = c->kv_str[0];
+    d.s_row = c->kv_str[1];
+    d.s_head = c->kv_str[2];
+    d.table = c->block_table;
+    d.bt_stride = c->bt_stride;
+    d.rows = c->rows;
+    d.outer = c->outer;
+    d.cap = static_cast<int>(cap);
+    d.Hkv = c->Hkv;
+    d.nsb = static_cast<int>(ceil_div(c->rows, sb));
+    d.log2sb = sb == 16 ? 4 : sb == 32 ? 5 : sb == 64 ? 6 : 7;
+    d.format = c->format;
+    why = EA_OK;
+    return true;
+}
+
+static bool ws_ok(const void *ws, size_t bytes)
+{
+    return ws && !(reinterpret_cast<uintptr_t>(ws) & 255u) && bytes >= sizeof(ea_ws_header);
+}
+
+template <int SB>
+static void launch_write(const WriteArgs &a, dim3 grid, cudaStream_t st)
+{
+    if (a.c.format == EA_CACHE_E4M3)
+        cache_write_kernel<SB, EA_CACHE_E4M3><<<grid, kCacheThreads, 0, st>>>(a);
+    else
+        cache_write_kernel<SB, EA_CACHE_INT8><<<grid, kCacheThreads, 0, st>>>(a);
+}
+
+template <int SB, int SRC>
+static void launch_compact_src(const CompactArgs &a, dim3 grid, cudaStream_t st)
+{
+    if (a.dst.format == EA_CACHE_E4M3)
+        cache_compact_kernel<SB, SRC, EA_CACHE_E4M3><<<grid, kCacheThreads, 0, st>>>(a);
+    else if (a.dst.format == EA_CACHE_INT8)
+        cache_compact_kernel<SB, SRC, EA_CACHE_INT8><<<grid, kCacheThreads, 0, st>>>(a);
+    else if constexpr (SB == 64)                        // bf16 has no blocks: cut in 64 rows
+        cache_compact_kernel<SB, SRC, EA_CACHE_BF16><<<grid, kCacheThreads, 0, st>>>(a);
+}
+
+template <int SB>
+static void launch_compact(const CompactArgs &a, dim3 grid, cudaStream_t st)
+{
+    if (a.src.format == EA_CACHE_BF16)
+        launch_compact_src<SB, EA_CACHE_BF16>(a, grid, st);
+    else if (a.src.format == EA_CACHE_E4M3)
+        launch_compact_src<SB, EA_CACHE_E4M3>(a, grid, st);
+    else
+        launch_compact_src<SB, EA_CACHE_INT8>(a, grid, st);
+}
+
+// Bytes [lo, hi) that K or V of a cache may span.
+static void span(const ea_cache *c, const void *p, uintptr_t &lo, uintptr_t &hi)
+{
+    const int64_t size = c->format == EA_CACHE_BF16 ? 2 : 1;
+    const int64_t last = (c->outer - 1) * c->kv_str[0] + (c->rows - 1) * c->kv_str[1] +
+                         (c->Hkv - 1) * c->kv_str[2] + c->d;
+    lo = reinterpret_cast<uintptr_t>(p);
+    hi = lo + static_cast<uintptr_t>(last * size);
+}
+
+} // namespace ea
+
+using namespace ea;
+
+extern "C" size_t ea_cache_workspace_size(void) { return sizeof(ea_ws_header); }
+
+extern "C" ea_status ea_cache_write(const ea_cache *c, const void *K_new, const void *V_new,
+                                    const int64_t n_str[4], const int32_t *start,
+                                    const int32_t *n_new, int B, int T, void *workspace,
+                                    size_t ws_bytes, void *stream)
+{
+    if (!K_new || !V_new || !n_str || T < 1)
+        return EA_ERR_INVALID_ARG;
+    WriteArgs a{};
+    ea_status why;
+    if (!cache_dev(c, B, a.c, why))
+        return why;
+    if (n_str[3] != 1)
+        return EA_ERR_INVALID_ARG;
+    for (int k = 0; k < 3; ++k)
+        if (n_str[k] <= 0 || n_str[k] % 8)
+            return EA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(K_new) | reinterpret_cast<uintptr_t>(V_new)) & 15u)
+        return EA_ERR_INVALID_ARG;
+    const int sb = 1 << a.c.log2sb;
+    // new tokens of any length start at any row of a block (bf16 pages need not
+    // hold a multiple of the 64 rows used there)
+    const int64_t blocks = (static_cast<int64_t>(T) + 2 * sb - 2) / sb;
+    if (blocks * a.c.Hkv >= (int64_t(1) << 31))
+        return EA_ERR_UNSUPPORTED;
+    if (c->format == EA_CACHE_BF16 && c->block_table && c->rows % 64)
+        return EA_ERR_UNSUPPORTED;
+    if (!ws_ok(workspace, ws_bytes))
+        return EA_ERR_WORKSPACE;
+    a.x[0] = static_cast<const __nv_bfloat16 *>(K_new);
+    a.x[1] = static_cast<const __nv_bfloat16 *>(V_new);
+    a.n_sb = n_str[0];
+    a.n_st = n_str[1];
+    a.n_sh = n_str[2];
+    a.start = start;
+    a.n_new = n_new;
+    a.err = &static_cast<ea_ws_header *>(workspace)->error;
+    a.T = T;
+    a.blocks = static_cast<int>(blocks);
+    const dim3 grid(static_cast<unsigned>(blocks * a.c.Hkv), static_cast<unsigned>(B), 2);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (a.c.format == EA_CACHE_BF16)
+        cache_write_kernel<64, EA_CACHE_BF16><<<grid, kCacheThreads, 0, st>>>(a);
+    else if (sb == 16)
+        launch_write<16>(a, grid, st);
+    else if (sb == 32)
+        launch_write<32>(a, grid, st);
+    else if (sb == 64)
+        launch_write<64>(a, grid, st);
+    else
+        launch_write<128>(a, grid, st);
+    return cudaGetLastError() == cudaSuccess ? EA_OK : EA_ERR_CUDA;
+}
+
+extern "C" ea_status ea_cache_compact(const ea_cache *src, const ea_cache *dst,
+                                      const int32_t *index, const int32_t *counts, int B, int keep,
+                                      const float *weights, float *weights_out, void *workspace,
+                                      size_t ws_bytes, void *stream)
+{
+    if (!index || !counts || keep < 1 || !weights != !weights_out || (weights && weights == weights_out))
+        return EA_ERR_INVALID_ARG;
+    CompactArgs a{};
+    ea_status why;
+    if (!cache_dev(src, B, a.src, why) || !cache_dev(dst, B, a.dst, why))
+        return why;
+    if (a.src.Hkv != a.dst.Hkv || keep > a.dst.cap)
+        return EA_ERR_INVALID_ARG;
+    if (dst->format == EA_CACHE_BF16 && dst->block_table && dst->rows % 64)
+        return EA_ERR_UNSUPPORTED;
+    if (!src->block_table || !dst->block_table) {
+        for (const void *p : {src->K, src->V})
+            for (const void *q : {dst->K, dst->V}) {
+                uintptr_t p0, p1, q0, q1;
+                span(src, p, p0, p1);
+                span(dst, q, q0, q1);
+                if (p0 < q1 && q0 < p1)
+                    return EA_ERR_INVALID_ARG;
+            }
+    }
+    if (!ws_ok(workspace, ws_bytes))
+        return EA_ERR_WORKSPACE;
+    const int sb = 1 << a.dst.log2sb;
+    const int64_t blocks = ceil_div(keep, sb);
+    if (blocks * a.dst.Hkv >= (int64_t(1) << 31))
+        return EA_ERR_UNSUPPORTED;
+    a.index = index;
+    a.counts = counts;
+    a.w = weights;
+    a.w_out = weights_out;
+    a.err = &static_cast<ea_ws_header *>(workspace)->error;
+    a.keep = keep;
+    const dim3 grid(static_cast<unsigned>(blocks * a.dst.Hkv), static_cast<unsigned>(B), 2);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (sb == 16)
+        launch_compact<16>(a, grid, st);
+    else if (sb == 32)
+        launch_compact<32>(a, grid, st);
+    else if (sb == 64)
+        launch_compact<64>(a, grid, st);
+    else
+        launch_compact<128>(a, grid, st);
+    return cudaGetLastError() == cudaSuccess ? EA_OK : EA_ERR_CUDA;
+}
+
+extern "C" ea_status ea_evict_select(const float *weights, const int32_t *seqlens, int B, int Hkv,
+                                     int Lmax, int keep, int sink, int recent, int32_t *index,
+                                     int32_t *new_seqlens, void *workspace, size_t ws_bytes,
+                                     void *stream)
+{
+    if (!weights || !seqlens || !index || !new_seqlens || B < 1 || Hkv < 1 || Lmax < 1 || keep < 1 ||
+        sink < 0 || recent < 0 || static_cast<int64_t>(sink) + recent > keep)
+        return EA_ERR_INVALID_ARG;
+    if (Lmax > EA_MAX_SEQ || keep > EA_MAX_SEQ || B > 65535 || Hkv > 65535)
+        return EA_ERR_UNSUPPORTED;
+    if (!ws_ok(workspace, ws_bytes))
+        return EA_ERR_WORKSPACE;
+    SelectArgs a{};
+    a.w = weights;
+    a.seqlens = seqlens;
+    a.index = index;
+    a.new_seqlens = new_seqlens;
+    a.err = &static_cast<ea_ws_header *>(workspace)->error;
+    a.Hkv = Hkv;
+    a.Lmax = Lmax;
+    a.keep = keep;
+    a.sink = sink;
+    a.recent = recent;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return EA_ERR_CUDA;
+    const int sms = num_sms(dev);
+    if (sms <= 0)
+        return EA_ERR_CUDA;
+    // CTAs of a (sequence, head): as many as fill the GPU, while each has a few
+    // thousand tokens
+    int C = 1;
+    while (C < kSelMaxCluster && static_cast<int64_t>(B) * Hkv * C * 2 <= 2 * sms && Lmax / (2 * C) >= 2048)
+        C *= 2;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(C), static_cast<unsigned>(Hkv), static_cast<unsigned>(B));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, evict_select_kernel, a) != cudaSuccess)
+        return EA_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? EA_OK : EA_ERR_CUDA;
+}

@@ -1,0 +1,176 @@
+"""Plain CPU implementations of the KV cache operators, in 64 bits, written from
+their definitions (imported by the tests of those operators).
+
+A reference cache is a dict: K, V (codes or bf16), ks, vs (float32 scales, None
+for bf16), table (int32 [B, pages] or None), sb (tokens of a scale block)."""
+import math
+
+import numpy as np
+import torch
+
+E4M3, INT8, BF16 = torch.float8_e4m3fn, torch.int8, torch.bfloat16
+QMAX = {E4M3: 448.0, INT8: 127.0}
+
+
+def tokens(shape, seed):
+    """bf16 N(0, 1), one token in fifty eight times larger."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(shape, generator=g)
+    big = torch.rand(shape[:-1], generator=g) < 0.02
+    return (x * torch.where(big, 8.0, 1.0)[..., None]).to(BF16)
+
+
+def block_scale(amax, dtype):
+    """The least power of two s >= 2^-64 with amax <= qmax * s; NaN for a non-finite amax."""
+    if not math.isfinite(amax):
+        return math.nan
+    e = -64
+    if amax > 0:
+        e = max(e, math.frexp(amax)[1] - 12)
+    while amax > QMAX[dtype] * 2.0 ** e:
+        e += 1
+    return 2.0 ** e
+
+
+def encode(x, dtype):
+    """float64 values (already divided by the scale) -> the nearest codes, ties to even."""
+    x = np.asarray(x, np.float64)
+    if dtype == INT8:
+        return torch.from_numpy(np.rint(x).astype(np.int8))
+    e = np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -6)))
+    step = np.exp2(e - 3)
+    y = np.copysign(np.abs(np.rint(x / step) * step), x)      # exactly an e4m3 value
+    return torch.from_numpy(y).float().to(E4M3)
+
+
+def rows_of(c, b, p):
+    """(outer index, row) of row p of sequence b; None if its page is outside the cache."""
+    if c["table"] is None:
+        return b, p
+    page = c["K"].shape[1]
+    o = int(c["table"][b, p // page])
+    return (o, p % page) if 0 <= o < c["K"].shape[0] else None
+
+
+def values(codes, scales, sb):
+    """float64 values of contiguous codes [B, L, H, D] with scales [B, H, n]."""
+    if scales is None:
+        return codes.double()
+    s = scales.double().repeat_interleave(sb, -1)[..., : codes.shape[1]]
+    return codes.float().double() * s.transpose(1, 2)[..., None]
+
+
+def capacity(c):
+    return c["K"].shape[1] * (1 if c["table"] is None else c["table"].shape[1])
+
+
+def make_table(B, n, spare, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randperm(B * n + spare, generator=g)[: B * n].view(B, n).to(torch.int32)
+
+
+def make_cache(B, cap, Hkv, dtype, sb, page, seed, spare=2):
+    """A reference cache whose every row holds a token (written whole)."""
+    table = make_table(B, -(-cap // page), spare, seed) if page else None
+    outer, rows = (B, cap) if not page else (B * table.shape[1] + spare, page)
+    c = dict(K=torch.zeros(outer, rows, Hkv, 128, dtype=dtype), V=torch.zeros(outer, rows, Hkv, 128, dtype=dtype),
+             ks=None, vs=None, table=table, sb=sb)
+    if dtype != BF16:
+        c["ks"] = torch.ones(outer, Hkv, -(-rows // sb))
+        c["vs"] = torch.ones_like(c["ks"])
+    n = capacity(c)
+    write_ref(c, tokens((B, n, Hkv, 128), seed + 1000), tokens((B, n, Hkv, 128), seed + 2000), [0] * B, [n] * B)
+    return c
+
+
+def _write_block(c, kv, sc, b, p0, lo, x):
+    """Rows lo .. lo + len(x) of sequence b, all in the block that starts at p0; x float64 [n, Hkv, 128]."""
+    at = rows_of(c, b, p0)
+    if at is None:
+        return
+    o, r = at
+    codes, dtype = c[kv], c[kv].dtype
+    k, n = lo - p0, len(x)
+    if dtype == BF16:
+        codes[o, r + k : r + k + n] = torch.from_numpy(x).to(BF16)
+        return
+    i = r // c["sb"]
+    for h in range(codes.shape[2]):
+        part = x[:, h]
+        amax = float(np.abs(part).max()) if np.isfinite(part).all() else math.inf
+        s = block_scale(amax, dtype)
+        if k:
+            was = float(c[sc][o, h, i])
+            if math.isnan(was) or math.isnan(s):
+                s = math.nan
+            elif was > s:
+                s = was
+            elif was < s:
+                old = codes[o, r : r + k, h].float().double().numpy()
+                codes[o, r : r + k, h] = encode(old * (was / s), dtype)
+        new = torch.zeros(n, 128).to(dtype) if math.isnan(s) else encode(part / s, dtype)
+        codes[o, r + k : r + k + n, h] = new
+        c[sc][o, h, i] = s
+
+
+def write_ref(c, K, V, start, n):
+    """ea_cache_write; start[b] None: the sequence is refused."""
+    sb = c["sb"] if c["ks"] is not None else 64
+    for kv, sc, x in (("K", "ks", K), ("V", "vs", V)):
+        for b in range(x.shape[0]):
+            if start[b] is None or n[b] == 0:
+                continue
+            p, end = start[b], start[b] + n[b]
+            xb = x[b].double().numpy()
+            while p < end:
+                p0 = p // sb * sb
+                stop = min(p0 + sb, end)
+                _write_block(c, kv, sc, b, p0, p, xb[p - start[b] : stop - start[b]])
+                p = stop
+
+
+def compact_ref(src, dst, index, counts, w, w_out):
+    """ea_cache_compact, into dst (and w_out)."""
+    B, Hkv = index.shape[:2]
+    sb = dst["sb"] if dst["ks"] is not None else 64
+    cap = capacity(src)
+    for b in range(B):
+        n = counts[b]
+        if not n:
+            continue
+        for kv, sc in (("K", "ks"), ("V", "vs")):
+            x = np.zeros((n, Hkv, 128))
+            for h in range(Hkv):
+                for i in range(n):
+                    p = int(index[b, h, i])
+                    at = rows_of(src, b, p) if 0 <= p < cap else None
+                    if at is None:
+                        continue
+                    v = src[kv][at[0], at[1], h].float().double().numpy()
+                    if src[sc] is not None:
+                        v = v * float(src[sc][at[0], h, at[1] // src["sb"]])
+                    x[i, h] = v
+            for p0 in range(0, n, sb):
+                _write_block(dst, kv, sc, b, p0, p0, x[p0 : p0 + sb][: n - p0])
+        if w is not None:
+            for h in range(Hkv):
+                w_out[b, h, :n] = w[b, h, index[b, h, :n].long()]
+
+
+def select_ref(w, lens, keep, sink, recent):
+    """ea_evict_select on float32 weights [B, Hkv, Lmax]."""
+    B, Hkv, _ = w.shape
+    index = np.full((B, Hkv, keep), -1, np.int32)
+    for b, L in enumerate(lens):
+        n = min(L, keep)
+        for h in range(Hkv):
+            if L <= keep:
+                index[b, h, :n] = np.arange(n)
+                continue
+            mid = np.arange(sink, L - recent)
+            x = w[b, h, mid].astype(np.float64)
+            nan = np.isnan(x)
+            order = np.lexsort((mid, -np.where(nan, 0.0, x), nan))       # numbers first, then heavy, then early
+            best = mid[order[: keep - sink - recent]]
+            index[b, h] = np.sort(np.concatenate([np.arange(sink), best, np.arange(L - recent, L)]))
+    return index, np.array([min(L, keep) for L in lens], np.int32)
