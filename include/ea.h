@@ -32,7 +32,8 @@
  *   - Every function returns an ea_status; no exception or abort crosses the ABI.
  *   - ea_route, ea_hybrid_attn_prefill, ea_hybrid_attn_prefill_varlen,
  *     ea_hybrid_attn_decode, ea_xa_estimate and the KV cache operators
- *     (ea_cache_write, ea_evict_select, ea_cache_compact) enqueue kernels only (no
+ *     (ea_cache_write, ea_hybrid_attn_decode_q8, ea_evict_select,
+ *     ea_cache_compact) enqueue kernels only (no
  *     allocation, no host synchronisation): after one call on the device
  *     (which raises the kernels' shared-memory limits), a call can be captured
  *     into a CUDA graph and replayed with new contents in the same buffers.
@@ -640,6 +641,40 @@ ea_status ea_evict_select(const float *weights, const int32_t *seqlens, int B, i
 ea_status ea_cache_compact(const ea_cache *src, const ea_cache *dst, const int32_t *index,
                            const int32_t *counts, int B, int keep, const float *weights,
                            float *weights_out, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of device workspace ea_hybrid_attn_decode_q8 needs (0 on invalid
+ * sizes); with_weights != 0 adds the scores of one step (4 bytes per query
+ * head and cache row), needed when key_weights is given. */
+size_t ea_decode_q8_workspace_size(int B, int Hq, int Hkv, int d, int Lmax, int num_splits,
+                                   int with_weights);
+
+/*
+ * ea_hybrid_attn_decode_q8 - ea_hybrid_attn_decode over an 8-bit cache
+ * (contiguous or paged), on the values its codes stand for, and the attention
+ * weight each cached token received.
+ *
+ *   cache        EA_CACHE_E4M3 or EA_CACHE_INT8; Lmax below is its capacity per
+ *                sequence (rows, or max_pages * rows)
+ *   key_weights  device float [B][Hkv][Lmax] contiguous, or NULL.  For every
+ *                key j < seqlens[b] of KV head h: the sum over the group's
+ *                query heads of exp(scale * q . k_j - LSE) if the head's mode
+ *                keeps j, else 0, is added to key_weights[b][h][j]
+ *                (accumulate != 0) or stored there (accumulate == 0).  Entries
+ *                at or behind seqlens[b] stay as they are.
+ *   workspace    ea_decode_q8_workspace_size(B, Hq, Hkv, d, Lmax, num_splits,
+ *                key_weights != NULL) bytes
+ * A kept key of a block with a NaN scale makes its head's O and LSE NaN.
+ * Codes and scales behind seqlens[b] are not used, whatever they hold.  Other
+ * arguments, modes, masks, constraints and errors as ea_hybrid_attn_decode;
+ * pages hold a multiple of 64 rows.
+ */
+ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cache, void *O, float *LSE,
+                                   const int64_t q_str[3], const int64_t o_str[3],
+                                   const int32_t *seqlens, int B, int Hq, float scale,
+                                   const uint8_t *m, int sink, int window,
+                                   const uint8_t *block_mask, int block_size, int num_splits,
+                                   float *key_weights, int accumulate, void *workspace,
+                                   size_t ws_bytes, void *stream);
 
 /*
  * ea_sparsity_ratios - model sparsity ratio and effective sparsity ratio of one

@@ -14,6 +14,7 @@ present, the device entry points raise instead of computing anything else.
     ea_hybrid_attn_decode    split-KV decode with the prefill-time routing
     ea_hybrid_attn_decode_paged  the same decode over a paged KV cache
     ea_cache_write           new tokens into a KV cache of 8 bits (or bf16), quantised
+    ea_hybrid_attn_decode_q8 the decode over an 8-bit cache, with the keys' attention weights
     ea_evict_select          which tokens stay when a cache is cut by those weights
     ea_cache_compact         gathers them into another cache
     ea_sparsity_ratios       Omega_MSR / Omega_ESR (host)
@@ -44,7 +45,8 @@ EXPORTS = ("ea_status_string", "ea_route", "ea_route_layers", "ea_prefill_worksp
            "ea_decode_workspace_size",
            "ea_hybrid_attn_decode", "ea_hybrid_attn_decode_paged", "ea_xa_workspace_size",
            "ea_xa_estimate", "ea_cache_workspace_size", "ea_cache_write", "ea_evict_select",
-           "ea_cache_compact", "ea_sparsity_ratios", "ea_check_errors")
+           "ea_cache_compact", "ea_decode_q8_workspace_size", "ea_hybrid_attn_decode_q8",
+           "ea_sparsity_ratios", "ea_check_errors")
 
 
 class EAError(RuntimeError):
@@ -148,12 +150,16 @@ def lib():
         L.ea_cache_write.argtypes = [P, P, P, P, P, P, i32, i32, P, sz, P]
         L.ea_evict_select.argtypes = [P, P, i32, i32, i32, i32, i32, i32, P, P, P, sz, P]
         L.ea_cache_compact.argtypes = [P, P, P, P, i32, i32, P, P, P, sz, P]
+        L.ea_decode_q8_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+        L.ea_decode_q8_workspace_size.restype = sz
+        L.ea_hybrid_attn_decode_q8.argtypes = [P, P, P, P, P, P, P, i32, i32, f32, P, i32, i32, P,
+                                               i32, i32, P, i32, P, sz, P]
         L.ea_sparsity_ratios.argtypes = [P, P, i32, i32, i32, i32, i32, P, i32,
                                          ctypes.POINTER(f64), ctypes.POINTER(f64)]
         L.ea_check_errors.argtypes = [P, P]
         for f in ("ea_route", "ea_route_layers", "ea_hybrid_attn_prefill", "ea_prefill_plan", "ea_prefill_attend",
                   "ea_hybrid_attn_decode", "ea_cache_write", "ea_evict_select", "ea_cache_compact",
-                  "ea_sparsity_ratios", "ea_check_errors"):
+                  "ea_hybrid_attn_decode_q8", "ea_sparsity_ratios", "ea_check_errors"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -796,6 +802,64 @@ def ea_cache_write(cache, K, V, start=None, n_new=None, *, workspace=None, strea
         _check("ea_cache_write", lib().ea_cache_write(
             cache._ref, K.data_ptr(), V.data_ptr(), _strides(K), _ptr(start), _ptr(n_new), B, T,
             workspace.data_ptr(), workspace.numel(), st))
+
+
+def ea_decode_q8_workspace_size(B, Hq, Hkv, Lmax, num_splits=0, weights=False, d=128):
+    return int(lib().ea_decode_q8_workspace_size(B, Hq, Hkv, d, Lmax, num_splits, 1 if weights else 0))
+
+
+def decode_q8_workspace(B, Hq, Hkv, Lmax, num_splits=0, weights=False, d=128, device="cuda"):
+    """A zeroed workspace of ea_hybrid_attn_decode_q8 (weights: with key_weights)."""
+    n = ea_decode_q8_workspace_size(B, Hq, Hkv, Lmax, num_splits, weights, d)
+    if n == 0:
+        raise ValueError("unsupported decode sizes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def ea_hybrid_attn_decode_q8(q, cache, seqlens, m, *, sink, window, block_mask=None, num_splits=0,
+                             scale=None, key_weights=None, accumulate=True, O=None, LSE=None,
+                             workspace=None, stream=None, want_lse=True):
+    """One decode step over an 8-bit KVCache: q [B, Hq, 128] bf16, seqlens int32
+    [B], m uint8 [B, Hkv], block_mask uint8 [B, Hkv, nB, nB] (nB =
+    ceil(capacity / 128)) when a head is BLOCK; all CUDA.  key_weights (float32
+    [B, Hkv, capacity]) receives each cached key's attention weight of this
+    step, summed over the group's heads: added (accumulate) or stored.
+    Returns (O, LSE)."""
+    _dev(q, "q", torch.bfloat16)
+    _dev(m, "m", torch.uint8)
+    if q.dim() != 3 or q.shape[0] != cache.B or q.shape[2] != 128:
+        raise ValueError("q must be [%d, Hq, 128]" % cache.B)
+    if not cache.quantized:
+        raise ValueError("a bfloat16 cache is read by ea_hybrid_attn_decode")
+    B, Hq, d = q.shape
+    if seqlens is None:
+        raise ValueError("seqlens is needed")
+    _i32_vec(seqlens, "seqlens", B)
+    _like(m, "m", (B, cache.Hkv), torch.uint8)
+    bm = _block_mask_arg(block_mask, B, cache.Hkv, cache.capacity)
+    if key_weights is not None:
+        _like(key_weights, "key_weights", (B, cache.Hkv, cache.capacity), torch.float32)
+    if O is not None:
+        _dev(O, "O", torch.bfloat16)
+        if O.shape != q.shape:
+            raise ValueError("O must have q's shape")
+    if LSE is not None:
+        _like(LSE, "LSE", (B, Hq), torch.float32)
+    _one_device(cache.K, q, seqlens, m, bm, key_weights, O, LSE, workspace)
+    with _at(cache.device, stream) as st:
+        if O is None:
+            O = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if LSE is None and want_lse:
+            LSE = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = decode_q8_workspace(B, Hq, cache.Hkv, cache.capacity, num_splits,
+                                            key_weights is not None, d, q.device)
+        _check("ea_hybrid_attn_decode_q8", lib().ea_hybrid_attn_decode_q8(
+            q.data_ptr(), cache._ref, O.data_ptr(), _ptr(LSE), _strides(q), _strides(O),
+            seqlens.data_ptr(), B, Hq, 1.0 / math.sqrt(d) if scale is None else float(scale),
+            m.data_ptr(), int(sink), int(window), _ptr(bm), TILE, int(num_splits),
+            _ptr(key_weights), 1 if accumulate else 0, workspace.data_ptr(), workspace.numel(), st))
+    return O, LSE
 
 
 def ea_evict_select(weights, seqlens, *, keep, sink=0, recent=0, index=None, new_seqlens=None,

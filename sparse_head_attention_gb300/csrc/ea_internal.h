@@ -86,6 +86,11 @@ bool encode_tmap_bf16_4d(void *tmap_out, const void *base, int d, int H, int S, 
                          const int64_t strides_elems[4], int box_inner, int box_rows,
                          bool swizzle128);
 
+// Encodes a 4-D map of 8-bit elements (same dims) with a 128 x 1 x box_rows x 1
+// box and 128-byte swizzle; d must be 128.
+bool encode_tmap_u8_4d(void *tmap_out, const void *base, int d, int H, int S, int B,
+                       const int64_t strides_elems[4], int box_rows);
+
 // Encodes a 5-D bf16 TMA tensor map that reads tokens as cells of `stride`
 // consecutive tokens: dims (head dim, heads, offset u in the cell, cell a,
 // batch), token a * stride + u; the sequence length must be nA * stride.  Box:

@@ -174,3 +174,83 @@ def select_ref(w, lens, keep, sink, recent):
             best = mid[order[: keep - sink - recent]]
             index[b, h] = np.sort(np.concatenate([np.arange(sink), best, np.arange(L - recent, L)]))
     return index, np.array([min(L, keep) for L in lens], np.int32)
+
+
+def logical(c):
+    """K, V [B, capacity, Hkv, 128] float64 of a reference cache, its pages in order (pages outside it: zeros)."""
+    out = []
+    for kv, sc in (("K", "ks"), ("V", "vs")):
+        codes, scales, table = c[kv], c[sc], c["table"]
+        if table is None:
+            out.append(values(codes, scales, c["sb"]).numpy())
+            continue
+        per = values(codes, scales, c["sb"])
+        ok = (table >= 0) & (table < codes.shape[0])
+        x = per[table.clamp(0, codes.shape[0] - 1).long()]
+        x = torch.where(ok[..., None, None, None], x, 0.0)
+        out.append(x.reshape(table.shape[0], -1, *codes.shape[2:]).numpy())
+    return out
+
+
+def value_scales(c):
+    """The scale of V of every row, [B, capacity, Hkv] float64 (pages outside the cache: 1)."""
+    rows, table = c["K"].shape[1], c["table"]
+    per = c["vs"].double().repeat_interleave(c["sb"], -1)[..., :rows].transpose(1, 2)       # [outer, rows, Hkv]
+    if table is None:
+        return per.numpy()
+    ok = (table >= 0) & (table < per.shape[0])
+    x = torch.where(ok[..., None, None], per[table.clamp(0, per.shape[0] - 1).long()], 1.0)
+    return x.reshape(table.shape[0], -1, per.shape[2]).numpy()
+
+
+def kept_keys(mode, L, sink, window, mask):
+    """Which of the keys 0 .. L - 1 a decode row of a sequence of length L keeps."""
+    j = np.arange(L)
+    if mode == 1:
+        return (j < sink) | (L - 1 - j < window)
+    if mode == 2:
+        return mask[(L - 1) // 128][j // 128] != 0
+    return np.ones(L, bool)
+
+
+def decode_ref(q, K, V, vs, lens, modes, sink, window, scale, bm=None):
+    """float64 (O, LSE, weights, tolerances) of a decode step on K, V [B, cap, Hkv, 128] float64.
+
+    Tolerances, from the arithmetic: a logit is an fp32 sum of 128 products, off by at most 128 * 2^-23 of the sum
+    of their magnitudes (each addition may be truncated), plus three fp32 roundings of its size; call that d.  The
+    probabilities are off by 2 d + 2^-20 relative (exp2 and the normaliser).  What multiplies V's codes is w_j = p_j s_j
+    (s_j the scale of V's block) in units that put the largest at 2^14, rounded to f16: by 2^-11 of itself, or, below
+    f16's normal range, by half of f16's smallest step 2^-24, which is 2^-25 / 2^14 = 2^-39 of the largest p s; times
+    the code v_j / s_j.  The output is rounded to bf16 (2^-8)."""
+    q = q.double().numpy()
+    B, Hq, D = q.shape
+    cap, Hkv = K.shape[1], K.shape[2]
+    g = Hq // Hkv
+    O, LSE, W = np.zeros((B, Hq, D)), np.full((B, Hq), -np.inf), np.zeros((B, Hkv, cap))
+    tO, tL, tW = np.zeros_like(O), np.zeros_like(LSE), np.zeros_like(W)
+    for b, L in enumerate(lens):
+        for h in range(Hkv):
+            if L == 0:
+                continue
+            keep = kept_keys(modes[b][h], L, sink, window, None if bm is None else bm[b, h])
+            at = np.nonzero(keep)[0]
+            if not len(at):
+                continue
+            k, v = K[b, at, h], V[b, at, h]
+            for i in range(h * g, (h + 1) * g):
+                x = scale * (k @ q[b, i])
+                d = 2.0 ** -16 * scale * (np.abs(k) @ np.abs(q[b, i])) + 2.0 ** -22 * np.abs(x)
+                top = x.max()
+                p = np.exp(x - top)
+                l = p.sum()
+                LSE[b, i] = top + np.log(l)
+                p /= l
+                O[b, i] = p @ v
+                W[b, h, at] += p
+                rel = 2 * d.max() + 2.0 ** -20
+                s = vs[b, at, h]
+                floor = 2.0 ** -39 * (p * s).max() * (np.abs(v) / s[:, None]).sum(0)
+                tO[b, i] = 2.0 ** -8 * np.abs(O[b, i]) + (rel + 2.0 ** -11) * (p @ np.abs(v)) * 1.01 + 1.01 * floor + 1e-30
+                tL[b, i] = d.max() + 2.0 ** -20 * (1 + abs(LSE[b, i]))
+                tW[b, h, at] += p * rel + 1e-38
+    return O, LSE, W, (tO, tL, tW)
