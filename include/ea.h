@@ -32,8 +32,8 @@
  *   - Every function returns an ea_status; no exception or abort crosses the ABI.
  *   - ea_route, ea_hybrid_attn_prefill, ea_hybrid_attn_prefill_varlen,
  *     ea_hybrid_attn_decode, ea_xa_estimate and the KV cache operators
- *     (ea_cache_write, ea_hybrid_attn_decode_q8, ea_evict_select,
- *     ea_cache_compact) enqueue kernels only (no
+ *     (ea_cache_write, ea_hybrid_attn_decode_q8, ea_key_weights,
+ *     ea_evict_select, ea_cache_compact) enqueue kernels only (no
  *     allocation, no host synchronisation): after one call on the device
  *     (which raises the kernels' shared-memory limits), a call can be captured
  *     into a CUDA graph and replayed with new contents in the same buffers.
@@ -675,6 +675,45 @@ ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cache, void *O
                                    const uint8_t *block_mask, int block_size, int num_splits,
                                    float *key_weights, int accumulate, void *workspace,
                                    size_t ws_bytes, void *stream);
+
+/* Bytes of device workspace ea_key_weights needs (0 on invalid sizes). */
+size_t ea_key_weights_workspace_size(int B, int Tq, int Lmax, int Hq, int Hkv, int d);
+
+/*
+ * ea_key_weights - the attention weight that the last Tq query rows of each
+ * sequence give its keys: all of a prefill (Tq = S), an observation window at
+ * its end, or one decode step over a bf16 cache (Tq = 1).
+ *
+ * Query row t of sequence b sits at position i = seqlens[b] - Tq + t (a
+ * negative one does not count); head h keeps key j <= i by its mode as
+ * ea_hybrid_attn_prefill states.  For every key j < seqlens[b]:
+ *   sum over rows t and the group's query heads that keep j of
+ *     exp(scale * q_t . k_j - LSE[b][qh][t])
+ * is added to weights[b][h][j] (accumulate != 0) or stored there
+ * (accumulate == 0).  Entries at or behind seqlens[b] stay as they are.  Rows
+ * with LSE = -inf (no kept key) give nothing.  The order of summation is
+ * fixed: equal calls give equal bits.
+ *
+ *   Q            device bf16 [B][Tq][Hq][d], element strides q_str[4]
+ *   K            device bf16 [B][Lmax][Hkv][d], element strides k_str[4]
+ *   LSE          device float, element (b, qh, t) at b * lse_str[0] +
+ *                qh * lse_str[1] + t (a prefill's LSE from row S - Tq on)
+ *   seqlens      device int32 [B], each in [0, Lmax] (else reported by
+ *                ea_check_errors and counted as 0), or NULL: Lmax for all
+ *   block_mask   device uint8 [B][Hkv][nB][nB], nB = ceil(Lmax / 128), or NULL
+ *                if no head is EA_BLOCK
+ *   weights      device float [B][Hkv][Lmax] contiguous
+ * Constraints: d == 128, Hq % Hkv == 0, Hq / Hkv <= 64, 1 <= Tq,
+ * 1 <= Lmax <= 2^21, sink >= 0, window >= 1, scale > 0, block_size == 128;
+ * base pointers of Q and K 16-byte aligned, their strides multiples of 8
+ * elements, head-dim strides 1; the workspace 256-byte aligned.
+ */
+ea_status ea_key_weights(const void *Q, const void *K, const float *LSE, const int64_t q_str[4],
+                         const int64_t k_str[4], const int64_t lse_str[2], const int32_t *seqlens,
+                         int B, int Tq, int Lmax, int Hq, int Hkv, int d, float scale,
+                         const uint8_t *m, int sink, int window, const uint8_t *block_mask,
+                         int block_size, float *weights, int accumulate, void *workspace,
+                         size_t ws_bytes, void *stream);
 
 /*
  * ea_sparsity_ratios - model sparsity ratio and effective sparsity ratio of one

@@ -15,6 +15,7 @@ present, the device entry points raise instead of computing anything else.
     ea_hybrid_attn_decode_paged  the same decode over a paged KV cache
     ea_cache_write           new tokens into a KV cache of 8 bits (or bf16), quantised
     ea_hybrid_attn_decode_q8 the decode over an 8-bit cache, with the keys' attention weights
+    ea_key_weights           the attention weight that a prefill's queries give its keys
     ea_evict_select          which tokens stay when a cache is cut by those weights
     ea_cache_compact         gathers them into another cache
     ea_sparsity_ratios       Omega_MSR / Omega_ESR (host)
@@ -46,7 +47,8 @@ EXPORTS = ("ea_status_string", "ea_route", "ea_route_layers", "ea_prefill_worksp
            "ea_hybrid_attn_decode", "ea_hybrid_attn_decode_paged", "ea_xa_workspace_size",
            "ea_xa_estimate", "ea_cache_workspace_size", "ea_cache_write", "ea_evict_select",
            "ea_cache_compact", "ea_decode_q8_workspace_size", "ea_hybrid_attn_decode_q8",
-           "ea_sparsity_ratios", "ea_check_errors")
+           "ea_key_weights_workspace_size", "ea_key_weights", "ea_sparsity_ratios",
+           "ea_check_errors")
 
 
 class EAError(RuntimeError):
@@ -154,12 +156,16 @@ def lib():
         L.ea_decode_q8_workspace_size.restype = sz
         L.ea_hybrid_attn_decode_q8.argtypes = [P, P, P, P, P, P, P, i32, i32, f32, P, i32, i32, P,
                                                i32, i32, P, i32, P, sz, P]
+        L.ea_key_weights_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+        L.ea_key_weights_workspace_size.restype = sz
+        L.ea_key_weights.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, f32, P, i32,
+                                     i32, P, i32, P, i32, P, sz, P]
         L.ea_sparsity_ratios.argtypes = [P, P, i32, i32, i32, i32, i32, P, i32,
                                          ctypes.POINTER(f64), ctypes.POINTER(f64)]
         L.ea_check_errors.argtypes = [P, P]
         for f in ("ea_route", "ea_route_layers", "ea_hybrid_attn_prefill", "ea_prefill_plan", "ea_prefill_attend",
                   "ea_hybrid_attn_decode", "ea_cache_write", "ea_evict_select", "ea_cache_compact",
-                  "ea_hybrid_attn_decode_q8", "ea_sparsity_ratios", "ea_check_errors"):
+                  "ea_hybrid_attn_decode_q8", "ea_key_weights", "ea_sparsity_ratios", "ea_check_errors"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -860,6 +866,56 @@ def ea_hybrid_attn_decode_q8(q, cache, seqlens, m, *, sink, window, block_mask=N
             m.data_ptr(), int(sink), int(window), _ptr(bm), TILE, int(num_splits),
             _ptr(key_weights), 1 if accumulate else 0, workspace.data_ptr(), workspace.numel(), st))
     return O, LSE
+
+
+def ea_key_weights_workspace_size(B, Tq, Lmax, Hq, Hkv, d=128):
+    return int(lib().ea_key_weights_workspace_size(B, Tq, Lmax, Hq, Hkv, d))
+
+
+def key_weights_workspace(B, Tq, Lmax, Hq, Hkv, d=128, device="cuda"):
+    """A zeroed workspace of ea_key_weights."""
+    n = ea_key_weights_workspace_size(B, Tq, Lmax, Hq, Hkv, d)
+    if n == 0:
+        raise ValueError("unsupported key weight sizes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def ea_key_weights(Q, K, LSE, m, *, sink, window, seqlens=None, block_mask=None, scale=None,
+                   weights=None, accumulate=True, workspace=None, stream=None):
+    """The attention weight that the last Tq query rows of each sequence give its
+    keys.  Q [B, Tq, Hq, 128], K [B, Lmax, Hkv, 128] bf16; LSE float32 [B, Hq,
+    Tq] (the prefill's for those rows, a view of its last columns; unit stride
+    along the rows); m uint8 [B, Hkv]; seqlens int32 [B] (None: Lmax; query row
+    t sits at position seqlens[b] - Tq + t); block_mask uint8 [B, Hkv, nB, nB]
+    (nB = ceil(Lmax / 128)) when a head is BLOCK; all CUDA.  weights (float32
+    [B, Hkv, Lmax]) is added to (accumulate) or written for the keys below
+    seqlens[b]; zeros are allocated if it is not given.  Returns it."""
+    _dev(Q, "Q", torch.bfloat16)
+    _dev(K, "K", torch.bfloat16)
+    _dev(LSE, "LSE", torch.float32)
+    if Q.dim() != 4 or K.dim() != 4 or Q.shape[0] != K.shape[0] or Q.shape[3] != K.shape[3]:
+        raise ValueError("Q must be [B, Tq, Hq, d], K [B, Lmax, Hkv, d]")
+    B, Tq, Hq, d = Q.shape
+    Lmax, Hkv = K.shape[1], K.shape[2]
+    if tuple(LSE.shape) != (B, Hq, Tq) or (Tq > 1 and LSE.stride(2) != 1):
+        raise ValueError("LSE must be [%d, %d, %d] with unit stride along the rows" % (B, Hq, Tq))
+    _like(m, "m", (B, Hkv), torch.uint8)
+    _i32_vec(seqlens, "seqlens", B)
+    bm = _block_mask_arg(block_mask, B, Hkv, Lmax)
+    if weights is not None:
+        _like(weights, "weights", (B, Hkv, Lmax), torch.float32)
+    _one_device(Q, K, LSE, m, seqlens, bm, weights, workspace)
+    with _at(Q.device, stream) as st:
+        if weights is None:
+            weights = torch.zeros(B, Hkv, Lmax, dtype=torch.float32, device=Q.device)
+        if workspace is None:
+            workspace = key_weights_workspace(B, Tq, Lmax, Hq, Hkv, d, Q.device)
+        _check("ea_key_weights", lib().ea_key_weights(
+            Q.data_ptr(), K.data_ptr(), LSE.data_ptr(), _strides(Q), _strides(K), _strides(LSE),
+            _ptr(seqlens), B, Tq, Lmax, Hq, Hkv, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
+            m.data_ptr(), int(sink), int(window), _ptr(bm), TILE, weights.data_ptr(),
+            1 if accumulate else 0, workspace.data_ptr(), workspace.numel(), st))
+    return weights
 
 
 def ea_evict_select(weights, seqlens, *, keep, sink=0, recent=0, index=None, new_seqlens=None,

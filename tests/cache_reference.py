@@ -254,3 +254,35 @@ def decode_ref(q, K, V, vs, lens, modes, sink, window, scale, bm=None):
                 tL[b, i] = d.max() + 2.0 ** -20 * (1 + abs(LSE[b, i]))
                 tW[b, h, at] += p * rel + 1e-38
     return O, LSE, W, (tO, tL, tW)
+
+
+def key_weights_ref(Q, K, LSE, modes, sink, window, lens, scale, bm=None):
+    """float64 (weights [B, Hkv, Lmax], tolerance) of ea_key_weights, LSE the float32 rows it is given.
+
+    Tolerance: a logit is an fp32 sum of 128 products, off by at most 128 * 2^-23 of the sum of their magnitudes; it
+    and the LSE are rounded a few times at their size (2^-22); exp2 and the sums' own rounding (a few hundred terms
+    added one after the other, then the tiles') stay below 2^-13 of the result: n = 1024 additions of 2^-24 each."""
+    Q, K, LSE = Q.double().numpy(), K.double().numpy(), LSE.double().numpy()
+    B, Tq, Hq, _ = Q.shape
+    Lmax, Hkv = K.shape[1], K.shape[2]
+    g = Hq // Hkv
+    W, tol = np.zeros((B, Hkv, Lmax)), np.zeros((B, Hkv, Lmax))
+    for b, L in enumerate(lens):
+        t = np.arange(max(0, Tq - L), Tq)
+        i, j = (L - Tq + t)[:, None], np.arange(L)[None, :]
+        for h in range(Hkv):
+            keep = j <= i
+            if modes[b][h] == 1:
+                keep = keep & ((j < sink) | (i - j < window))
+            elif modes[b][h] == 2:
+                keep = keep & (bm[b, h][i // 128, j // 128] != 0)
+            for q in range(h * g, (h + 1) * g):
+                x = scale * (Q[b, t, q] @ K[b, :L, h].T)
+                lse = LSE[b, q, t][:, None]
+                d = 2.0 ** -16 * scale * (np.abs(Q[b, t, q]) @ np.abs(K[b, :L, h]).T) + 2.0 ** -21 * (
+                    np.abs(x) + np.where(np.isfinite(lse), np.abs(lse), 0))
+                keep_q = keep & np.isfinite(lse)
+                p = np.where(keep_q, np.exp(np.where(keep_q, x - np.where(np.isfinite(lse), lse, 0), 0)), 0)
+                W[b, h, :L] += p.sum(0)
+                tol[b, h, :L] += (p * np.expm1(d)).sum(0) + 2.0 ** -13 * p.sum(0) + 1e-37
+    return W, tol
