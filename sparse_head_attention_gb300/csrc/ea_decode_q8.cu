@@ -14,10 +14,10 @@
 //   - The producer warp keeps kStages tiles in flight by TMA (one 128-byte
 //     swizzled box of 64 rows per K or V), and the tile's scales by 4-byte
 //     asynchronous copies that arrive on the same barrier.
-//   - Each of the eight compute warps takes whole tiles in turn (tile n goes to
-//     warp n mod 8): no exchange between warps within a chunk of keys, the
-//     softmax's maximum is reduced once per 64 keys, and a warp has eight tile
-//     times for the latency of its own tile.
+//   - The compute warps take whole tiles in turn (tile n goes to warp n mod
+//     kQ8Warps): no exchange between warps within a chunk of keys, the softmax's
+//     maximum is reduced once per 64 keys, and a warp has several tile times for
+//     the latency of its own tile.
 //   - Products are m16n8k16 f16 MMAs with the keys (then the head dims) as the 16
 //     rows and the group's up to eight query heads as the 8 columns, so no row is
 //     padding: S^T = C^K Q^T and O^T += C^V^T W^T.  e4m3 and int8 codes are exact
@@ -46,7 +46,7 @@ namespace ea {
 
 constexpr int kQ8Stages = 12;
 constexpr int kQ8TileBytes = kDecKeys * EA_HEAD_DIM;   // K or V codes of one tile: 8 KB
-constexpr int kQ8Warps = 8;                            // compute warps
+constexpr int kQ8Warps = 6;                            // compute warps
 constexpr int kQ8Threads = (kQ8Warps + 1) * 32;        // + one producer warp
 constexpr int kQ8Groups = kDecKeys / 16;               // 16-key groups of a tile: one scale each at most
 constexpr float kQ8Shift = 14.f;                       // w <= 2^14
@@ -67,6 +67,11 @@ struct __align__(1024) Q8Smem {
 };
 constexpr size_t kQ8SmemBytes = sizeof(Q8Smem) + 1024;
 static_assert(kQ8SmemBytes <= 232448, "shared memory of one CTA");
+// Every use of a stage belongs to the same warp, which so waits for its uses in
+// order.  (A wait names a phase by its parity: were tile n - kQ8Stages another
+// warp's, a warp early at tile n could take the phase before it, still being
+// loaded, for its own.)
+static_assert(kQ8Stages % kQ8Warps == 0, "a stage belongs to one warp");
 
 struct Q8Args {
     DecodeArgs d;
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int slot = it & 1;
-            if (!mbar_wait(&sm.chunk_empty[slot], ((it >> 1) & 1) ^ 1, abort, &a.hdr->error))
+            if (!mbar_wait_warp(&sm.chunk_empty[slot], ((it >> 1) & 1) ^ 1, abort, &a.hdr->error))
                 break;
             int c = -1;
             if (lane == 0) {
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 }
                 const int page = a.block_table ? __shfl_sync(0xffffffffu, my_page, t & 31) : 0;
                 const int s = issued % kQ8Stages;
-                if (!mbar_wait(&sm.empty[s], ((issued / kQ8Stages) & 1) ^ 1, abort, &a.hdr->error)) {
+                if (!mbar_wait_warp(&sm.empty[s], ((issued / kQ8Stages) & 1) ^ 1, abort, &a.hdr->error)) {
                     ok = false;
                     break;
                 }
@@ -281,10 +286,10 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             }
         }
         // Before leaving on an abort, let the copies already issued land.
-        if (*abort) {
+        if (__any_sync(0xffffffffu, *abort)) {
             for (uint32_t k = issued > kQ8Stages ? issued - kQ8Stages : 0; k < issued; ++k) {
                 volatile int no_abort = 0;
-                mbar_wait(&sm.full[k % kQ8Stages], (k / kQ8Stages) & 1, &no_abort, nullptr);
+                mbar_wait_warp(&sm.full[k % kQ8Stages], (k / kQ8Stages) & 1, &no_abort, nullptr);
             }
         }
         return;
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     uint32_t base = 0;                          // tiles of the chunks before this one
     for (int it = 0;; ++it) {
         const int slot = it & 1;
-        bool ok = mbar_wait(&sm.chunk_full[slot], (it >> 1) & 1, abort, &a.hdr->error);
+        bool ok = mbar_wait_warp(&sm.chunk_full[slot], (it >> 1) & 1, abort, &a.hdr->error);
         const int c = ok ? sm.chunk[slot] : -1;
         __syncwarp();
         if (ok && lane == 0)
@@ -472,11 +477,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         };
 
         // this warp's tiles of the chunk
-        const int first = static_cast<int>((warp - base) & (kQ8Warps - 1));
+        const int first = static_cast<int>((warp + kQ8Warps - base % kQ8Warps) % kQ8Warps);
         for (int t = first; ok && t < ci.n_tiles; t += kQ8Warps) {
             const uint32_t n = base + t;
             const int s = n % kQ8Stages;
-            if (!mbar_wait(&sm.full[s], (n / kQ8Stages) & 1, abort, &a.hdr->error)) {
+            if (!mbar_wait_warp(&sm.full[s], (n / kQ8Stages) & 1, abort, &a.hdr->error)) {
                 ok = false;
                 break;
             }

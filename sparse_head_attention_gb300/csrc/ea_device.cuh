@@ -103,6 +103,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, volati
     }
 }
 
+// mbar_wait by a whole warp, with one result for all of its lanes: the branch on
+// it is uniform.  Where a failed wait leaves by another way than a good one,
+// lanes that saw the phase complete at different tries need not meet again
+// before the instructions behind the wait, and ldmatrix, mma, movmatrix and
+// tcgen05 loads are only defined for a converged warp.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                               uint32_t *err)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err));
+}
+
 __device__ __forceinline__ void fence_barrier_init()
 {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");

@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(256) kw_setup_kernel(const KwArgs a)
 __device__ __forceinline__ int kw_take(const KwArgs &a, KwSmem &sm, int it)
 {
     const int slot = it & 1;
-    if (!mbar_wait(&sm.item_full[slot], (it >> 1) & 1, &sm.abort, &a.hdr->error))
+    if (!mbar_wait_warp(&sm.item_full[slot], (it >> 1) & 1, &sm.abort, &a.hdr->error))
         return -2;
     const int item = sm.item[slot];
     __syncwarp();
@@ -199,7 +199,7 @@ __device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const CUten
     bool ok = true;
     for (int it = 0; ok; ++it) {
         const int slot = it & 1;
-        if (!mbar_wait(&sm.item_empty[slot], ((it >> 1) & 1) ^ 1, &sm.abort, err))
+        if (!mbar_wait_warp(&sm.item_empty[slot], ((it >> 1) & 1) ^ 1, &sm.abort, err))
             break;
         int item = -1;
         KwItem x;
@@ -219,7 +219,7 @@ __device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const CUten
         if (item < 0)
             break;
         const int ks = kn % kWKStages;
-        if (!mbar_wait(&sm.k_empty[ks], ((kn / kWKStages) & 1) ^ 1, &sm.abort, err))
+        if (!mbar_wait_warp(&sm.k_empty[ks], ((kn / kWKStages) & 1) ^ 1, &sm.abort, err))
             break;
         ++kn;
         if (lane == 0) {
@@ -230,7 +230,7 @@ __device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const CUten
         __syncwarp();
         ok = kw_tiles(a, x, lane, [&](const KwTile &t) {
             const int qs = qn % kWQStages;
-            if (!mbar_wait(&sm.q_empty[qs], ((qn / kWQStages) & 1) ^ 1, &sm.abort, err))
+            if (!mbar_wait_warp(&sm.q_empty[qs], ((qn / kWQStages) & 1) ^ 1, &sm.abort, err))
                 return false;
             ++qn;
             if (lane == 0) {
@@ -255,12 +255,12 @@ __device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const CUten
         });
     }
     // Before leaving on an abort, let the copies already issued land.
-    if (*static_cast<volatile int *>(&sm.abort)) {
+    if (__any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
         volatile int no_abort = 0;
         for (uint32_t k = kn > kWKStages ? kn - kWKStages : 0; k < kn; ++k)
-            mbar_wait(&sm.k_full[k % kWKStages], (k / kWKStages) & 1, &no_abort, nullptr);
+            mbar_wait_warp(&sm.k_full[k % kWKStages], (k / kWKStages) & 1, &no_abort, nullptr);
         for (uint32_t k = qn > kWQStages ? qn - kWQStages : 0; k < qn; ++k)
-            mbar_wait(&sm.q_full[k % kWQStages], (k / kWQStages) & 1, &no_abort, nullptr);
+            mbar_wait_warp(&sm.q_full[k % kWQStages], (k / kWQStages) & 1, &no_abort, nullptr);
     }
 }
 
@@ -275,14 +275,14 @@ __device__ __forceinline__ void kw_mma(const KwArgs &a, KwSmem &sm, uint32_t tme
         KwItem x;
         kw_item(a, item, x);
         const int ks = kn % kWKStages;
-        if (!mbar_wait(&sm.k_full[ks], (kn / kWKStages) & 1, &sm.abort, err))
+        if (!mbar_wait_warp(&sm.k_full[ks], (kn / kWKStages) & 1, &sm.abort, err))
             break;
         ++kn;
         const uint32_t kaddr = smem_u32(sm.k[ks]);
         const bool ok = kw_tiles(a, x, lane, [&](const KwTile &t) {
             const int buf = n % kWGroups, qs = n % kWQStages;
-            if (!mbar_wait(&sm.s_free[buf], ((n / kWGroups) & 1) ^ 1, &sm.abort, err) ||
-                !mbar_wait(&sm.q_full[qs], (n / kWQStages) & 1, &sm.abort, err))
+            if (!mbar_wait_warp(&sm.s_free[buf], ((n / kWGroups) & 1) ^ 1, &sm.abort, err) ||
+                !mbar_wait_warp(&sm.q_full[qs], (n / kWQStages) & 1, &sm.abort, err))
                 return false;
             ++n;
             tc_fence_after();
@@ -309,9 +309,9 @@ __device__ __forceinline__ void kw_mma(const KwArgs &a, KwSmem &sm, uint32_t tme
     }
     // Before leaving on an abort, let the MMAs already issued finish (their
     // operands and accumulators go with the CTA).
-    if (*static_cast<volatile int *>(&sm.abort) && n > 0) {
+    if (__any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort)) && n > 0) {
         volatile int no_abort = 0;
-        mbar_wait(&sm.s_full[(n - 1) % kWGroups], ((n - 1) / kWGroups) & 1, &no_abort, nullptr);
+        mbar_wait_warp(&sm.s_full[(n - 1) % kWGroups], ((n - 1) / kWGroups) & 1, &no_abort, nullptr);
     }
 }
 
@@ -337,7 +337,7 @@ __device__ __forceinline__ void kw_lse(const KwArgs &a, KwSmem &sm, int lane)
                 const int c = i * 32 + lane, hh = c / t.nr, r = c - hh * t.nr;
                 v[i] = hh < t.nh && r < t.cnt ? __ldg(row + hh * a.lse_sh + r) : 0.f;
             }
-            if (!mbar_wait(&sm.s_free[buf], ((n / kWGroups) & 1) ^ 1, &sm.abort, err))
+            if (!mbar_wait_warp(&sm.s_free[buf], ((n / kWGroups) & 1) ^ 1, &sm.abort, err))
                 return false;
             ++n;
 #pragma unroll
@@ -401,8 +401,8 @@ __device__ __forceinline__ void kw_sum(const KwArgs &a, KwSmem &sm, uint32_t tme
             if (static_cast<int>(mine % kWGroups) != wg)
                 return true;
             const uint32_t phase = (mine / kWGroups) & 1;
-            if (!mbar_wait(&sm.lse_full[wg], phase, &sm.abort, err) ||
-                !mbar_wait(&sm.s_full[wg], phase, &sm.abort, err))
+            if (!mbar_wait_warp(&sm.lse_full[wg], phase, &sm.abort, err) ||
+                !mbar_wait_warp(&sm.s_full[wg], phase, &sm.abort, err))
                 return false;
             tc_fence_after();
             const int cols = t.nh * t.nr;
