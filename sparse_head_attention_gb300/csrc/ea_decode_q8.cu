@@ -12,8 +12,11 @@
 // measured 6.79 TB/s an SM receives 45 bytes a ns, one 64-key tile of K and V
 // (16 KB) every 0.37 us.
 //   - The producer warp keeps kStages tiles in flight by TMA (one 128-byte
-//     swizzled box of 64 rows per K or V), and the tile's scales by 4-byte
-//     asynchronous copies that arrive on the same barrier.
+//     swizzled box of 64 rows per K or V); its own time per tile counts (700 cycles
+//     at that rate), so its lanes work out 32 tiles' places at once, and the
+//     compute warps load the scales themselves, a tile ahead.  (Scales as 4-byte
+//     asynchronous copies on the tile's barrier: 434 us for 16 sequences of
+//     64K; written beside the tile by the producer: 385.)
 //   - The compute warps take whole tiles in turn (tile n goes to warp n mod
 //     kQ8Warps): no exchange between warps within a chunk of keys, the softmax's
 //     maximum is reduced once per 64 keys, and a warp has several tile times for
@@ -57,7 +60,6 @@ struct __align__(1024) Q8Smem {
     float red_o[kQ8Warps][8][EA_HEAD_DIM];
     float red_m[kQ8Warps][8];
     float red_l[kQ8Warps][8];
-    float scale[kQ8Stages][2 * kQ8Groups];             // K's, then V's, of each 16-key group
     uint64_t full[kQ8Stages];
     uint64_t empty[kQ8Stages];
     uint64_t chunk_full[2], chunk_empty[2];
@@ -149,16 +151,6 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
-// 4-byte asynchronous copy of a scale (0 where the block holds no token), and
-// its arrival on `bar` once this thread's copies have landed.
-__device__ __forceinline__ void cp_async_scale(float *dst, const float *src, bool valid, uint64_t *bar)
-{
-    const int n = valid ? 4 : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(n)
-                 : "memory");
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // Barrier of the compute warps that also tells whether any of them failed.
 __device__ __forceinline__ bool compute_sync_or(bool failed)
 {
@@ -195,7 +187,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
     if (tid == 0) {
         sm.abort = 0;
         for (int s = 0; s < kQ8Stages; ++s) {
-            mbar_init(&sm.full[s], 1 + 2 * kQ8Groups);
+            mbar_init(&sm.full[s], 1);
             mbar_init(&sm.empty[s], 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -217,7 +209,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
 
     if (warp == kQ8Warps) {
         // ------------------------------------------------------------ producer
-        uint32_t issued = 0;
+        uint32_t issued = 0, phase = 0;
+        int st = 0;                             // issued % kQ8Stages, and its phase
         bool ok = true;
         for (int it = 0; ok; ++it) {
             const int slot = it & 1;
@@ -235,54 +228,55 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             if (c < 0)
                 break;
             const ChunkInfo ci = chunk_info(a, c, sm.plan);
-            int my_page = 0;
-            for (int t = 0; t < ci.n_tiles; ++t) {
-                // lane j looks up the page of tile 32 k + j, a group of 32 ahead
-                if (a.block_table && (t & 31) == 0) {
-                    my_page = 0;
-                    if (t + lane < ci.n_tiles) {
-                        int k0, nv;
-                        tile_rows(a, ci, t + lane, k0, nv);
-                        if (in_bounds(k0 / a.page_size, a.Lmax / a.page_size, &a.hdr->error))
-                            my_page = a.block_table[ci.b * a.bt_stride + k0 / a.page_size];
+            // Lane j holds the place of tile 32 k + j (row, and sequence or page),
+            // looked up a group of 32 tiles ahead of the copies that need it.
+            int row_of = 0, outer_of = 0, row_next = 0, outer_next = 0;
+            auto place = [&](int t, int &row, int &outer) {
+                row = 0;
+                outer = ci.b;
+                if (t >= ci.n_tiles)
+                    return;
+                int key0, nv;
+                tile_rows(a, ci, t, key0, nv);
+                row = key0;
+                if (a.block_table) {
+                    const int at = key0 / a.page_size;
+                    row = key0 - at * a.page_size;
+                    outer = in_bounds(at, a.Lmax / a.page_size, &a.hdr->error)
+                                ? a.block_table[ci.b * a.bt_stride + at]
+                                : -1;
+                    // a page outside the cache is reported; its copy reads the
+                    // fill value (a box outside the tensor is zero-filled)
+                    if (outer < 0 || outer >= a.num_pages) {
+                        raise_error(&a.hdr->error, EA_DEVERR_CHECK);
+                        outer = -1;
                     }
                 }
-                const int page = a.block_table ? __shfl_sync(0xffffffffu, my_page, t & 31) : 0;
-                const int s = issued % kQ8Stages;
-                if (!mbar_wait_warp(&sm.empty[s], ((issued / kQ8Stages) & 1) ^ 1, abort, &a.hdr->error)) {
+            };
+            place(lane, row_next, outer_next);
+            for (int t = 0; t < ci.n_tiles; ++t) {
+                if ((t & 31) == 0) {
+                    row_of = row_next;
+                    outer_of = outer_next;
+                    place(t + 32 + lane, row_next, outer_next);
+                }
+                const int row = __shfl_sync(0xffffffffu, row_of, t & 31);
+                const int outer = __shfl_sync(0xffffffffu, outer_of, t & 31);
+                if (!mbar_wait_warp(&sm.empty[st], phase ^ 1, abort, &a.hdr->error)) {
                     ok = false;
                     break;
                 }
-                int key0, nv;
-                tile_rows(a, ci, t, key0, nv);
-                int row = key0, outer = ci.b;
-                bool there = true;
-                if (a.block_table) {
-                    row = key0 % a.page_size;
-                    outer = page;
-                    there = page >= 0 && page < a.num_pages;
-                }
-                if (lane < 2 * kQ8Groups) {
-                    // scales of the tile's 16-key groups that begin below the
-                    // sequence's end (the others' blocks may not exist)
-                    const int grp = lane % kQ8Groups;
-                    const bool live = there && key0 + 16 * grp < ci.ks.L;
-                    const float *base = lane < kQ8Groups ? qa.ks : qa.vs;
-                    const int64_t at = (static_cast<int64_t>(live ? outer : 0) * a.Hkv + ci.h) * qa.nsb +
-                                       (live ? (row + 16 * grp) >> qa.log2sb : 0);
-                    cp_async_scale(&sm.scale[s][lane], base + at, live, &sm.full[s]);
-                }
                 if (lane == 0) {
-                    // a page outside the cache is reported; its copy reads the
-                    // fill value (a box outside the tensor is zero-filled)
-                    if (!there)
-                        raise_error(&a.hdr->error, EA_DEVERR_CHECK);
-                    mbar_arrive_expect_tx(&sm.full[s], 2 * kQ8TileBytes);
-                    tma_load_4d(sm.k[s], &tm_k, 0, ci.h, row, outer, &sm.full[s]);
-                    tma_load_4d(sm.v[s], &tm_v, 0, ci.h, row, outer, &sm.full[s]);
+                    mbar_arrive_expect_tx(&sm.full[st], 2 * kQ8TileBytes);
+                    tma_load_4d(sm.k[st], &tm_k, 0, ci.h, row, outer, &sm.full[st]);
+                    tma_load_4d(sm.v[st], &tm_v, 0, ci.h, row, outer, &sm.full[st]);
                 }
                 __syncwarp();
                 ++issued;
+                if (++st == kQ8Stages) {
+                    st = 0;
+                    phase ^= 1;
+                }
             }
         }
         // Before leaving on an abort, let the copies already issued land.
@@ -354,7 +348,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         if constexpr (WEIGHTS)
             score = qa.scores + (static_cast<int64_t>(ci.b) * a.Hkv + ci.h) * a.Lmax * qa.gp + 2 * qd;
 
-        auto tile = [&](auto masked_tag, int s, int key0) {
+        // sc: lane i < 8 holds K's (then V's) scale of group i % 4
+        auto tile = [&](auto masked_tag, int s, int key0, float sc) {
             constexpr bool kMasked = decltype(masked_tag)::value;
             const uint32_t kb = smem_u32(sm.k[s]), vb = smem_u32(sm.v[s]);
             const int lrow = ((lane >> 3) & 1) * 8 + (lane & 7), lcol = lane >> 4;
@@ -383,7 +378,8 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                     codes_f16<E4M3, false>(w[3], f[1], f[3]);
                     mma_f16(acc, f, qb[j + 1][0], qb[j + 1][1]);
                 }
-                const float ks = sm.scale[s][i], lv = lg2(sm.scale[s][kQ8Groups + i]);
+                const float ks = __shfl_sync(0xffffffffu, sc, i);
+                const float lv = lg2(__shfl_sync(0xffffffffu, sc, kQ8Groups + i));
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     x[i][e] = __fmul_rn(acc[e], cs[e & 1] * ks);   // not fused with lv: as it is stored
@@ -438,7 +434,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                                  (m_run[1] == NEG_INF ? 0.f : m_run[1]) - kQ8Shift};
 #pragma unroll
             for (int i = 0; i < kQ8Groups; ++i) {
-                const float iv = 1.f / sm.scale[s][kQ8Groups + i];
+                const float iv = __frcp_rn(__shfl_sync(0xffffffffu, sc, kQ8Groups + i));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     x[i][e] = ex2(x[i][e] - mb[e & 1]);
@@ -476,9 +472,35 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             }
         };
 
+        // Lanes 0 - 3: K's scales of a tile's 16-key groups, 4 - 7: V's; 1 for groups
+        // that begin behind the sequence's end (their blocks may hold nothing)
+        // and for pages outside the cache (their codes read as zeros).
+        auto load_scale = [&](int t) -> float {
+            if (lane >= 2 * kQ8Groups || t >= ci.n_tiles)
+                return 1.f;
+            int key0, nv;
+            tile_rows(a, ci, t, key0, nv);
+            int row = key0 + 16 * (lane % kQ8Groups), outer = ci.b;
+            if (row >= ci.ks.L)
+                return 1.f;
+            if (a.block_table) {
+                const int at = key0 / a.page_size;
+                row -= at * a.page_size;
+                outer = in_bounds(at, a.Lmax / a.page_size, &a.hdr->error)
+                            ? a.block_table[ci.b * a.bt_stride + at]
+                            : -1;
+                if (outer < 0 || outer >= a.num_pages)
+                    return 1.f;
+            }
+            const float *p = lane < kQ8Groups ? qa.ks : qa.vs;
+            return __ldg(p + (static_cast<int64_t>(outer) * a.Hkv + ci.h) * qa.nsb + (row >> qa.log2sb));
+        };
         // this warp's tiles of the chunk
         const int first = static_cast<int>((warp + kQ8Warps - base % kQ8Warps) % kQ8Warps);
+        float sc_next = load_scale(first);
         for (int t = first; ok && t < ci.n_tiles; t += kQ8Warps) {
+            const float sc = sc_next;
+            sc_next = load_scale(t + kQ8Warps);
             const uint32_t n = base + t;
             const int s = n % kQ8Stages;
             if (!mbar_wait_warp(&sm.full[s], (n / kQ8Stages) & 1, abort, &a.hdr->error)) {
@@ -491,9 +513,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             const bool whole = ci.list ? last <= ci.ks.L
                                        : last <= ci.ks.n0 || (key0 >= ci.ks.w0 && last <= ci.ks.L);
             if (whole)
-                tile(std::false_type{}, s, key0);
+                tile(std::false_type{}, s, key0, sc);
             else
-                tile(std::true_type{}, s, key0);
+                tile(std::true_type{}, s, key0, sc);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sm.empty[s]);
