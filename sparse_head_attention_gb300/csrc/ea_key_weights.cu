@@ -6,22 +6,36 @@
 // one pass over the products and no softmax statistics are needed.
 //
 // The products are S^T = K Q^T: keys are the 128 rows of a tcgen05 MMA tile (the
-// TMEM lanes) and query rows its columns, so that a thread owns one key and the
-// sum over queries is a sum over the columns it reads: no reduction across
-// threads, no atomics, one order of summation.  An item is one 128-key tile of a
-// (sequence, KV head), or one of `parts` shares of its queries; its key tile is
-// loaded once, and the queries' tiles stream past it:
-//   warp 0     TMA: K tiles (2 stages of 32 KB) and query tiles (4 of 32 KB)
-//   warp 1     the MMAs, into one of four 128-column TMEM buffers
-//   warp 2     the rows' LSE, in log2 units, into shared memory
-//   warps 4-19 four warpgroups; the one whose buffer is ready reads its columns
-//              and adds 2^(s * scale * log2 e - lse)
-// A query tile has up to 128 columns.  Where fewer than 65 rows see the key tile
-// (a decode step, an observation window) it holds several heads' rows side by
-// side, each padded to a multiple of 16, so that one token's step costs one
-// 16-column MMA per head and is bound by reading K.  Long rows cost per
-// 128 x 128 tile 128^3 multiply-adds (512 cycles of the tensor core) and 16384
-// exponentials.
+// TMEM lanes) and query rows its up to 256 columns, so that a thread owns one
+// key and the sum over queries is a sum over the columns it reads: no reduction
+// across threads, no atomics, one order of summation.  Roles:
+//   warp 0     TMA: key tiles and query tiles
+//   warp 1     the MMAs, into two 256-column TMEM buffers (few rows: and warp 3)
+//   warp 2     the rows' LSE as a ninth k-step of the product: -LSE / scale in three
+//              bf16 parts (24 bits) in a query's row, against ones in a key's
+//   warps 4-19 four warpgroups, two to a buffer: each reads half of its columns
+//              and adds 2^(s * scale * log2 e)
+// (A summing thread needs every column's LSE.  Read from shared memory beside
+// the products, 16 bytes a lane, that took as many of its cycles as the MMAs'
+// operands do and paced the kernel: 1200 us for 16K x 16K and 32 heads, 637 with
+// nothing summed.)
+// A query tile holds 128 rows of two heads (256 rows of one where the group is
+// one head), or fewer rows of more heads, each padded to a multiple of 16.
+//
+// Many rows (more than one query tile per key tile): an item is 256 keys, whose
+// two key tiles stay in shared memory, one per TMEM buffer, while query tiles
+// stream past both in halves of 64 dims (4 stages of 32 KB).  Two key tiles, so
+// that a query tile's 64 KB from L2 feed 2048 cycles of MMAs; with one, the MMAs
+// waited for them (2 stages of 64 KB: 1073 us for 16K x 16K and 32 heads).  256
+// columns, because with 128 the operands' reads from shared memory pace the
+// MMA (48 % of its cycles busy for 31 % of its rate).  Bound by the tensor core
+// (2^22 multiply-adds, 1024 cycles, per 128 x 256 tile) and as much by the SFUs
+// (32768 exponentials at 32 a cycle).
+//
+// Few rows (a decode step, an observation window): one query tile serves all key
+// tiles of an item and stays in shared memory; key tiles pass through 4 stages of
+// 32 KB (2 were too few for HBM's latency: 3750 cycles a tile) and the two buffers
+// in turn.  Bound by reading K.
 //
 // With few key tiles the queries of each are cut into `parts` shares, whose sums
 // go to the workspace and are added in order by a last kernel.
@@ -33,28 +47,45 @@
 
 namespace ea {
 
-constexpr int kWTile = 128;                       // keys per tile, query columns per tile
-constexpr int kWHalf = kWTile * 128;              // 64 dims of 128 rows: 16 KB
-constexpr int kWKStages = 2;
-constexpr int kWQStages = 4;
-constexpr int kWGroups = 4;                       // warpgroups, TMEM buffers, LSE buffers
+constexpr int kWTile = 128;                       // keys per tile
+constexpr int kWCols = 256;                       // query columns per tile
+constexpr int kWKHalf = kWTile * 128;             // 64 dims of 128 keys: 16 KB
+constexpr int kWQHalf = kWCols * 128;             // 64 dims of 256 rows: 32 KB
+static_assert(2 * kWKHalf == kWQHalf, "a key tile is as large as half a query tile");
+constexpr int kWStages = 4;                       // many rows: halves of query tiles (32 KB);
+                                                  // few rows: key tiles (32 KB)
+constexpr int kWXBytes = 32;                      // 16 bf16 of one row of the LSE k-step
+constexpr int kWBufs = 2;                         // TMEM and LSE buffers
+constexpr int kWGroups = 4;                       // warpgroups, two to a buffer
 constexpr int kWFirstWarp = 4;
 constexpr int kWThreads = (kWFirstWarp + 4 * kWGroups) * 32;
-constexpr int kWSumThreads = 4 * kWGroups * 32;
-constexpr uint32_t kWTmemCols = kWGroups * kWTile;
+constexpr int kWSlots = 4;                        // items handed on, and key tiles being joined
+constexpr uint32_t kWTmemCols = kWBufs * kWCols;
 constexpr int kWMaxParts = 64;
 
+// An item: key tiles (many rows: pairs of them) [kt0, kt1) of one (sequence, KV
+// head) and one share of their queries.
+struct KwItem {
+    int valid;             // 0: none left
+    int b, h, part, kt0, kt1;
+    int L, off;            // query row t sits at position off + t
+    int mode;
+};
+
 struct __align__(1024) KwSmem {
-    uint8_t k[kWKStages][2 * kWHalf];
-    uint8_t q[kWQStages][2 * kWHalf];
-    float lse[kWGroups][kWTile];
-    float red[2][kWGroups][kWTile];
-    uint64_t k_full[kWKStages], k_empty[kWKStages];
-    uint64_t q_full[kWQStages], q_empty[kWQStages];
-    uint64_t s_full[kWGroups], s_free[kWGroups];
-    uint64_t lse_full[kWGroups];
-    uint64_t item_full[2], item_empty[2];
-    int item[2];
+    uint8_t held[2 * kWQHalf];                    // many rows: two key tiles; few rows: a query tile
+    uint8_t ring[kWStages][kWQHalf];
+    uint8_t qx[kWBufs][kWXBytes * kWCols];        // the LSE k-step: query rows
+    uint8_t kx[kWXBytes * kWTile];                // and key rows (ones)
+    float red[kWSlots][kWGroups][kWTile];
+    uint64_t k_full[kWStages], k_empty[kWStages];
+    uint64_t q_full[kWStages], q_empty[kWStages];
+    uint64_t s_full[kWBufs], s_free[kWBufs];
+    uint64_t lse_full[kWBufs], lse_empty[kWBufs];
+    uint64_t red_full[kWSlots], red_empty[kWSlots];
+    uint64_t item_full[kWSlots], item_empty[kWSlots];
+    uint64_t drain[2];
+    KwItem item[kWSlots];
     uint32_t tmem_base;
     int abort;
 };
@@ -68,89 +99,120 @@ struct KwArgs {
     const uint8_t *m, *block_mask;
     float *weights, *partial;
     ea_ws_header *hdr;
-    int B, Tq, Lmax, Hkv, g, nB, sink, window, parts, accumulate;
+    int B, Tq, Lmax, Hkv, g, nB, sink, window, parts, run, accumulate;
+    int seg, seg_log2;     // query rows of one head in a tile: 128, or 256 for groups of one head
+    int box;               // rows of a query box: 128, or all of Tq (rounded up to 16)
     int n_items;
     float c2;              // scale * log2(e)
+    float inv_scale;
 };
 
-struct KwItem {
-    int b, h, kt, part;
-    int L, off;            // query row t sits at position off + t
-    int mode;
-    int ta, te;            // query rows that see the tile (not EA_BLOCK)
-    int s0, s1;            // this share's segments: 128 rows from ta on, or (EA_BLOCK) query blocks
-};
+// Keys that share the query tiles.
+template <bool MANY>
+__host__ __device__ constexpr int kw_keys()
+{
+    return MANY ? 2 * kWTile : kWTile;
+}
 
-// Items: key tile outermost (the first ones are seen by the most queries), then
-// share, sequence, head.  False: the sequence has no such tile.
+// Items: runs of key tiles outermost (the first ones are seen by the most
+// queries), then share, sequence, head.  False: the sequence has no such tile.
+template <bool MANY>
 __device__ __forceinline__ bool kw_item(const KwArgs &a, int item, KwItem &x)
 {
     const int units = a.B * a.Hkv;
     const int u = item % units, kp = item / units;
     x.part = kp % a.parts;
-    x.kt = kp / a.parts;
+    x.kt0 = kp / a.parts * a.run;
     x.b = u / a.Hkv;
     x.h = u % a.Hkv;
     x.L = a.seqlens ? a.seqlens[x.b] : a.Lmax;
     if (x.L < 0 || x.L > a.Lmax)
         x.L = 0;
-    const int k0 = x.kt * kWTile;
-    if (k0 >= x.L)
-        return false;
+    x.kt1 = min(x.kt0 + a.run, (x.L + kw_keys<MANY>() - 1) / kw_keys<MANY>());
     x.off = x.L - a.Tq;
     x.mode = a.m[u];
-    x.ta = max(0, k0 - x.off);
-    x.te = a.Tq;
-    int n;
+    x.valid = 1;
+    return x.kt0 < x.kt1;
+}
+
+// The queries of one key tile that an item takes.
+struct KwRange {
+    int ta, te;            // query rows that see the tile (not EA_BLOCK: te)
+    int s0, s1;            // this share's segments: a.seg rows from ta on, or (EA_BLOCK) query blocks
+};
+
+template <bool MANY>
+__device__ __forceinline__ KwRange kw_range(const KwArgs &a, const KwItem &x, int kt)
+{
+    KwRange r;
+    const int k0 = kt * kw_keys<MANY>();
+    r.ta = max(0, k0 - x.off);
+    r.te = a.Tq;
+    int n, first = 0;
     if (x.mode == EA_BLOCK) {
-        const int b0 = (x.off + x.ta) / kWTile;              // ta >= -off
-        n = a.block_mask ? (x.L - 1) / kWTile + 1 - b0 : 0;
-        x.s0 = b0 + static_cast<int>(static_cast<int64_t>(x.part) * n / a.parts);
-        x.s1 = b0 + static_cast<int>(static_cast<int64_t>(x.part + 1) * n / a.parts);
-        return true;
+        first = (x.off + r.ta) / kWTile;                     // ta >= -off
+        n = a.block_mask ? (x.L - 1) / kWTile + 1 - first : 0;
+    } else {
+        if (x.mode == EA_SSA && k0 >= a.sink)                // the last key's window ends the rows
+            r.te = min(a.Tq, k0 + kw_keys<MANY>() - 1 + a.window - x.off);
+        n = x.mode > EA_BLOCK || r.te <= r.ta ? 0 : (r.te - r.ta + a.seg - 1) >> a.seg_log2;
     }
-    if (x.mode == EA_SSA && k0 >= a.sink)                    // the last key's window ends the rows
-        x.te = static_cast<int>(min(static_cast<int64_t>(a.Tq),
-                                    static_cast<int64_t>(k0) + kWTile - 1 + a.window - x.off));
-    n = x.mode > EA_BLOCK ? 0 : max(0, (x.te - x.ta + kWTile - 1) / kWTile);
-    x.s0 = static_cast<int>(static_cast<int64_t>(x.part) * n / a.parts);
-    x.s1 = static_cast<int>(static_cast<int64_t>(x.part + 1) * n / a.parts);
-    return true;
+    r.s0 = first;
+    r.s1 = first + n;
+    if (a.parts > 1) {                                       // n <= 2^14, parts <= 64
+        r.s0 = first + x.part * n / a.parts;
+        r.s1 = first + (x.part + 1) * n / a.parts;
+    }
+    return r;
 }
 
 // A column tile: rows [t0, t0 + cnt) of heads [head0, head0 + nh) of the group,
 // nr columns (cnt rounded up to 16) a head.
 struct KwTile {
     int t0, cnt, nr, head0, nh;
+    uint32_t keep;         // bit p: the rows' block keeps key tile p of a pair (EA_BLOCK)
 };
 
-// Calls f(tile) for every column tile of an item, in order, until f returns
-// false; a whole warp calls it.
-template <class F>
-__device__ __forceinline__ bool kw_tiles(const KwArgs &a, const KwItem &x, int lane, F f)
+// Heads of nr columns (16 .. 256, in sixteens) that fit a tile: 256 / nr, without
+// a division (the roles' integer code runs at one warp's pace, between MMAs).
+__device__ __forceinline__ int kw_heads(int nr)
 {
-    for (int s = x.s0; s < x.s1; s += 32) {
-        uint32_t bits = x.s1 - s >= 32 ? 0xffffffffu : (1u << (x.s1 - s)) - 1u;
+    return static_cast<int>((0x1112347Full >> (nr / 4 - 4)) & 15u) + 1;
+}
+
+// Calls f(tile) for every column tile of a key tile, in order, until f returns
+// false; a whole warp calls it.
+template <bool MANY, class F>
+__device__ __forceinline__ bool kw_tiles(const KwArgs &a, const KwItem &x, const KwRange &rg, int kt,
+                                         int lane, F f)
+{
+    for (int s = rg.s0; s < rg.s1; s += 32) {
+        uint32_t bits = rg.s1 - s >= 32 ? 0xffffffffu : (1u << (rg.s1 - s)) - 1u;
+        uint32_t bits0 = bits, bits1 = bits;
         if (x.mode == EA_BLOCK) {
-            const int qb = s + lane;
-            const int64_t at = ((static_cast<int64_t>(x.b) * a.Hkv + x.h) * a.nB + qb) * a.nB + x.kt;
-            bits = __ballot_sync(0xffffffffu, qb < x.s1 && a.block_mask[at] != 0);
+            const int qb = s + lane, kb = MANY ? 2 * kt : kt;
+            const uint8_t *row = a.block_mask +
+                                 ((static_cast<int64_t>(x.b) * a.Hkv + x.h) * a.nB + qb) * a.nB + kb;
+            bits0 = __ballot_sync(0xffffffffu, qb < rg.s1 && row[0] != 0);
+            bits1 = MANY ? __ballot_sync(0xffffffffu, qb < rg.s1 && kb + 1 < a.nB && row[1] != 0) : 0u;
+            bits = bits0 | bits1;
         }
         while (bits) {
-            const int i = s + __ffs(bits) - 1;
+            const int bit = __ffs(bits) - 1, i = s + bit;
             bits &= bits - 1;
             KwTile t;
+            t.keep = ((bits0 >> bit) & 1u) | ((bits1 >> bit) & 1u) << 1;
             int end;
             if (x.mode == EA_BLOCK) {
-                t.t0 = max(i * kWTile - x.off, x.ta);
+                t.t0 = max(i * kWTile - x.off, rg.ta);
                 end = min((i + 1) * kWTile - x.off, a.Tq);
             } else {
-                t.t0 = x.ta + i * kWTile;
-                end = min(t.t0 + kWTile, x.te);
+                t.t0 = rg.ta + i * a.seg;
+                end = min(t.t0 + a.seg, rg.te);
             }
             t.cnt = end - t.t0;
             t.nr = (t.cnt + 15) & ~15;
-            const int hp = kWTile / t.nr;
+            const int hp = kw_heads(t.nr);
             for (t.head0 = 0; t.head0 < a.g; t.head0 += hp) {
                 t.nh = min(hp, a.g - t.head0);
                 if (!f(t))
@@ -160,6 +222,23 @@ __device__ __forceinline__ bool kw_tiles(const KwArgs &a, const KwItem &x, int l
     }
     return true;
 }
+
+// A query tile held in shared memory, followed alike by the producer and the MMA
+// warp (its LSE by its warp): a tile equal to the one before it is not loaded again.
+struct KwHeld {
+    int b, h, t0, cnt, head0;
+    uint32_t n;            // query tiles loaded
+    __device__ __forceinline__ bool same(const KwItem &x, const KwTile &t)
+    {
+        const bool eq = n > 0 && b == x.b && h == x.h && t0 == t.t0 && cnt == t.cnt && head0 == t.head0;
+        b = x.b;
+        h = x.h;
+        t0 = t.t0;
+        cnt = t.cnt;
+        head0 = t.head0;
+        return eq;
+    }
+};
 
 // ------------------------------------------------------------ setup
 // Re-arms the queue and reports modes, masks and lengths that cannot be used.
@@ -178,177 +257,332 @@ __global__ void __launch_bounds__(256) kw_setup_kernel(const KwArgs a)
 }
 
 // ------------------------------------------------------------ roles
-// Next item of the queue, handed on in slot it % 2; -1: none left, -2: gave up.
-__device__ __forceinline__ int kw_take(const KwArgs &a, KwSmem &sm, int it)
+// Next item of the queue (slot it % kWSlots); 0: none left, -1: gave up.
+__device__ __forceinline__ int kw_take(const KwArgs &a, KwSmem &sm, int it, KwItem &x)
 {
-    const int slot = it & 1;
-    if (!mbar_wait_warp(&sm.item_full[slot], (it >> 1) & 1, &sm.abort, &a.hdr->error))
-        return -2;
-    const int item = sm.item[slot];
+    const int slot = it % kWSlots;
+    if (!mbar_wait_warp(&sm.item_full[slot], (it / kWSlots) & 1, &sm.abort, &a.hdr->error))
+        return -1;
+    x = sm.item[slot];
     __syncwarp();
     if ((threadIdx.x & 31) == 0)
         mbar_arrive(&sm.item_empty[slot]);
-    return item;
+    return x.valid;
 }
 
-__device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const CUtensorMap *tm_q,
-                                            const CUtensorMap *tm_q16, const KwArgs &a, KwSmem &sm, int lane)
+// The query tiles' tensor maps: boxes of 64 dims x `rows` rows, and of 16 rows for
+// tiles that are not whole boxes.  (A copy takes its issuing thread about 240
+// cycles: 32 boxes of 16 rows for one tile cost more than the tile's MMAs.)
+struct KwMaps {
+    CUtensorMap rows, r16;
+};
+
+// Dims 64 half .. + 63 of a query tile's rows, into dst.
+__device__ __forceinline__ void kw_load_q(const KwMaps &tm, const KwArgs &a, uint8_t *dst, int head, int b,
+                                          const KwTile &t, int half, uint64_t *bar)
+{
+    const bool whole = t.nr == a.box || (t.nr == kWCols && a.box == kWTile);
+    const int box = whole ? a.box : 16;
+    const CUtensorMap *map = whole ? &tm.rows : &tm.r16;
+    int row = 0;
+    for (int hh = 0; hh < t.nh; ++hh)
+        for (int r = 0; r < t.nr; r += box, row += box)
+            tma_load_4d(dst + row * 128, map, 64 * half, head + hh, t.t0 + r, b, bar);
+}
+
+// A ring position: stage and phase.
+template <int N>
+struct KwRing {
+    int s = 0;
+    uint32_t phase = 0;
+    uint32_t n = 0;        // steps taken
+    __device__ __forceinline__ void next()
+    {
+        ++n;
+        if (++s == N) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+template <bool MANY>
+__device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const KwMaps &tm_q, const KwArgs &a, KwSmem &sm, int lane)
 {
     uint32_t *err = &a.hdr->error;
-    uint32_t kn = 0, qn = 0;
+    constexpr int KS = MANY ? 1 : kWStages, QS = MANY ? kWStages : 1;
+    KwRing<KS> k;
+    KwRing<QS> q;
+    KwHeld held{};
     bool ok = true;
+    auto draw = [&]() { return lane == 0 ? atomicAdd(&a.hdr->work_counter, 1u) : 0u; };
+    uint32_t next = draw();                                  // drawn an item ahead
     for (int it = 0; ok; ++it) {
-        const int slot = it & 1;
-        if (!mbar_wait_warp(&sm.item_empty[slot], ((it >> 1) & 1) ^ 1, &sm.abort, err))
+        const int slot = it % kWSlots;
+        KwItem x{};
+        // runs that no sequence reaches are passed over here
+        while (true) {
+            const uint32_t v = __shfl_sync(0xffffffffu, next, 0);
+            x.valid = 0;
+            if (v >= static_cast<uint32_t>(a.n_items))
+                break;
+            next = draw();
+            if (kw_item<MANY>(a, static_cast<int>(v), x))
+                break;
+        }
+        if (!mbar_wait_warp(&sm.item_empty[slot], ((it / kWSlots) & 1) ^ 1, &sm.abort, err))
             break;
-        int item = -1;
-        KwItem x;
-        // tiles that no sequence has are passed over here
-        do {
-            if (lane == 0) {
-                const uint32_t v = atomicAdd(&a.hdr->work_counter, 1u);
-                item = v < static_cast<uint32_t>(a.n_items) ? static_cast<int>(v) : -1;
-            }
-            item = __shfl_sync(0xffffffffu, item, 0);
-        } while (item >= 0 && !kw_item(a, item, x));
         if (lane == 0) {
-            sm.item[slot] = item;
+            sm.item[slot] = x;
             mbar_arrive(&sm.item_full[slot]);
         }
         __syncwarp();
-        if (item < 0)
+        if (!x.valid)
             break;
-        const int ks = kn % kWKStages;
-        if (!mbar_wait_warp(&sm.k_empty[ks], ((kn / kWKStages) & 1) ^ 1, &sm.abort, err))
-            break;
-        ++kn;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.k_full[ks], 2 * kWHalf);
-            tma_load_4d(sm.k[ks], tm_k, 0, x.h, x.kt * kWTile, x.b, &sm.k_full[ks]);
-            tma_load_4d(sm.k[ks] + kWHalf, tm_k, 64, x.h, x.kt * kWTile, x.b, &sm.k_full[ks]);
-        }
-        __syncwarp();
-        ok = kw_tiles(a, x, lane, [&](const KwTile &t) {
-            const int qs = qn % kWQStages;
-            if (!mbar_wait_warp(&sm.q_empty[qs], ((qn / kWQStages) & 1) ^ 1, &sm.abort, err))
-                return false;
-            ++qn;
+        for (int kt = x.kt0; ok && kt < x.kt1; ++kt) {
+            const KwRange rg = kw_range<MANY>(a, x, kt);
+            if (rg.s0 >= rg.s1)
+                continue;
+            if (!mbar_wait_warp(&sm.k_empty[k.s], k.phase ^ 1, &sm.abort, err)) {
+                ok = false;
+                break;
+            }
             if (lane == 0) {
-                const int head = x.h * a.g + t.head0;
-                mbar_arrive_expect_tx(&sm.q_full[qs], t.nh * t.nr * 256);
-                if (t.nr == kWTile) {
-                    tma_load_4d(sm.q[qs], tm_q, 0, head, t.t0, x.b, &sm.q_full[qs]);
-                    tma_load_4d(sm.q[qs] + kWHalf, tm_q, 64, head, t.t0, x.b, &sm.q_full[qs]);
-                } else {
-                    int row = 0;
-                    for (int hh = 0; hh < t.nh; ++hh)
-                        for (int r = 0; r < t.nr; r += 16, row += 16) {
-                            tma_load_4d(sm.q[qs] + row * 128, tm_q16, 0, head + hh, t.t0 + r, x.b,
-                                        &sm.q_full[qs]);
-                            tma_load_4d(sm.q[qs] + kWHalf + row * 128, tm_q16, 64, head + hh, t.t0 + r,
-                                        x.b, &sm.q_full[qs]);
-                        }
+                constexpr int tiles = MANY ? 2 : 1;
+                mbar_arrive_expect_tx(&sm.k_full[k.s], tiles * 2 * kWKHalf);
+#pragma unroll
+                for (int p = 0; p < tiles; ++p) {
+                    uint8_t *dst = MANY ? sm.held + p * 2 * kWKHalf : sm.ring[k.s];
+                    const int row = (kt * tiles + p) * kWTile;
+                    tma_load_4d(dst, tm_k, 0, x.h, row, x.b, &sm.k_full[k.s]);
+                    tma_load_4d(dst + kWKHalf, tm_k, 64, x.h, row, x.b, &sm.k_full[k.s]);
                 }
             }
             __syncwarp();
-            return true;
-        });
+            k.next();
+            ok = kw_tiles<MANY>(a, x, rg, kt, lane, [&](const KwTile &t) {
+                const int head = x.h * a.g + t.head0;
+                if constexpr (MANY) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (!mbar_wait_warp(&sm.q_empty[q.s], q.phase ^ 1, &sm.abort, err))
+                            return false;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&sm.q_full[q.s], t.nh * t.nr * 128);
+                            kw_load_q(tm_q, a, sm.ring[q.s], head, x.b, t, half, &sm.q_full[q.s]);
+                        }
+                        __syncwarp();
+                        q.next();
+                    }
+                } else if (!held.same(x, t)) {
+                    if (!mbar_wait_warp(&sm.q_empty[q.s], q.phase ^ 1, &sm.abort, err))
+                        return false;
+                    ++held.n;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&sm.q_full[q.s], t.nh * t.nr * 256);
+                        kw_load_q(tm_q, a, sm.held, head, x.b, t, 0, &sm.q_full[q.s]);
+                        kw_load_q(tm_q, a, sm.held + kWQHalf, head, x.b, t, 1, &sm.q_full[q.s]);
+                    }
+                    __syncwarp();
+                    q.next();
+                }
+                return true;
+            });
+        }
     }
     // Before leaving on an abort, let the copies already issued land.
     if (__any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
         volatile int no_abort = 0;
-        for (uint32_t k = kn > kWKStages ? kn - kWKStages : 0; k < kn; ++k)
-            mbar_wait_warp(&sm.k_full[k % kWKStages], (k / kWKStages) & 1, &no_abort, nullptr);
-        for (uint32_t k = qn > kWQStages ? qn - kWQStages : 0; k < qn; ++k)
-            mbar_wait_warp(&sm.q_full[k % kWQStages], (k / kWQStages) & 1, &no_abort, nullptr);
+        for (uint32_t n = k.n > KS ? k.n - KS : 0; n < k.n; ++n)
+            mbar_wait_warp(&sm.k_full[n % KS], (n / KS) & 1, &no_abort, nullptr);
+        for (uint32_t n = q.n > QS ? q.n - QS : 0; n < q.n; ++n)
+            mbar_wait_warp(&sm.q_full[n % QS], (n / QS) & 1, &no_abort, nullptr);
     }
 }
 
-__device__ __forceinline__ void kw_mma(const KwArgs &a, KwSmem &sm, uint32_t tmem, int lane)
+// The LSE k-step's operands are stored without swizzle: 8 rows x 16 bytes of a
+// core matrix follow one another, the two along k are 128 bytes apart, the next
+// eight rows 256.
+__device__ __forceinline__ uint64_t kw_sdesc_x(uint32_t saddr)
+{
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(128 >> 4) << 16 |
+           static_cast<uint64_t>(256 >> 4) << 32 | static_cast<uint64_t>(1) << 46;
+}
+
+__device__ __forceinline__ uint8_t *kw_row_x(uint8_t *base, int row)
+{
+    return base + (row >> 3) * 256 + (row & 7) * 16;
+}
+
+// Few rows: two warps, one per TMEM buffer, take every other query tile, so that
+// one does its waits and descriptors (about 1000 cycles a tile) while the other's
+// MMAs run.  Many rows: one warp (p = 0) for both key tiles of the pair, one after
+// the other, so that the first one's sums run under the second one's MMAs.
+// (Alternating between them every 64 dims ended both together and left MMAs and
+// exponentials to take turns: 1091 us for 16K x 16K and 32 heads against 890; a
+// warp each, in turns by a token: 945.)
+template <bool MANY>
+__device__ __forceinline__ void kw_mma(const KwArgs &a, KwSmem &sm, uint32_t tmem, int lane, int p)
 {
     uint32_t *err = &a.hdr->error;
-    uint32_t kn = 0, n = 0;
-    for (int it = 0;; ++it) {
-        const int item = kw_take(a, sm, it);
-        if (item < 0)
-            break;
-        KwItem x;
-        kw_item(a, item, x);
-        const int ks = kn % kWKStages;
-        if (!mbar_wait_warp(&sm.k_full[ks], (kn / kWKStages) & 1, &sm.abort, err))
-            break;
-        ++kn;
-        const uint32_t kaddr = smem_u32(sm.k[ks]);
-        const bool ok = kw_tiles(a, x, lane, [&](const KwTile &t) {
-            const int buf = n % kWGroups, qs = n % kWQStages;
-            if (!mbar_wait_warp(&sm.s_free[buf], ((n / kWGroups) & 1) ^ 1, &sm.abort, err) ||
-                !mbar_wait_warp(&sm.q_full[qs], (n / kWQStages) & 1, &sm.abort, err))
-                return false;
-            ++n;
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t idesc = idesc_bf16_f32(kWTile, t.nh * t.nr, false, false);
-                const uint32_t qaddr = smem_u32(sm.q[qs]);
+    constexpr int KS = MANY ? 1 : kWStages, QS = MANY ? kWStages : 1;
+    KwRing<KS> k;
+    KwRing<QS> q;
+    uint32_t n = 0, uses = 0;                                // column tiles, and those of this warp
+    const uint32_t ring = smem_u32(sm.ring[0]), held_addr = smem_u32(sm.held);
+    const uint64_t kx = kw_sdesc_x(smem_u32(sm.kx));
+    KwHeld held{};
+    bool ok = true;
+    KwItem x;
+    // the nine MMAs of a tile: 2 x 64 dims and the LSE
+    auto mma = [&](uint32_t d, uint32_t ka, uint32_t qa0, uint32_t qa1, uint32_t qx, uint32_t idesc) {
+        const uint64_t k0 = sdesc_sw128(ka, 16, 1024), k1 = sdesc_sw128(ka + kWKHalf, 16, 1024);
+        const uint64_t q0 = sdesc_sw128(qa0, 16, 1024), q1 = sdesc_sw128(qa1, 16, 1024);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t o = (k >> 2) * kWHalf + (k & 3) * 32;
-                    tc_mma(tmem + buf * kWTile, sdesc_sw128(kaddr + o, 16, 1024),
-                           sdesc_sw128(qaddr + o, 16, 1024), idesc, k > 0 ? 1u : 0u);
+        for (int i = 0; i < 4; ++i)
+            tc_mma(d, k0 + 2 * i, q0 + 2 * i, idesc, i == 0 ? 0u : 1u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            tc_mma(d, k1 + 2 * i, q1 + 2 * i, idesc, 1u);
+        tc_mma(d, kx, kw_sdesc_x(qx), idesc, 1u);
+    };
+    for (int it = 0; ok && kw_take(a, sm, it, x) > 0; ++it) {
+        for (int kt = x.kt0; ok && kt < x.kt1; ++kt) {
+            const KwRange rg = kw_range<MANY>(a, x, kt);
+            if (rg.s0 >= rg.s1)
+                continue;
+            ok = mbar_wait_warp(&sm.k_full[k.s], k.phase, &sm.abort, err);
+            if (!ok)
+                break;
+            const uint32_t kaddr = MANY ? held_addr : ring + k.s * kWQHalf;
+            ok = kw_tiles<MANY>(a, x, rg, kt, lane, [&](const KwTile &t) {
+                const uint32_t idesc = idesc_bf16_f32(kWTile, t.nh * t.nr, false, false);
+                const uint32_t mine = n++;
+                if constexpr (MANY) {
+                    const int lb = mine % kWBufs;
+                    const uint32_t q0 = ring + q.s * kWQHalf, qx = smem_u32(sm.qx[lb]);
+                    if (!mbar_wait_warp(&sm.lse_full[lb], (mine / kWBufs) & 1, &sm.abort, err) ||
+                        !mbar_wait_warp(&sm.q_full[q.s], q.phase, &sm.abort, err) ||
+                        !mbar_wait_warp(&sm.q_full[q.s + 1], q.phase, &sm.abort, err))
+                        return false;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        if (!mbar_wait_warp(&sm.s_free[b], (mine & 1) ^ 1, &sm.abort, err))
+                            return false;
+                        tc_fence_after();
+                        if (lane == 0) {
+                            mma(tmem + b * kWCols, kaddr + b * 2 * kWKHalf, q0, q0 + kWQHalf, qx, idesc);
+                            tc_commit(&sm.s_full[b]);
+                            if (b == 1) {
+                                tc_commit(&sm.q_empty[q.s]);
+                                tc_commit(&sm.q_empty[q.s + 1]);
+                                tc_commit(&sm.lse_empty[lb]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    q.next();
+                    q.next();                            // two halves: q.s is 0 or 2
+                } else {
+                    if (!held.same(x, t)) {
+                        // the tile before it is done with once this warp's MMAs so far are
+                        if (held.n > 0) {
+                            if (lane == 0)
+                                tc_commit(&sm.q_empty[q.s]);
+                            __syncwarp();
+                            q.next();
+                        }
+                        if (!mbar_wait_warp(&sm.q_full[q.s], q.phase, &sm.abort, err))
+                            return false;
+                        ++held.n;
+                    }
+                    if (static_cast<int>(mine % kWBufs) != p)
+                        return true;
+                    if (!mbar_wait_warp(&sm.lse_full[p], uses & 1, &sm.abort, err) ||
+                        !mbar_wait_warp(&sm.s_free[p], (uses & 1) ^ 1, &sm.abort, err))
+                        return false;
+                    ++uses;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        mma(tmem + p * kWCols, kaddr, held_addr, held_addr + kWQHalf, smem_u32(sm.qx[p]), idesc);
+                        tc_commit(&sm.s_full[p]);
+                        tc_commit(&sm.lse_empty[p]);
+                    }
+                    __syncwarp();
                 }
-                tc_commit(&sm.s_full[buf]);
-                tc_commit(&sm.q_empty[qs]);
-            }
+                return true;
+            });
+            if (ok && lane == 0)
+                tc_commit(&sm.k_empty[k.s]);
             __syncwarp();
-            return true;
-        });
-        if (!ok)
-            break;
-        if (lane == 0)
-            tc_commit(&sm.k_empty[ks]);
-        __syncwarp();
+            k.next();
+        }
     }
     // Before leaving on an abort, let the MMAs already issued finish (their
-    // operands and accumulators go with the CTA).
+    // operands and accumulators go with the CTA): a commit on a barrier of their
+    // own covers all of this warp's.
     if (__any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort)) && n > 0) {
         volatile int no_abort = 0;
-        mbar_wait_warp(&sm.s_full[(n - 1) % kWGroups], ((n - 1) / kWGroups) & 1, &no_abort, nullptr);
+        if (lane == 0)
+            tc_commit(&sm.drain[p]);
+        __syncwarp();
+        mbar_wait_warp(&sm.drain[p], 0, &no_abort, nullptr);
     }
 }
 
-// LSE of each tile's columns in log2 units; rows that keep nothing (-inf) get
-// +inf, so that they give 2^-inf = 0.
+// -LSE / scale of each tile's columns, in three bf16 parts whose sum is the fp32
+// value; rows that keep nothing (LSE = -inf) get -inf, so that they give
+// 2^-inf = 0.
+template <bool MANY>
 __device__ __forceinline__ void kw_lse(const KwArgs &a, KwSmem &sm, int lane)
 {
     uint32_t *err = &a.hdr->error;
     const float INF = __int_as_float(0x7f800000);
-    uint32_t n = 0;
-    for (int it = 0;; ++it) {
-        const int item = kw_take(a, sm, it);
-        if (item < 0)
-            break;
-        KwItem x;
-        kw_item(a, item, x);
-        const bool ok = kw_tiles(a, x, lane, [&](const KwTile &t) {
-            const int buf = n % kWGroups;
-            const float *row = a.lse + x.b * a.lse_sb + (x.h * a.g + t.head0) * a.lse_sh + t.t0;
-            float v[4];
+    KwRing<kWBufs> buf;
+    bool ok = true;
+    KwItem x;
+    KwHeld held[kWBufs] = {};                                // n: 1 once the buffer holds a tile's
+    for (int it = 0; ok && kw_take(a, sm, it, x) > 0; ++it)
+        for (int kt = x.kt0; ok && kt < x.kt1; ++kt)
+            ok = kw_tiles<MANY>(a, x, kw_range<MANY>(a, x, kt), kt, lane, [&](const KwTile &t) {
+                const bool same = !MANY && (buf.s ? held[1].same(x, t) : held[0].same(x, t));
+                float v[kWCols / 32];
+                if (!same) {
+                    held[0].n |= buf.s == 0;
+                    held[1].n |= buf.s == 1;
+                    const float *row = a.lse + x.b * a.lse_sb + (x.h * a.g + t.head0) * a.lse_sh + t.t0;
+                    if (t.nr == kWTile) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int c = i * 32 + lane, hh = c / t.nr, r = c - hh * t.nr;
-                v[i] = hh < t.nh && r < t.cnt ? __ldg(row + hh * a.lse_sh + r) : 0.f;
-            }
-            if (!mbar_wait_warp(&sm.s_free[buf], ((n / kWGroups) & 1) ^ 1, &sm.abort, err))
-                return false;
-            ++n;
+                        for (int i = 0; i < kWCols / 32; ++i) {
+                            const int hh = i / 4, r = i % 4 * 32 + lane;
+                            v[i] = hh < t.nh && r < t.cnt ? __ldg(row + hh * a.lse_sh + r) : 0.f;
+                        }
+                    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sm.lse[buf][i * 32 + lane] = v[i] == -INF ? INF : v[i] * 1.4426950408889634f;
-            mbar_arrive(&sm.lse_full[buf]);
-            return true;
-        });
-        if (!ok)
-            break;
-    }
+                        for (int i = 0; i < kWCols / 32; ++i) {
+                            const int c = i * 32 + lane, hh = c / t.nr, r = c - hh * t.nr;
+                            v[i] = hh < t.nh && r < t.cnt ? __ldg(row + hh * a.lse_sh + r) : 0.f;
+                        }
+                    }
+                }
+                if (!mbar_wait_warp(&sm.lse_empty[buf.s], buf.phase ^ 1, &sm.abort, err))
+                    return false;
+                if (!same) {
+#pragma unroll
+                    for (int i = 0; i < kWCols / 32; ++i) {
+                        const float f = v[i] == -INF ? -INF : v[i] * -a.inv_scale;
+                        const float hi = __bfloat162float(__float2bfloat16_rn(f));
+                        const float r1 = fabsf(f) < INF && fabsf(hi) < INF ? f - hi : 0.f;
+                        const float mid = __bfloat162float(__float2bfloat16_rn(r1));
+                        *reinterpret_cast<uint4 *>(kw_row_x(sm.qx[buf.s], i * 32 + lane)) =
+                            make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(r1 - mid, 0.f), 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+                mbar_arrive(&sm.lse_full[buf.s]);
+                buf.next();
+                return true;
+            });
 }
 
 // 32 lanes x 16 columns of 32-bit TMEM -> 16 registers per thread.
@@ -363,139 +597,196 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
                  : "memory");
 }
 
-// Barrier of the summing warps that also tells whether any of them failed.
-__device__ __forceinline__ bool kw_sync_or(bool failed)
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
 {
-    int any;
-    asm volatile("{\n\t.reg .pred p, q;\n\t"
-                 "setp.ne.s32 p, %1, 0;\n\t"
-                 "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
-                 "selp.s32 %0, 1, 0, q;\n\t}"
-                 : "=r"(any)
-                 : "r"(failed ? 1 : 0), "n"(kWSumThreads)
-                 : "memory");
-    return any != 0;
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
+// Adds 2^(v * c2) over N columns to two pairs of sums; with MASKED only the
+// columns e with lo <= e < hi.
+template <int N, bool MASKED>
+__device__ __forceinline__ void kw_add(const uint32_t (&v)[N], uint64_t c2, int lo, int hi, uint64_t &s0,
+                                       uint64_t &s1)
+{
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+        float p[4];
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), c2), p[0], p[1]);
+        f2_unpack(f2_mul(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), c2), p[2], p[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            p[k] = ex2(p[k]);
+            if (MASKED)
+                p[k] = e + k >= lo && e + k < hi ? p[k] : 0.f;
+        }
+        s0 = f2_add(s0, f2_pack(p[0], p[1]));
+        s1 = f2_add(s1, f2_pack(p[2], p[3]));
+    }
+}
+
+// The columns [c0, c1) of one key tile's products: thread sums, rows [lo, hi) of
+// each head.  ts: the buffer's TMEM address at this warp's lanes.
+__device__ __forceinline__ float kw_columns(uint32_t ts, int c0, int c1, int nr, int lo, int hi, uint64_t c2)
+{
+    uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0;
+    if (__all_sync(0xffffffffu, lo <= 0 && hi >= nr)) {
+        int c = c0;
+        for (; c + 64 <= c1; c += 64) {
+            // the second load runs under the first one's sums
+            uint32_t v0[32], v1[32];
+            tmem_ld32(ts + c, v0);
+            tmem_wait_ld();
+            tmem_ld32(ts + c + 32, v1);
+            kw_add<32, false>(v0, c2, 0, 0, s0, s1);
+            tmem_wait_ld();
+            kw_add<32, false>(v1, c2, 0, 0, s0, s1);
+        }
+        for (; c < c1; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(ts + c, v);
+            tmem_wait_ld();
+            kw_add<16, false>(v, c2, 0, 0, s0, s1);
+        }
+    } else if (__any_sync(0xffffffffu, lo < hi)) {
+        for (int c = c0; c < c1; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(ts + c, v);
+            tmem_wait_ld();
+            const int r0 = c % nr;
+            kw_add<16, true>(v, c2, lo - r0, hi - r0, s0, s1);
+        }
+    }
+    float p0, p1;
+    f2_unpack(f2_add(s0, s1), p0, p1);
+    return p0 + p1;
+}
+
+template <bool MANY>
 __device__ __forceinline__ void kw_sum(const KwArgs &a, KwSmem &sm, uint32_t tmem, int warp, int lane)
 {
     uint32_t *err = &a.hdr->error;
     const int wg = (warp - kWFirstWarp) >> 2;
     const int key = (warp & 3) * 32 + lane;                  // TMEM lane
-    const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * kWTile;
+    const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint64_t c2 = f2_pack(a.c2, a.c2);
-    uint32_t n = 0;                                          // tiles so far, all warpgroups'
-    for (int it = 0;; ++it) {
-        const int item = kw_take(a, sm, it);
-        if (item < 0) {
-            kw_sync_or(item == -2);
-            return;
-        }
-        KwItem x;
-        kw_item(a, item, x);
-        const int j = x.kt * kWTile + key;
-        const bool bounded = x.mode == EA_SSA && j >= a.sink;
-        float total = 0.f;
-        const bool ok = kw_tiles(a, x, lane, [&](const KwTile &t) {
-            const uint32_t mine = n++;
-            if (static_cast<int>(mine % kWGroups) != wg)
+    const int buf = wg >> 1, half = wg & 1;
+    uint32_t n = 0, kc = 0;                                  // column tiles and key tiles so far
+    bool ok = true;
+    KwItem x;
+    for (int it = 0; ok && kw_take(a, sm, it, x) > 0; ++it) {
+        for (int kt = x.kt0; ok && kt < x.kt1; ++kt) {
+            const KwRange rg = kw_range<MANY>(a, x, kt);
+            const int j = (MANY ? 2 * kt + buf : kt) * kWTile + key;
+            const bool bounded = x.mode == EA_SSA && j >= a.sink;
+            float total = 0.f;
+            ok = kw_tiles<MANY>(a, x, rg, kt, lane, [&](const KwTile &t) {
+                const uint32_t mine = n++;
+                // few rows: the two buffers take turns; many rows: both serve every tile
+                if (!MANY && static_cast<int>(mine % kWBufs) != buf)
+                    return true;
+                if (!mbar_wait_warp(&sm.s_full[buf], MANY ? mine & 1 : (mine / kWBufs) & 1, &sm.abort, err))
+                    return false;
+                tc_fence_after();
+                const int q16 = t.nh * t.nr / 16, mid = 16 * ((q16 + 1) / 2);
+                // rows [lo, hi) of each head keep key j
+                const int lo = j - (x.off + t.t0);
+                int hi = bounded ? min(t.cnt, lo + a.window) : t.cnt;
+                if (MANY && !((t.keep >> buf) & 1u))
+                    hi = 0;
+                const float w = kw_columns(ts + buf * kWCols, half ? mid : 0, half ? 16 * q16 : mid, t.nr, lo,
+                                           hi, c2);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.s_free[buf]);
+                total += w;
                 return true;
-            const uint32_t phase = (mine / kWGroups) & 1;
-            if (!mbar_wait_warp(&sm.lse_full[wg], phase, &sm.abort, err) ||
-                !mbar_wait_warp(&sm.s_full[wg], phase, &sm.abort, err))
-                return false;
-            tc_fence_after();
-            const int cols = t.nh * t.nr;
-            // columns [lo, hi) of each head's rows keep key j
-            const int i0 = x.off + t.t0;
-            const int lo = j - i0;
-            const int hi = bounded ? static_cast<int>(min(static_cast<int64_t>(t.cnt),
-                                                          static_cast<int64_t>(lo) + a.window))
-                                   : t.cnt;
-            const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= t.nr);
-            uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0;
-            for (int c = 0; c < cols; c += 16) {
-                uint32_t v[16];
-                tmem_ld16(ts + c, v);
-                tmem_wait_ld();
-                const int r0 = c % t.nr;
-#pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const float4 l = *reinterpret_cast<const float4 *>(&sm.lse[wg][c + e]);
-                    const uint64_t y0 = f2_fma(f2_pack(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
-                                               c2, f2_pack(-l.x, -l.y));
-                    const uint64_t y1 = f2_fma(f2_pack(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
-                                               c2, f2_pack(-l.z, -l.w));
-                    float p[4];
-                    f2_unpack(y0, p[0], p[1]);
-                    f2_unpack(y1, p[2], p[3]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        p[k] = ex2(p[k]);
-                        if (!whole) {
-                            const int r = r0 + e + k;
-                            p[k] = r >= lo && r < hi ? p[k] : 0.f;
-                        }
-                    }
-                    s0 = f2_add(s0, f2_pack(p[0], p[1]));
-                    s1 = f2_add(s1, f2_pack(p[2], p[3]));
-                }
-            }
-            tc_fence_before();
-            mbar_arrive(&sm.s_free[wg]);
-            float p0, p1;
-            f2_unpack(f2_add(s0, s1), p0, p1);
-            total += p0 + p1;
-            return true;
-        });
-        float (&red)[kWGroups][kWTile] = sm.red[it & 1];
-        red[wg][key] = total;
-        if (kw_sync_or(!ok))
-            return;
-        if (wg == 0 && j < x.L) {
+            });
+            if (!ok)
+                break;
+            // the warpgroups' sums are joined: many rows, a buffer's two by the first of
+            // them; few rows, all four by each in turn
+            const int slot = kc % kWSlots;
+            const uint32_t phase = (kc / kWSlots) & 1;
+            ++kc;
+            ok = mbar_wait_warp(&sm.red_empty[slot], phase ^ 1, &sm.abort, err);
+            if (!ok)
+                break;
+            sm.red[slot][wg][key] = total;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.red_full[slot]);
+            if (MANY ? half != 0 : slot != wg)
+                continue;
+            ok = mbar_wait_warp(&sm.red_full[slot], phase, &sm.abort, err);
+            if (!ok)
+                break;
             float w = 0.f;
 #pragma unroll
             for (int k = 0; k < kWGroups; ++k)
-                w += red[k][key];
-            const int64_t at = (static_cast<int64_t>(x.b) * a.Hkv + x.h) * a.Lmax + j;
-            if (a.parts > 1)
-                a.partial[static_cast<int64_t>(x.part) * a.B * a.Hkv * a.Lmax + at] = w;
-            else
-                a.weights[at] = a.accumulate ? a.weights[at] + w : w;
+                if (!MANY || k / 2 == buf)
+                    w += sm.red[slot][k][key];
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.red_empty[slot]);
+            if (j < x.L) {
+                const int64_t at = (static_cast<int64_t>(x.b) * a.Hkv + x.h) * a.Lmax + j;
+                if (a.parts > 1)
+                    a.partial[static_cast<int64_t>(x.part) * a.B * a.Hkv * a.Lmax + at] = w;
+                else
+                    a.weights[at] = a.accumulate ? a.weights[at] + w : w;
+            }
         }
     }
 }
+static_assert(kWSlots == kWGroups, "few rows: warpgroup w joins the key tiles of slot w");
 
+template <bool MANY>
 __global__ void __launch_bounds__(kWThreads, 1)
-    key_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q,
-                       const __grid_constant__ CUtensorMap tm_q16, const KwArgs a)
+    key_weights_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ KwMaps tm_q,
+                       const KwArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     KwSmem &sm = *reinterpret_cast<KwSmem *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int kMma = MANY ? 1 : 2;                        // MMA warps
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kWKStages; ++s) {
+        for (int s = 0; s < kWStages; ++s) {
             mbar_init(&sm.k_full[s], 1);
-            mbar_init(&sm.k_empty[s], 1);
-        }
-        for (int s = 0; s < kWQStages; ++s) {
+            mbar_init(&sm.k_empty[s], kMma);
             mbar_init(&sm.q_full[s], 1);
-            mbar_init(&sm.q_empty[s], 1);
+            mbar_init(&sm.q_empty[s], kMma);
         }
-        for (int s = 0; s < kWGroups; ++s) {
+        for (int s = 0; s < kWBufs; ++s) {
             mbar_init(&sm.s_full[s], 1);
-            mbar_init(&sm.s_free[s], 128);
+            mbar_init(&sm.s_free[s], 8);                      // the warps of a buffer's warpgroups
             mbar_init(&sm.lse_full[s], 32);
+            mbar_init(&sm.lse_empty[s], 1);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kWSlots; ++s) {
+            mbar_init(&sm.red_full[s], 4 * kWGroups);
+            mbar_init(&sm.red_empty[s], MANY ? 8 : 4);        // the joining warpgroups' warps
             mbar_init(&sm.item_full[s], 1);
-            mbar_init(&sm.item_empty[s], 2 + 4 * kWGroups);   // MMA, LSE and summing warps
+            mbar_init(&sm.item_empty[s], kMma + 1 + 4 * kWGroups);   // MMA, LSE and summing warps
         }
+        mbar_init(&sm.drain[0], 1);
+        mbar_init(&sm.drain[1], 1);
         sm.abort = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
     }
+    // the LSE k-step: ones against a row's three parts, zeros behind them
+    for (int i = threadIdx.x; i < kWBufs * kWCols + kWTile; i += kWThreads) {
+        uint8_t *row = i < kWBufs * kWCols ? kw_row_x(sm.qx[i / kWCols], i % kWCols)
+                                           : kw_row_x(sm.kx, i - kWBufs * kWCols);
+        *reinterpret_cast<uint4 *>(row) =
+            i < kWBufs * kWCols ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(row + 128) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
     if (warp == 1) {
         tmem_alloc(&sm.tmem_base, kWTmemCols);
         tmem_relinquish();
@@ -505,13 +796,16 @@ __global__ void __launch_bounds__(kWThreads, 1)
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     if (warp == 0)
-        kw_producer(&tm_k, &tm_q, &tm_q16, a, sm, lane);
+        kw_producer<MANY>(&tm_k, tm_q, a, sm, lane);
     else if (warp == 1)
-        kw_mma(a, sm, tmem, lane);
+        kw_mma<MANY>(a, sm, tmem, lane, 0);
     else if (warp == 2)
-        kw_lse(a, sm, lane);
+        kw_lse<MANY>(a, sm, lane);
+    else if (!MANY && warp == 3)
+        kw_mma<MANY>(a, sm, tmem, lane, 1);
     else if (warp >= kWFirstWarp)
-        kw_sum(a, sm, tmem, warp, lane);
+        kw_sum<MANY>(a, sm, tmem, warp, lane);
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
@@ -539,15 +833,52 @@ __global__ void __launch_bounds__(256) kw_join_kernel(const KwArgs a)
     a.weights[at] = a.accumulate ? a.weights[at] + w : w;
 }
 
-// Shares per key tile: enough items for about four per SM of this GPU's 152,
-// none shorter than one 128-row segment.  A fixed number of SMs, so that a
-// workspace and the result do not depend on the device.
-static int kw_parts(int B, int Tq, int Lmax, int Hkv)
+// How the work is cut, from the sizes alone and for this GPU's 152 SMs, so that a
+// workspace and the result do not depend on where they are made.
+//   many   more query columns than one tile holds: pairs of key tiles share them
+//   parts  shares of a key tile's queries: enough items for about four per SM,
+//          none shorter than a tile's rows
+//   run    key tiles per item: one (pair), except where one query tile serves
+//          all of them, which costs about as much to load as three key tiles:
+//          one item per SM, of at most 16 tiles (17 GFLOP over 32K keys: 2 tiles
+//          an item 67 us, 4 55, 8 51)
+struct KwPlan {
+    bool many;
+    int seg, parts, run;
+    int64_t units;         // key tiles or pairs of one sequence
+};
+
+static KwPlan kw_plan(int B, int Tq, int Lmax, int Hkv, int g)
 {
-    const int64_t items = ceil_div(Lmax, kWTile) * B * Hkv;
-    const int64_t want = ceil_div(4 * 152, items), most = ceil_div(Tq, kWTile);
-    const int64_t p = want < most ? want : most;
-    return static_cast<int>(p < 1 ? 1 : p > kWMaxParts ? kWMaxParts : p);
+    KwPlan p;
+    p.seg = g == 1 ? kWCols : kWTile;
+    p.many = ceil_div(Tq, 16) * 16 * g > kWCols;
+    p.units = ceil_div(Lmax, p.many ? 2 * kWTile : kWTile);
+    const int64_t tiles = p.units * B * Hkv;
+    const int64_t want = ceil_div(4 * 152, tiles), most = ceil_div(Tq, p.seg);
+    const int64_t parts = want < most ? want : most;
+    p.parts = static_cast<int>(parts < 1 ? 1 : parts > kWMaxParts ? kWMaxParts : parts);
+    const int64_t run = p.many ? 1 : ceil_div(tiles, 152);
+    p.run = static_cast<int>(run > 16 ? 16 : run);
+    return p;
+}
+
+template <bool MANY>
+static cudaError_t launch_kw(const CUtensorMap &tk, const KwMaps &tq, const KwArgs &a, int sms, int dev, cudaStream_t st)
+{
+    static bool attr_done[64] = {};   // the attribute is set once per device
+    if (dev >= 64 || !attr_done[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<MANY>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(kKwSmemBytes));
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            attr_done[dev] = true;
+    }
+    key_weights_kernel<MANY><<<static_cast<unsigned>(a.n_items < sms ? a.n_items : sms), kWThreads,
+                               kKwSmemBytes, st>>>(tk, tq, a);
+    return cudaGetLastError();
 }
 
 } // namespace ea
@@ -559,7 +890,7 @@ extern "C" size_t ea_key_weights_workspace_size(int B, int Tq, int Lmax, int Hq,
     if (B < 1 || Tq < 1 || Lmax < 1 || Lmax > EA_MAX_SEQ || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 ||
         d != EA_HEAD_DIM)
         return 0;
-    const int parts = kw_parts(B, Tq, Lmax, Hkv);
+    const int parts = kw_plan(B, Tq, Lmax, Hkv, Hq / Hkv).parts;
     return sizeof(ea_ws_header) +
            (parts > 1 ? align_up(sizeof(float) * static_cast<size_t>(parts) * B * Hkv * Lmax, 256) : 0);
 }
@@ -607,19 +938,26 @@ extern "C" ea_status ea_key_weights(const void *Q, const void *K, const float *L
     a.g = Hq / Hkv;
     a.nB = static_cast<int>(ceil_div(Lmax, EA_TILE));
     a.sink = sink;
-    a.window = window;
-    a.parts = kw_parts(B, Tq, Lmax, Hkv);
+    a.window = window < 2 * EA_MAX_SEQ ? window : 2 * EA_MAX_SEQ;   // (sums of positions stay in 32 bits)
+    const KwPlan plan = kw_plan(B, Tq, Lmax, Hkv, a.g);
+    a.parts = plan.parts;
+    a.run = plan.run;
+    a.seg = plan.seg;
+    a.seg_log2 = plan.seg == kWTile ? 7 : 8;
     a.accumulate = accumulate != 0;
     a.c2 = scale * 1.4426950408889634f;
-    const int64_t items = static_cast<int64_t>(a.nB) * a.parts * B * Hkv;
+    a.inv_scale = 1.f / scale;
+    const int64_t items = ceil_div(plan.units, a.run) * a.parts * B * Hkv;
     if (items >= (int64_t(1) << 31) - 1024)
         return EA_ERR_UNSUPPORTED;
     a.n_items = static_cast<int>(items);
 
-    alignas(64) CUtensorMap tk, tq, tq16;
+    alignas(64) CUtensorMap tk;
+    alignas(64) KwMaps tq;
+    a.box = static_cast<int>(ceil_div(Tq, 16) * 16 < kWTile ? ceil_div(Tq, 16) * 16 : kWTile);
     if (!encode_tmap_bf16_4d(&tk, K, d, Hkv, Lmax, B, k_str, 64, kWTile, true) ||
-        !encode_tmap_bf16_4d(&tq, Q, d, Hq, Tq, B, q_str, 64, kWTile, true) ||
-        !encode_tmap_bf16_4d(&tq16, Q, d, Hq, Tq, B, q_str, 64, 16, true))
+        !encode_tmap_bf16_4d(&tq.rows, Q, d, Hq, Tq, B, q_str, 64, a.box, true) ||
+        !encode_tmap_bf16_4d(&tq.r16, Q, d, Hq, Tq, B, q_str, 64, 16, true))
         return EA_ERR_INVALID_ARG;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
@@ -627,18 +965,11 @@ extern "C" ea_status ea_key_weights(const void *Q, const void *K, const float *L
     const int sms = num_sms(dev);
     if (sms <= 0)
         return EA_ERR_CUDA;
-    static bool attr_done[64] = {};   // the attribute is set once per device
-    if (dev >= 64 || !attr_done[dev]) {
-        if (cudaFuncSetAttribute(key_weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kKwSmemBytes)) != cudaSuccess)
-            return EA_ERR_CUDA;
-        if (dev < 64)
-            attr_done[dev] = true;
-    }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     kw_setup_kernel<<<1, 256, 0, st>>>(a);
-    key_weights_kernel<<<static_cast<unsigned>(items < sms ? items : sms), kWThreads, kKwSmemBytes, st>>>(
-        tk, tq, tq16, a);
+    if ((plan.many ? launch_kw<true>(tk, tq, a, sms, dev, st)
+                   : launch_kw<false>(tk, tq, a, sms, dev, st)) != cudaSuccess)
+        return EA_ERR_CUDA;
     if (a.parts > 1)
         kw_join_kernel<<<dim3(static_cast<unsigned>(ceil_div(Lmax, 256)), static_cast<unsigned>(B * Hkv)), 256,
                          0, st>>>(a);

@@ -252,3 +252,39 @@ def test_prefill_evict_and_decode_together(dev, dtype):
                                    atol=2.0 ** -10 * got["ks"].max().item())
     Or, Lr, _, (tO, tL, _) = decode_ref(q, Ks, Vs, value_scales(got), n2.tolist(), modes, sink, recent, SCALE)
     assert (np.abs(O.float().cpu().numpy() - Or) <= tO).all() and (np.abs(L.cpu().numpy() - Lr) <= tL).all()
+
+
+@pytest.mark.parametrize("Tq,Hq", [(1, 32), (64, 32), (17, 8)])
+def test_runs_of_key_tiles_that_share_one_query_tile(dev, Tq, Hq):
+    # enough key tiles that an item takes several: the query tile and its LSE stay while keys pass; ragged lengths and
+    # streaming heads (most of whose key tiles no row sees) between them; against the same formula in torch, float64
+    B, Hkv, L, sink, window = 3, 8, 32768 + 77, 100, 300
+    lens = [L, 20000, 129]
+    Q, K = tokens((B, Tq, Hq, 128), seed=21).to(dev), tokens((B, L, Hkv, 128), seed=22).to(dev)
+    LSE = (torch.rand(B, Hq, Tq, generator=torch.Generator().manual_seed(23)) + 12).to(dev)
+    modes = [[(FULL, SSA)[(b + h) % 2] for h in range(Hkv)] for b in range(B)]
+    ws = ea.key_weights_workspace(B, Tq, L, Hq, Hkv, device=dev)
+    w = torch.full((B, Hkv, L), -1.0, device=dev)
+    ea.ea_key_weights(Q, K, LSE, torch.tensor(modes, dtype=torch.uint8, device=dev), sink=sink, window=window,
+                      seqlens=torch.tensor(lens, dtype=torch.int32, device=dev), weights=w, accumulate=False, workspace=ws)
+    check_no_device_error(ws)
+    g = Hq // Hkv
+    for b, n in enumerate(lens):
+        assert (w[b, :, n:] == -1).all()
+        t = torch.arange(max(0, Tq - n), Tq, device=dev)
+        i, j = (n - Tq + t)[:, None], torch.arange(n, device=dev)[None]
+        for h in range(Hkv):
+            keep = j <= i
+            if modes[b][h] == SSA:
+                keep = keep & ((j < sink) | (i - j < window))
+            want, tol = torch.zeros(n, dtype=torch.float64, device=dev), torch.zeros(n, dtype=torch.float64, device=dev)
+            for q in range(h * g, (h + 1) * g):
+                x = Q[b, t, q].double() @ K[b, :n, h].double().T * SCALE
+                d = 2.0 ** -16 * SCALE * (Q[b, t, q].double().abs() @ K[b, :n, h].double().abs().T) + 2.0 ** -21 * (x.abs() + 13)
+                p = torch.where(keep, torch.exp(x - LSE[b, q, t].double()[:, None]), 0.0)
+                want += p.sum(0)
+                tol += (p * torch.expm1(d)).sum(0) + 2.0 ** -13 * p.sum(0) + 1e-37
+            # (these LSE are not the rows' own: some sums lie above the largest float32, and are infinite there)
+            got = w[b, h, :n].double()
+            over = got.isinf() & (got > 0) & (want + tol > torch.finfo(torch.float32).max)
+            assert (((got - want).abs() <= tol) | over).all()
