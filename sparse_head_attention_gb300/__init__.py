@@ -734,33 +734,43 @@ def kv_cache_paged(num_pages, page_size, Hkv, block_table, *, dtype=torch.float8
     return _alloc_cache(num_pages, page_size, Hkv, dtype, scale_block, block_table.device, block_table)
 
 
-def _one_device(*tensors):
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) > 1:
-        raise ValueError("tensors on several devices: %s" % sorted(map(str, devs)))
+def _one_device(first, *tensors):
+    dev = first.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors on several devices: %s and %s" % (dev, t.device))
 
 
 class _at:
     """Runs a call on the device of its tensors and on the stream it names (the
     device's current one if none), allocations included."""
 
+    __slots__ = ("device", "ctx")
+
     def __init__(self, device, stream):
-        self.ctx = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(device))
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
-            self.ctx.append(torch.cuda.stream(stream))
+        self.device = device
+        self.ctx = None
+        if stream is not None and stream.device != device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        if stream is not None or device.index != torch._C._cuda_getDevice():
+            self.ctx = [torch.cuda.device(device)]
+            if stream is not None:
+                self.ctx.append(torch.cuda.stream(stream))
 
     def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if self.ctx:
+            for c in self.ctx:
+                c.__enter__()
+        # (torch.cuda.current_stream() takes several microseconds to make a Stream)
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+        if self.ctx:
+            for c in reversed(self.ctx):
+                c.__exit__(*exc)
+
+
+_I64 = {n: ctypes.c_int64 * n for n in (3, 4)}
 
 
 def _i32_vec(t, name, B):
@@ -806,7 +816,7 @@ def ea_cache_write(cache, K, V, start=None, n_new=None, *, workspace=None, strea
         if workspace is None:
             workspace = cache_workspace(cache.device)
         _check("ea_cache_write", lib().ea_cache_write(
-            cache._ref, K.data_ptr(), V.data_ptr(), _strides(K), _ptr(start), _ptr(n_new), B, T,
+            cache._ref, K.data_ptr(), V.data_ptr(), _I64[4](*K.stride()), _ptr(start), _ptr(n_new), B, T,
             workspace.data_ptr(), workspace.numel(), st))
 
 
@@ -861,7 +871,7 @@ def ea_hybrid_attn_decode_q8(q, cache, seqlens, m, *, sink, window, block_mask=N
             workspace = decode_q8_workspace(B, Hq, cache.Hkv, cache.capacity, num_splits,
                                             key_weights is not None, d, q.device)
         _check("ea_hybrid_attn_decode_q8", lib().ea_hybrid_attn_decode_q8(
-            q.data_ptr(), cache._ref, O.data_ptr(), _ptr(LSE), _strides(q), _strides(O),
+            q.data_ptr(), cache._ref, O.data_ptr(), _ptr(LSE), _I64[3](*q.stride()), _I64[3](*O.stride()),
             seqlens.data_ptr(), B, Hq, 1.0 / math.sqrt(d) if scale is None else float(scale),
             m.data_ptr(), int(sink), int(window), _ptr(bm), TILE, int(num_splits),
             _ptr(key_weights), 1 if accumulate else 0, workspace.data_ptr(), workspace.numel(), st))
@@ -911,7 +921,7 @@ def ea_key_weights(Q, K, LSE, m, *, sink, window, seqlens=None, block_mask=None,
         if workspace is None:
             workspace = key_weights_workspace(B, Tq, Lmax, Hq, Hkv, d, Q.device)
         _check("ea_key_weights", lib().ea_key_weights(
-            Q.data_ptr(), K.data_ptr(), LSE.data_ptr(), _strides(Q), _strides(K), _strides(LSE),
+            Q.data_ptr(), K.data_ptr(), LSE.data_ptr(), _I64[4](*Q.stride()), _I64[4](*K.stride()), _I64[3](*LSE.stride()),
             _ptr(seqlens), B, Tq, Lmax, Hq, Hkv, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
             m.data_ptr(), int(sink), int(window), _ptr(bm), TILE, weights.data_ptr(),
             1 if accumulate else 0, workspace.data_ptr(), workspace.numel(), st))
