@@ -548,6 +548,8 @@ ea_status ea_xa_estimate(const void *Q, const void *K, const int64_t q_str[4],
  *                max_pages * rows tokens
  *   scale_block  16, 32, 64 or 128 (ignored for EA_CACHE_BF16); pages hold a
  *                multiple of it
+ * Codes and scales are as the operators here write them (powers of two, 2^-64 at
+ * least; no NaN code of E4M3): ea_cache_write and ea_cache_compact rely on it.
  * Constraints: d == 128; K, V 16-byte aligned, the strides of the first three
  * dimensions multiples of 16 bytes, head-dim stride 1; a paged sequence's
  * capacity below 2^31.

@@ -9,10 +9,18 @@
 //                         threads hold a whole block in registers: one read
 //                         finds the block's largest value, sets the scale, and
 //                         the same registers are rounded and stored.
-//   cache_compact_kernel  the same over gathered rows of another cache.
-//   evict_select_kernel   a cluster of CTAs per (sequence, KV head): a radix
-//                         search for the lightest weight that stays, then one
-//                         ordered pass that lists the tokens.
+//   cache_compact_kernel  the same over gathered rows of another cache, K's and
+//                         V's block by one CTA (an index, a page and a row's
+//                         place serve both).  From 8 bits to 8 bits it is the
+//                         instructions that count: codes stay in f16 pairs (a
+//                         power of two per row is exact there), about 10 per
+//                         four codes instead of 50 in fp32.
+//   evict_select_kernel   a cluster of CTAs per (sequence, KV head): the weights
+//                         are read once into shared memory as ordered keys; a
+//                         radix search (three digits, histograms summed over
+//                         the cluster) finds the lightest that stays, and one
+//                         ordered pass lists the tokens.  Bound by latency: a
+//                         load, three cluster barriers, a few scans.
 #include <cuda_runtime.h>
 
 #include "ea_cache.cuh"
@@ -142,17 +150,16 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const WriteA
             if (!(was <= s)) {
                 s = isnan(s) ? s : was;      // larger, or NaN: it stays
             } else if (was < s) {
-                const float f = was / s;
+                const __half2 f = __float2half2_rn(was / s);   // below 1
 #pragma unroll
                 for (int i = 0; i < kPasses; ++i) {
                     const int k = i * kRowsPerPass + r;
                     if (p0 + k < lo) {
                         uint2 *w = reinterpret_cast<uint2 *>(dst + k * a.c.s_row);
-                        float u[4], v[4];
-                        decode4<kE4M3>(w->x, u);
-                        decode4<kE4M3>(w->y, v);
-                        *w = make_uint2(encode4<kE4M3>(u[0] * f, u[1] * f, u[2] * f, u[3] * f),
-                                        encode4<kE4M3>(v[0] * f, v[1] * f, v[2] * f, v[3] * f));
+                        uint32_t c[4];
+                        codes_f16<kE4M3>(w->x, c[0], c[1]);
+                        codes_f16<kE4M3>(w->y, c[2], c[3]);
+                        *w = make_uint2(encode4_f16<kE4M3>(c[0], c[1], f), encode4_f16<kE4M3>(c[2], c[3], f));
                     }
                 }
             }
@@ -186,73 +193,132 @@ struct CompactArgs {
     int keep;
 };
 
-// One row's eight elements of a cache, as stored.
+// A thread's 16 bytes of a row as stored: 8 bf16 or 16 codes.
 template <int FMT>
-struct Raw8 {
-    uint2 v;
-};
-template <>
-struct Raw8<EA_CACHE_BF16> {
-    uint4 v;
-};
+constexpr int kElems = FMT == EA_CACHE_BF16 ? 8 : 16;
 
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// Their largest magnitude as float bits, scale applied.
 template <int FMT>
-__device__ __forceinline__ void values8(const Raw8<FMT> &raw, float s, float (&x)[8])
+__device__ __forceinline__ uint32_t row_amax(const uint4 &raw, float s)
 {
     if constexpr (FMT == EA_CACHE_BF16) {
-        unpack8(raw.v, x);
+        float x[8];
+        unpack8(raw, x);
+        return amax8(x);
     } else {
-        float u[4], v[4];
-        decode4<FMT == EA_CACHE_E4M3>(raw.v.x, u);
-        decode4<FMT == EA_CACHE_E4M3>(raw.v.y, v);
+        __half2 m = __half2half2(__ushort_as_half(0));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            x[i] = u[i] * s;
-            x[4 + i] = v[i] * s;
+            uint32_t lo, hi;
+            codes_f16<FMT == EA_CACHE_E4M3>(word(raw, i), lo, hi);
+            m = __hmax2(m, amax4_f16(lo, hi));
         }
+        return __float_as_uint(__half2float(__hmax(__low2half(m), __high2half(m))) * s) & 0x7fffffffu;
     }
 }
 
+// Stores them as codes of a block of scale 1 / inv (zeros for a NaN scale).
+template <int SRC, bool E4M3>
+__device__ __forceinline__ void put_codes(uint8_t *dst, const uint4 &raw, float s, float inv, bool dead)
+{
+    if constexpr (SRC == EA_CACHE_BF16) {
+        float x[8];
+        unpack8(raw, x);
+        const uint2 w = make_uint2(encode4<E4M3>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                                   encode4<E4M3>(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+        *reinterpret_cast<uint2 *>(dst) = dead ? make_uint2(0u, 0u) : w;
+    } else {
+        // the ratio of the scales; it is at most qmax where a code is not 0
+        const __half2 f = __float2half2_rn(fminf(s * inv, 512.f));
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t lo, hi;
+            codes_f16<SRC == EA_CACHE_E4M3>(word(raw, i), lo, hi);
+            w[i] = dead ? 0u : encode4_f16<E4M3>(lo, hi, f);
+        }
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Stores them as bf16.
+template <int SRC>
+__device__ __forceinline__ void put_bf16(__nv_bfloat16 *dst, const uint4 &raw, float s)
+{
+    if constexpr (SRC == EA_CACHE_BF16) {
+        *reinterpret_cast<uint4 *>(dst) = raw;
+    } else {
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t c[2];
+            codes_f16<SRC == EA_CACHE_E4M3>(word(raw, i), c[0], c[1]);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 v = f16_f32(c[k]);
+                o[2 * i + k] = pack_bf16x2(v.x * s, v.y * s);
+            }
+        }
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+// Three dependent loads deep (index, page, data) with little work behind them, so
+// what counts is how many are in flight: the index is read before the count is
+// known, K's and V's rows together, and registers are kept low enough for many
+// CTAs.
 template <int SB, int SRC, int DST>
-__global__ void __launch_bounds__(kCacheThreads) cache_compact_kernel(const CompactArgs a)
+__global__ void __launch_bounds__(kCacheThreads, SB > 64 ? 3 : SRC == EA_CACHE_BF16 ? 5 : SB == 64 ? 6 : 10)
+    cache_compact_kernel(const CompactArgs a)
 {
     constexpr bool kE4M3 = DST == EA_CACHE_E4M3;
-    constexpr int kPasses = SB / kRowsPerPass;
+    constexpr int kRowThreads = EA_HEAD_DIM / kElems<SRC>, kRowsPerPass = kCacheThreads / kRowThreads;
+    constexpr int kPasses = SB / kRowsPerPass;         // 1 at least: 16 rows a pass
+    // K and V at once, unless that takes too many registers
+    constexpr int KV = SRC == EA_CACHE_BF16 ? 1 : 2;
     using Elem = typename std::conditional<SRC == EA_CACHE_BF16, uint16_t, uint8_t>::type;
-    __shared__ uint32_t red[4];
+    __shared__ uint32_t red[2][4];
     const int h = blockIdx.x % a.dst.Hkv, blk = blockIdx.x / a.dst.Hkv;
-    const int b = blockIdx.y, kv = blockIdx.z;
+    const int b = blockIdx.y, p0 = blk * SB;
+    const int r = threadIdx.x / kRowThreads, e0 = threadIdx.x % kRowThreads * kElems<SRC>;
+    const int64_t unit = static_cast<int64_t>(b) * a.dst.Hkv + h;
+    const int32_t *index = a.index + unit * a.keep;
+    int at[kPasses], so[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const int p = p0 + i * kRowsPerPass + r;
+        at[i] = p < a.keep ? __ldg(index + p) : -1;
+    }
     const int n = a.counts[b];
     if (n < 0 || n > a.keep) {
-        if (threadIdx.x == 0 && blockIdx.x == 0 && kv == 0)
+        if (threadIdx.x == 0 && blockIdx.x == 0)
             raise_error(a.err, EA_DEVERR_CHECK);
         return;
     }
-    const int p0 = blk * SB;
     if (p0 >= n)
         return;
     int outer, row0;
     if (!locate(a.dst, b, p0, outer, row0, a.err))
         return;
-    const int r = threadIdx.x / kRowThreads, e0 = threadIdx.x % kRowThreads * 8;
-    const int64_t unit = static_cast<int64_t>(b) * a.dst.Hkv + h;
-    const int32_t *index = a.index + unit * a.keep;
-    const Elem *src = static_cast<const Elem *>(a.src.code[kv]) + h * a.src.s_head + e0;
-
-    // rows of this thread: index, then page, then data, each step's loads together
-    int at[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
         const int p = p0 + i * kRowsPerPass + r;
-        at[i] = p < n ? __ldg(index + p) : -1;
-        if (p < n && (at[i] < 0 || at[i] >= a.src.cap)) {
-            raise_error(a.err, EA_DEVERR_CHECK);
+        if (p >= n) {
             at[i] = -1;
+        } else {
+            if (at[i] < 0 || at[i] >= a.src.cap) {
+                raise_error(a.err, EA_DEVERR_CHECK);
+                at[i] = -1;
+            }
+            if (a.w && e0 == 0)
+                a.w_out[unit * a.dst.cap + p] = at[i] >= 0 ? __ldg(a.w + unit * a.src.cap + at[i]) : 0.f;
         }
-    }
-    int so[kPasses];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
         so[i] = b;
         if (a.src.table && at[i] >= 0) {
             int row;
@@ -261,65 +327,60 @@ __global__ void __launch_bounds__(kCacheThreads) cache_compact_kernel(const Comp
             at[i] = row;
         }
     }
-    Raw8<SRC> raw[kPasses];
-    float sc[kPasses];
-    const float *ssrc = a.src.scale[kv];
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        raw[i] = Raw8<SRC>{};
-        sc[i] = 0.f;
-        if (at[i] >= 0) {
-            raw[i].v = __ldg(reinterpret_cast<const decltype(raw[i].v) *>(src + so[i] * a.src.s_outer +
-                                                                         at[i] * a.src.s_row));
-            if constexpr (SRC != EA_CACHE_BF16)
-                sc[i] = __ldg(ssrc + (static_cast<int64_t>(so[i]) * a.src.Hkv + h) * a.src.nsb +
-                              (at[i] >> a.src.log2sb));
-        }
-    }
+    const int64_t src0 = h * a.src.s_head + e0;
     const int64_t dst0 = outer * a.dst.s_outer + row0 * a.dst.s_row + h * a.dst.s_head + e0;
-    float x[8];
-    if constexpr (DST == EA_CACHE_BF16) {
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.dst.code[kv]) + dst0;
+    uint4 raw[KV][kPasses];
+    float sc[KV][kPasses];
+    auto load = [&](int kv, uint4 (&rw)[kPasses], float (&s)[kPasses]) {
+        const Elem *src = static_cast<const Elem *>(a.src.code[kv]) + src0;
+        const float *ssrc = a.src.scale[kv];
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
-            const int k = i * kRowsPerPass + r;
-            if (p0 + k < n) {
-                values8<SRC>(raw[i], sc[i], x);
-                *reinterpret_cast<uint4 *>(dst + k * a.dst.s_row) =
-                    make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+            rw[i] = make_uint4(0u, 0u, 0u, 0u);
+            s[i] = 1.f;
+            if (at[i] >= 0) {
+                rw[i] = __ldg(reinterpret_cast<const uint4 *>(src + so[i] * a.src.s_outer + at[i] * a.src.s_row));
+                if constexpr (SRC != EA_CACHE_BF16)
+                    s[i] = __ldg(ssrc + (static_cast<int64_t>(so[i]) * a.src.Hkv + h) * a.src.nsb +
+                                 (at[i] >> a.src.log2sb));
             }
         }
-    } else {
-        uint32_t mx = 0;
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            values8<SRC>(raw[i], sc[i], x);
-            mx = max(mx, amax8(x));
-        }
-        const float s = block_scale(cta_max(mx, red), kE4M3);
-        if (threadIdx.x == 0)
-            a.dst.scale[kv][(static_cast<int64_t>(outer) * a.dst.Hkv + h) * a.dst.nsb + row0 / SB] = s;
-        const bool dead = isnan(s);
-        const float inv = 1.f / s;
-        uint8_t *dst = static_cast<uint8_t *>(a.dst.code[kv]) + dst0;
-#pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-            const int k = i * kRowsPerPass + r;
-            if (p0 + k < n) {
-                values8<SRC>(raw[i], sc[i], x);
-                uint2 w = make_uint2(0u, 0u);
-                if (!dead)
-                    w = make_uint2(encode4<kE4M3>(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                                   encode4<kE4M3>(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
-                *reinterpret_cast<uint2 *>(dst + k * a.dst.s_row) = w;
-            }
-        }
+    };
+    if constexpr (KV == 2) {
+        load(0, raw[0], sc[0]);
+        load(1, raw[1], sc[1]);
     }
-    if (kv == 0 && a.w) {
-        for (int k = threadIdx.x; k < SB && p0 + k < n; k += kCacheThreads) {
-            const int i = index[p0 + k];
-            a.w_out[unit * a.dst.cap + p0 + k] = i >= 0 && i < a.src.cap ? a.w[unit * a.src.cap + i] : 0.f;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+        uint4 (&rw)[kPasses] = raw[kv % KV];
+        float (&s_row)[kPasses] = sc[kv % KV];
+        if constexpr (KV == 1)
+            load(kv, rw, s_row);
+        if constexpr (DST == EA_CACHE_BF16) {
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.dst.code[kv]) + dst0;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int k = i * kRowsPerPass + r;
+                if (p0 + k < n)
+                    put_bf16<SRC>(dst + k * a.dst.s_row, rw[i], s_row[i]);
+            }
+        } else {
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i)
+                mx = max(mx, row_amax<SRC>(rw[i], s_row[i]));
+            const float s = block_scale(cta_max(mx, red[kv]), kE4M3);
+            if (threadIdx.x == 0)
+                a.dst.scale[kv][(static_cast<int64_t>(outer) * a.dst.Hkv + h) * a.dst.nsb + row0 / SB] = s;
+            const bool dead = isnan(s);
+            const float inv = 1.f / s;                  // a power of two: exact
+            uint8_t *dst = static_cast<uint8_t *>(a.dst.code[kv]) + dst0;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int k = i * kRowsPerPass + r;
+                if (p0 + k < n)
+                    put_codes<SRC, kE4M3>(dst + k * a.dst.s_row, rw[i], s_row[i], inv, dead);
+            }
         }
     }
 }
@@ -329,6 +390,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelBits = 11;                 // digits: bits 31..21, 20..10, 9..0
 constexpr int kSelBins = 1 << kSelBits;
 constexpr int kSelMaxCluster = 8;
+constexpr int kSelMaxKeys = 50 * 1024;       // keys a CTA holds in shared memory at most
 
 struct SelectArgs {
     const float *w;
@@ -336,13 +398,16 @@ struct SelectArgs {
     int32_t *index, *new_seqlens;
     uint32_t *err;
     int Hkv, Lmax, keep, sink, recent;
+    int cap;                                 // keys a CTA holds in shared memory (a multiple of 4)
 };
 
 struct SelSmem {
     uint32_t hist[3][kSelBins];
     uint32_t warp[32];
     uint32_t digit, above;                   // result of one radix step
-    uint32_t n_above, n_equal;               // this CTA's tokens above / at the threshold
+    uint32_t before[3];                      // tokens above the step's digit in the CTAs before this one
+    uint32_t equal_before;                   // tokens at the threshold there
+    alignas(16) uint32_t keys[];             // [cap]
 };
 
 // Order-preserving bits of a weight: larger weight, larger key; -0 equals +0;
@@ -355,10 +420,10 @@ __device__ __forceinline__ uint32_t weight_key(float f)
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cl_addr)
+__device__ __forceinline__ uint2 ld_cluster_u32x2(uint32_t cl_addr)
 {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cl_addr) : "memory");
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cl_addr) : "memory");
     return v;
 }
 
@@ -391,7 +456,8 @@ __device__ __forceinline__ uint32_t cta_scan(uint32_t v, uint32_t *warp_sums, ui
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a)
 {
-    __shared__ SelSmem sm;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    SelSmem &sm = *reinterpret_cast<SelSmem *>(smem_raw);
     const int tid = threadIdx.x;
     const int C = gridDim.x, rank = blockIdx.x;        // one cluster spans the x dimension
     const int unit = blockIdx.y + gridDim.y * blockIdx.z;
@@ -416,34 +482,68 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
     }
     for (int i = tid; i < 3 * kSelBins; i += kSelThreads)
         (&sm.hist[0][0])[i] = 0u;
+    if (tid < 3)
+        sm.before[tid] = 0u;
+    if (tid == 3)
+        sm.equal_before = 0u;
     __syncthreads();
 
-    // this CTA's share of the middle tokens [sink, L - recent)
+    // this CTA's share of the middle tokens [sink, L - recent): lo + 0 .. lo + n - 1
     const float *w = a.w + static_cast<int64_t>(unit) * a.Lmax;
     const int m0 = a.sink, m1 = L - a.recent;
     const int len = (m1 - m0 + C - 1) / C;
-    const int lo = min(m0 + rank * len, m1), hi = min(lo + len, m1);
+    const int lo = min(m0 + rank * len, m1), n = min(lo + len, m1) - lo;
+    const int held = min(n, a.cap);                     // the rest (very long sequences) is read again
+    auto key_at = [&](int i) { return i < held ? sm.keys[i] : weight_key(__ldg(w + lo + i)); };
+    const uint32_t zero = weight_key(0.f);
+    uint32_t zeros = 0;
+#pragma unroll 8
+    for (int i = tid; i < n; i += kSelThreads) {
+        const uint32_t k = weight_key(__ldg(w + lo + i));
+        if (i < held)
+            sm.keys[i] = k;
+        // tokens that were never looked at are many: counted here, not one by one in their bin
+        if (k == zero)
+            ++zeros;
+        else
+            atomicAdd(&sm.hist[0][k >> 21], 1u);
+    }
+    zeros = __reduce_add_sync(0xffffffffu, zeros);
+    if ((tid & 31) == 0 && zeros)
+        atomicAdd(&sm.hist[0][zero >> 21], zeros);
+
     uint32_t want = a.keep - a.sink - a.recent;         // tokens of the middle that stay (< m1 - m0)
     uint32_t prefix = 0;                                // the threshold's digits found so far
 #pragma unroll 1
     for (int step = 0; step < 3; ++step) {
         const int shift = step == 0 ? 21 : step == 1 ? 10 : 0;
         const uint32_t mask = step == 2 ? 0x3ffu : 0x7ffu;
-        const int up = shift + (step == 2 ? 10 : 11);
+        if (step > 0) {
+            const int up = step == 1 ? 21 : 10;
 #pragma unroll 4
-        for (int i = lo + tid; i < hi; i += kSelThreads) {
-            const uint32_t k = weight_key(__ldg(w + i));
-            if (step == 0 || (k >> up) == prefix)
-                atomicAdd(&sm.hist[step][(k >> shift) & mask], 1u);
+            for (int i = tid; i < n; i += kSelThreads) {
+                const uint32_t k = key_at(i);
+                if ((k >> up) == prefix)
+                    atomicAdd(&sm.hist[step][(k >> shift) & mask], 1u);
+            }
         }
         cluster_sync_all();
-        // thread t sums bins from the top: 2047 - 2t and 2046 - 2t
-        uint32_t c0 = 0, c1 = 0;
+        // thread t sums two bins from the top, 2047 - 2t and 2046 - 2t, over the
+        // cluster, and over the CTAs before this one
+        uint32_t c0 = 0, c1 = 0, b0 = 0, b1 = 0;
         const int top = kSelBins - 1 - 2 * tid;
-        for (int r = 0; r < C; ++r) {
-            c0 += ld_cluster_u32(mapa_shared(smem_u32(&sm.hist[step][top]), r));
-            c1 += ld_cluster_u32(mapa_shared(smem_u32(&sm.hist[step][top - 1]), r));
-        }
+        const uint32_t bins = smem_u32(&sm.hist[step][top - 1]);
+#pragma unroll
+        for (int r = 0; r < kSelMaxCluster; ++r)
+            if (r < C) {
+                const uint2 v = ld_cluster_u32x2(mapa_shared(bins, r));
+                c1 += v.x;
+                c0 += v.y;
+                if (r < rank) {
+                    b1 += v.x;
+                    b0 += v.y;
+                }
+            }
         uint32_t total;
         const uint32_t incl = cta_scan(c0 + c1, sm.warp, total), excl = incl - c0 - c1;
         // the bin that holds the want-th largest (want 0: nothing of the middle stays)
@@ -457,59 +557,53 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
         __syncthreads();
         if (want == 0)
             break;                                       // the same in every CTA
-        prefix = step == 0 ? sm.digit : prefix << (step == 2 ? 10 : 11) | sm.digit;
+        const int digit = sm.digit;
         want -= sm.above;
+        prefix = step == 0 ? digit : prefix << (step == 2 ? 10 : 11) | digit;
+        const uint32_t above =
+            __reduce_add_sync(0xffffffffu, (top > digit ? b0 : 0u) + (top - 1 > digit ? b1 : 0u));
+        if ((tid & 31) == 0 && above)
+            atomicAdd(&sm.before[step], above);
+        if (step == 2 && (top == digit || top - 1 == digit))
+            sm.equal_before = top == digit ? b0 : b1;
         __syncthreads();
     }
     // tokens with a key above `prefix` stay, and the first `want` of those equal to it
     const bool none = a.keep == a.sink + a.recent;
     const uint32_t thr = none ? 0xffffffffu : prefix;    // no key reaches 0xffffffff
-    if (tid == 0)
-        sm.n_above = sm.n_equal = 0u;
-    __syncthreads();
-    uint32_t na = 0, ne = 0;
-#pragma unroll 4
-    for (int i = lo + tid; i < hi; i += kSelThreads) {
-        const uint32_t k = weight_key(__ldg(w + i));
-        na += k > thr;
-        ne += k == thr;
-    }
-    na = __reduce_add_sync(0xffffffffu, na);
-    ne = __reduce_add_sync(0xffffffffu, ne);
-    if ((tid & 31) == 0) {
-        atomicAdd(&sm.n_above, na);
-        atomicAdd(&sm.n_equal, ne);
-    }
-    cluster_sync_all();
-    uint32_t above = 0, equal = 0;                       // in the CTAs before this one
-    for (int r = 0; r < rank; ++r) {
-        above += ld_cluster_u32(mapa_shared(smem_u32(&sm.n_above), r));
-        equal += ld_cluster_u32(mapa_shared(smem_u32(&sm.n_equal), r));
-    }
     // ordered list: four consecutive tokens a thread
-    uint32_t pos = a.sink + above + min(equal, want);
-    for (int i0 = lo; i0 < hi; i0 += 4 * kSelThreads) {
+    uint32_t equal = none ? 0u : sm.equal_before;
+    uint32_t pos = a.sink + (none ? 0u : sm.before[0] + sm.before[1] + sm.before[2]) + min(equal, want);
+    for (int i0 = 0; i0 < n; i0 += 4 * kSelThreads) {
         uint32_t k[4], mine = 0;                         // tokens above << 16 | equal, of this thread
+        const int i4 = i0 + 4 * tid;
+        if (i4 + 4 <= held) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(&sm.keys[i4]);
+            k[0] = v.x;
+            k[1] = v.y;
+            k[2] = v.z;
+            k[3] = v.w;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = i0 + 4 * tid + j;
-            k[j] = i < hi ? weight_key(__ldg(w + i)) : 0u;
-            mine += i < hi ? (k[j] > thr ? 0x10000u : k[j] == thr ? 1u : 0u) : 0u;
+            for (int j = 0; j < 4; ++j)
+                k[j] = i4 + j < n ? key_at(i4 + j) : 0u;
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            mine += i4 + j < n ? (k[j] > thr ? 0x10000u : k[j] == thr ? 1u : 0u) : 0u;
         uint32_t total;
         const uint32_t before = cta_scan(mine, sm.warp, total) - mine;
         uint32_t eq = equal + (before & 0xffffu);        // equal ones before this thread's
         uint32_t at = pos + (before >> 16) + (min(eq, want) - min(equal, want));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int i = i0 + 4 * tid + j;
-            if (i >= hi)
+            if (i4 + j >= n)
                 break;
             bool stay = k[j] > thr;
             if (k[j] == thr)
                 stay = eq++ < want;
             if (stay)
-                out[at++] = i;
+                out[at++] = lo + i4 + j;
         }
         pos += (total >> 16) + (min(equal + (total & 0xffffu), want) - min(equal, want));
         equal += total & 0xffffu;
@@ -519,7 +613,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
         out[i] = i;
     for (int i = rank * kSelThreads + tid; i < a.recent; i += C * kSelThreads)
         out[a.keep - a.recent + i] = m1 + i;
-    cluster_sync_all();                                  // no CTA leaves while its counts may be read
+    cluster_sync_all();                                  // no CTA leaves while its histograms may be read
 }
 
 // ------------------------------------------------------------ launches
@@ -725,7 +819,7 @@ extern "C" ea_status ea_cache_compact(const ea_cache *src, const ea_cache *dst,
     a.w_out = weights_out;
     a.err = &static_cast<ea_ws_header *>(workspace)->error;
     a.keep = keep;
-    const dim3 grid(static_cast<unsigned>(blocks * a.dst.Hkv), static_cast<unsigned>(B), 2);
+    const dim3 grid(static_cast<unsigned>(blocks * a.dst.Hkv), static_cast<unsigned>(B));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (sb == 16)
         launch_compact<16>(a, grid, st);
@@ -772,6 +866,17 @@ extern "C" ea_status ea_evict_select(const float *weights, const int32_t *seqlen
     int C = 1;
     while (C < kSelMaxCluster && static_cast<int64_t>(B) * Hkv * C * 2 <= 2 * sms && Lmax / (2 * C) >= 2048)
         C *= 2;
+    const int share = static_cast<int>(ceil_div(Lmax, C) + 3) & ~3;
+    a.cap = share < kSelMaxKeys ? share : kSelMaxKeys;
+    const size_t smem = sizeof(SelSmem) + sizeof(uint32_t) * static_cast<size_t>(a.cap);
+    static bool attr_done[64] = {};   // the attribute is set once per device
+    if (dev >= 64 || !attr_done[dev]) {
+        if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(sizeof(SelSmem) + sizeof(uint32_t) * kSelMaxKeys)) != cudaSuccess)
+            return EA_ERR_CUDA;
+        if (dev < 64)
+            attr_done[dev] = true;
+    }
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -780,6 +885,7 @@ extern "C" ea_status ea_evict_select(const float *weights, const int32_t *seqlen
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(static_cast<unsigned>(C), static_cast<unsigned>(Hkv), static_cast<unsigned>(B));
     cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cfg.attrs = attr;
     cfg.numAttrs = 1;

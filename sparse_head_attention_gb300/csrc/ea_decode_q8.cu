@@ -114,30 +114,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Codes at bytes (0, 1) and (2, 3) of w as two f16 pairs; with PAIR_KEYS bytes
-// (0, 2) and (1, 3).  int8: c + 128 placed in the fraction of 1024, minus 1152.
-template <bool E4M3, bool PAIR_KEYS>
-__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
-{
-    if constexpr (E4M3) {
-        if constexpr (PAIR_KEYS)
-            w = __byte_perm(w, 0u, 0x3120);
-        asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-            : "=r"(lo), "=r"(hi)
-            : "r"(w));
-    } else {
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t a = __byte_perm(u, 0x64646464u, PAIR_KEYS ? 0x4240 : 0x4140);
-        const uint32_t b = __byte_perm(u, 0x64646464u, PAIR_KEYS ? 0x4341 : 0x4342);
-        const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-        const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
-        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
-        lo = *reinterpret_cast<const uint32_t *>(&x);
-        hi = *reinterpret_cast<const uint32_t *>(&y);
-    }
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
 {
     const __half2 v = __floats2half2_rn(lo, hi);
