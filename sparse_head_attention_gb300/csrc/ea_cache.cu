@@ -390,7 +390,7 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelBits = 11;                 // digits: bits 31..21, 20..10, 9..0
 constexpr int kSelBins = 1 << kSelBits;
 constexpr int kSelMaxCluster = 8;
-constexpr int kSelMaxKeys = 50 * 1024;       // keys a CTA holds in shared memory at most
+constexpr int kSelMaxKeys = 46 * 1024;       // keys a CTA holds in shared memory at most
 
 struct SelectArgs {
     const float *w;
@@ -398,17 +398,22 @@ struct SelectArgs {
     int32_t *index, *new_seqlens;
     uint32_t *err;
     int Hkv, Lmax, keep, sink, recent;
-    int cap;                                 // keys a CTA holds in shared memory (a multiple of 4)
+    int cap;                                 // keys a CTA holds in shared memory
 };
 
 struct SelSmem {
     uint32_t hist[3][kSelBins];
+    uint32_t coarse[3][kSelBins / 8];        // sums of eight bins each
     uint32_t warp[32];
     uint32_t digit, above;                   // result of one radix step
     uint32_t before[3];                      // tokens above the step's digit in the CTAs before this one
     uint32_t equal_before;                   // tokens at the threshold there
-    alignas(16) uint32_t keys[];             // [cap]
+    uint32_t keys[];                         // [sel_place(cap)]
 };
+
+// Where key i of a CTA lies: a word is left out after every sixteen, so that
+// threads that read runs of consecutive keys meet different banks.
+__host__ __device__ __forceinline__ int sel_place(int i) { return i + (i >> 4); }
 
 // Order-preserving bits of a weight: larger weight, larger key; -0 equals +0;
 // a NaN is below everything.
@@ -420,10 +425,10 @@ __device__ __forceinline__ uint32_t weight_key(float f)
     return (u >> 31) ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint2 ld_cluster_u32x2(uint32_t cl_addr)
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cl_addr)
 {
-    uint2 v;
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cl_addr) : "memory");
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cl_addr) : "memory");
     return v;
 }
 
@@ -494,14 +499,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
     const int len = (m1 - m0 + C - 1) / C;
     const int lo = min(m0 + rank * len, m1), n = min(lo + len, m1) - lo;
     const int held = min(n, a.cap);                     // the rest (very long sequences) is read again
-    auto key_at = [&](int i) { return i < held ? sm.keys[i] : weight_key(__ldg(w + lo + i)); };
+    auto key_at = [&](int i) { return i < held ? sm.keys[sel_place(i)] : weight_key(__ldg(w + lo + i)); };
     const uint32_t zero = weight_key(0.f);
     uint32_t zeros = 0;
 #pragma unroll 8
     for (int i = tid; i < n; i += kSelThreads) {
         const uint32_t k = weight_key(__ldg(w + lo + i));
         if (i < held)
-            sm.keys[i] = k;
+            sm.keys[sel_place(i)] = k;
         // tokens that were never looked at are many: counted here, not one by one in their bin
         if (k == zero)
             ++zeros;
@@ -520,90 +525,139 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
         const uint32_t mask = step == 2 ? 0x3ffu : 0x7ffu;
         if (step > 0) {
             const int up = step == 1 ? 21 : 10;
-#pragma unroll 4
-            for (int i = tid; i < n; i += kSelThreads) {
-                const uint32_t k = key_at(i);
+            auto count = [&](uint32_t k) {
                 if ((k >> up) == prefix)
                     atomicAdd(&sm.hist[step][(k >> shift) & mask], 1u);
-            }
+            };
+#pragma unroll 8
+            for (int i = tid; i < held; i += kSelThreads)
+                count(sm.keys[sel_place(i)]);
+            for (int i = held + tid; i < n; i += kSelThreads)
+                count(weight_key(__ldg(w + lo + i)));
+        }
+        // Sums over the cluster are of eight bins each first (reading all 2048 bins
+        // of eight CTAs took 4200 cycles a step), then of the eight that hold the
+        // want-th largest.
+        __syncthreads();
+        if (tid < kSelBins / 8) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(&sm.hist[step][8 * tid]);
+            const uint4 v = *reinterpret_cast<const uint4 *>(&sm.hist[step][8 * tid + 4]);
+            sm.coarse[step][tid] = u.x + u.y + u.z + u.w + v.x + v.y + v.z + v.w;
         }
         cluster_sync_all();
-        // thread t sums two bins from the top, 2047 - 2t and 2046 - 2t, over the
-        // cluster, and over the CTAs before this one
-        uint32_t c0 = 0, c1 = 0, b0 = 0, b1 = 0;
-        const int top = kSelBins - 1 - 2 * tid;
-        const uint32_t bins = smem_u32(&sm.hist[step][top - 1]);
+        if (tid < 256) {
+            // thread t: the coarse bin 255 - t, over the cluster and over the CTAs before this one
+            uint32_t c = 0, before = 0;
+            const uint32_t bin = smem_u32(&sm.coarse[step][255 - tid]);
 #pragma unroll
-        for (int r = 0; r < kSelMaxCluster; ++r)
-            if (r < C) {
-                const uint2 v = ld_cluster_u32x2(mapa_shared(bins, r));
-                c1 += v.x;
-                c0 += v.y;
-                if (r < rank) {
-                    b1 += v.x;
-                    b0 += v.y;
+            for (int r = 0; r < kSelMaxCluster; ++r)
+                if (r < C) {
+                    const uint32_t v = ld_cluster_u32(mapa_shared(bin, r));
+                    c += v;
+                    before += r < rank ? v : 0u;
+                }
+            uint32_t x = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if ((tid & 31) >= o)
+                    x += y;
+            }
+            if ((tid & 31) == 31)
+                sm.warp[tid >> 5] = x;
+            named_bar_sync(1, 256);
+            uint32_t excl = x - c;
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                excl += k < tid >> 5 ? sm.warp[k] : 0u;
+            if (want > excl && want <= excl + c) {
+                sm.digit = 255 - tid;
+                sm.above = excl;
+            }
+            named_bar_sync(1, 256);
+            const int coarse = sm.digit;
+            named_bar_sync(1, 256);                      // read before the fine one replaces it
+            if (want > 0 && 255 - tid > coarse && before)
+                atomicAdd(&sm.before[step], before);
+            // the eight bins, by the first warp: lane l takes bin 7 - l % 8 of CTAs l / 8 and l / 8 + 4
+            if (tid < 32 && want > 0) {
+                uint32_t all = 0, bef = 0;
+                const uint32_t fine = smem_u32(&sm.hist[step][8 * coarse + 7 - (tid & 7)]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int r = (tid >> 3) + 4 * k;
+                    if (r < C) {
+                        const uint32_t v = ld_cluster_u32(mapa_shared(fine, r));
+                        all += v;
+                        bef += r < rank ? v : 0u;
+                    }
+                }
+#pragma unroll
+                for (int o = 8; o < 32; o <<= 1) {
+                    all += __shfl_xor_sync(0xffffffffu, all, o);
+                    bef += __shfl_xor_sync(0xffffffffu, bef, o);
+                }
+                // lane l < 8: bins from the top
+                uint32_t up = all, bup = bef;
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, up, o);
+                    const uint32_t z = __shfl_up_sync(0xffffffffu, bup, o);
+                    if ((tid & 7) >= o) {
+                        up += y;
+                        bup += z;
+                    }
+                }
+                const uint32_t excl8 = sm.above + up - all;
+                __syncwarp();
+                if (tid < 8 && want > excl8 && want <= excl8 + all) {
+                    sm.digit = 8 * coarse + 7 - tid;
+                    sm.above = excl8;
+                    if (bup - bef)
+                        atomicAdd(&sm.before[step], bup - bef);
+                    if (step == 2)
+                        sm.equal_before = bef;
                 }
             }
-        uint32_t total;
-        const uint32_t incl = cta_scan(c0 + c1, sm.warp, total), excl = incl - c0 - c1;
-        // the bin that holds the want-th largest (want 0: nothing of the middle stays)
-        if (want > excl && want <= excl + c0) {
-            sm.digit = top;
-            sm.above = excl;
-        } else if (want > excl + c0 && want <= incl) {
-            sm.digit = top - 1;
-            sm.above = excl + c0;
         }
         __syncthreads();
         if (want == 0)
             break;                                       // the same in every CTA
-        const int digit = sm.digit;
         want -= sm.above;
-        prefix = step == 0 ? digit : prefix << (step == 2 ? 10 : 11) | digit;
-        const uint32_t above =
-            __reduce_add_sync(0xffffffffu, (top > digit ? b0 : 0u) + (top - 1 > digit ? b1 : 0u));
-        if ((tid & 31) == 0 && above)
-            atomicAdd(&sm.before[step], above);
-        if (step == 2 && (top == digit || top - 1 == digit))
-            sm.equal_before = top == digit ? b0 : b1;
-        __syncthreads();
+        prefix = step == 0 ? sm.digit : prefix << (step == 2 ? 10 : 11) | sm.digit;
     }
     // tokens with a key above `prefix` stay, and the first `want` of those equal to it
     const bool none = a.keep == a.sink + a.recent;
     const uint32_t thr = none ? 0xffffffffu : prefix;    // no key reaches 0xffffffff
-    // ordered list: four consecutive tokens a thread
+    // ordered list: each thread takes its run of consecutive tokens, up to 32 (one
+    // scan for up to 32K tokens of a CTA)
     uint32_t equal = none ? 0u : sm.equal_before;
     uint32_t pos = a.sink + (none ? 0u : sm.before[0] + sm.before[1] + sm.before[2]) + min(equal, want);
-    for (int i0 = 0; i0 < n; i0 += 4 * kSelThreads) {
-        uint32_t k[4], mine = 0;                         // tokens above << 16 | equal, of this thread
-        const int i4 = i0 + 4 * tid;
-        if (i4 + 4 <= held) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(&sm.keys[i4]);
-            k[0] = v.x;
-            k[1] = v.y;
-            k[2] = v.z;
-            k[3] = v.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                k[j] = i4 + j < n ? key_at(i4 + j) : 0u;
+    for (int i0 = 0; i0 < n; i0 += 32 * kSelThreads) {
+        const int per = min(32, (n - i0 + kSelThreads - 1) / kSelThreads);
+        const int f = min(i0 + tid * per, n), e = min(f + per, n);
+        uint32_t hi = 0, eqs = 0;                        // bit j: token f + j above / at the threshold
+#pragma unroll 8
+        for (int j = 0; j < e - f; ++j) {
+            const uint32_t k = key_at(f + j);
+            hi |= (k > thr ? 1u : 0u) << j;
+            eqs |= (k == thr ? 1u : 0u) << j;
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            mine += i4 + j < n ? (k[j] > thr ? 0x10000u : k[j] == thr ? 1u : 0u) : 0u;
         uint32_t total;
+        const uint32_t mine = __popc(hi) << 16 | __popc(eqs);
         const uint32_t before = cta_scan(mine, sm.warp, total) - mine;
-        uint32_t eq = equal + (before & 0xffffu);        // equal ones before this thread's
+        const uint32_t eq = equal + (before & 0xffffu);  // equal ones before this thread's
         uint32_t at = pos + (before >> 16) + (min(eq, want) - min(equal, want));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (i4 + j >= n)
-                break;
-            bool stay = k[j] > thr;
-            if (k[j] == thr)
-                stay = eq++ < want;
-            if (stay)
-                out[at++] = lo + i4 + j;
+        // of this thread's equal ones the first want - eq stay
+        uint32_t stay = hi, left = want > eq ? want - eq : 0u;
+        while (left > 0 && eqs) {
+            stay |= eqs & (0u - eqs);
+            eqs &= eqs - 1;
+            --left;
+        }
+        while (stay) {
+            out[at++] = lo + f + __ffs(stay) - 1;
+            stay &= stay - 1;
         }
         pos += (total >> 16) + (min(equal + (total & 0xffffu), want) - min(equal, want));
         equal += total & 0xffffu;
@@ -868,11 +922,11 @@ extern "C" ea_status ea_evict_select(const float *weights, const int32_t *seqlen
         C *= 2;
     const int share = static_cast<int>(ceil_div(Lmax, C) + 3) & ~3;
     a.cap = share < kSelMaxKeys ? share : kSelMaxKeys;
-    const size_t smem = sizeof(SelSmem) + sizeof(uint32_t) * static_cast<size_t>(a.cap);
+    const size_t smem = sizeof(SelSmem) + sizeof(uint32_t) * static_cast<size_t>(sel_place(a.cap));
     static bool attr_done[64] = {};   // the attribute is set once per device
     if (dev >= 64 || !attr_done[dev]) {
         if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(sizeof(SelSmem) + sizeof(uint32_t) * kSelMaxKeys)) != cudaSuccess)
+                                 static_cast<int>(sizeof(SelSmem) + sizeof(uint32_t) * sel_place(kSelMaxKeys))) != cudaSuccess)
             return EA_ERR_CUDA;
         if (dev < 64)
             attr_done[dev] = true;
