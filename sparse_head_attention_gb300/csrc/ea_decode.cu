@@ -642,6 +642,7 @@ static ea_status decode_launch(const void *q, const void *Kc, const void *Vc, vo
     a.num_sms = 0;   // set below
     a.chunk_min = EA_DECODE_AUTO_CHUNK;
     a.chunk_max = EA_DECODE_MAX_CHUNK;
+    a.max_chunks = static_cast<int64_t>(B) * Hkv * max_splits;
     a.block_mask = block_mask;
     a.nBm = static_cast<int>(nBm);
     a.blk_count = reinterpret_cast<int32_t *>(ws + L.blk_count);

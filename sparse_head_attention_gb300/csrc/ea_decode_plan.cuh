@@ -41,6 +41,8 @@ struct DecodeArgs {
     // launch and no queue
     int self_plan;
     int chunk_min, chunk_max;   // automatic chunk size (kept keys)
+    int few_chunks;             // a short step takes fewer chunks per SM (chunk_keys)
+    int64_t max_chunks;         // chunks that the workspace has room for
 };
 
 // Up to this many units a step is planned inside the split kernel.  Measured
@@ -186,6 +188,23 @@ static __global__ void __launch_bounds__(kBlkThreads) decode_blocks_kernel(Decod
         a.blk_count[u] = count;
 }
 
+// Kept keys per chunk when the split count is automatic: about four chunks per SM
+// over the step, between chunk_min and chunk_max keys.  With few_chunks a step of
+// fewer than 4096 (2048) keys per SM takes two (one) per SM, less one for every
+// unit (each rounds its chunks up), so that a short step is one even wave.
+__device__ __forceinline__ long long chunk_keys(const DecodeArgs &a, long long work)
+{
+    const long long sms = a.num_sms > 0 ? a.num_sms : 1;
+    long long target = 4 * sms;
+    if (a.few_chunks && work < 4096 * sms) {
+        const long long units = static_cast<long long>(a.B) * a.Hkv;
+        target = work < 2048 * sms ? sms : 2 * sms;
+        target -= units < target / 2 ? units : target / 2;
+    }
+    const long long chunk = (work + target - 1) / target;
+    return chunk < a.chunk_min ? a.chunk_min : (chunk > a.chunk_max ? a.chunk_max : chunk);
+}
+
 // One CTA: per-unit chunk counts, their prefix sum, and the chunk list.  The
 // automatic chunk size aims at about four chunks per SM over the whole step
 // (fewer, longer chunks mean fewer partial results to write and merge), between
@@ -224,9 +243,7 @@ static __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(Decode
 #pragma unroll
     for (int w = 0; w < kPlanThreads / 32; ++w)
         total_work += red_work[w];
-    const long long target = 4ll * (a.num_sms > 0 ? a.num_sms : 1);
-    long long chunk = (total_work + target - 1) / target;
-    chunk = chunk < a.chunk_min ? a.chunk_min : (chunk > a.chunk_max ? a.chunk_max : chunk);
+    const long long chunk = chunk_keys(a, total_work);
     int local = 0;
     for (int u = lo; u < hi; ++u) {
         const int work = a.unit_splits[u];
@@ -258,7 +275,7 @@ static __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(Decode
         const int ns = a.unit_splits[u];
         for (int sp = 0; sp < ns; ++sp)
             if (in_bounds(static_cast<int64_t>(run) + sp,
-                          static_cast<int64_t>(units) * a.max_splits, &a.hdr->error))
+                          a.max_chunks, &a.hdr->error))
                 a.chunks[run + sp] = (u << kSplitBits) | sp;
         run += ns;
     }
@@ -396,9 +413,7 @@ __device__ __forceinline__ void self_plan(const DecodeArgs &a, SelfPlan &plan, i
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    const long long target = 4ll * (a.num_sms > 0 ? a.num_sms : 1);
-    long long chunk = (mine + target - 1) / target;
-    chunk = chunk < a.chunk_min ? a.chunk_min : (chunk > a.chunk_max ? a.chunk_max : chunk);
+    const long long chunk = chunk_keys(a, mine);
     int ns[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 2; ++k)

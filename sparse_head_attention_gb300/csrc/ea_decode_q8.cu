@@ -534,8 +534,7 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 osum = fmaf(sm.red_o[w][hh][dd], f, osum);
             }
             const int64_t pidx = static_cast<int64_t>(c) * a.g + hh;
-            if (!in_bounds(pidx, static_cast<int64_t>(a.B) * a.Hkv * a.max_splits * a.g,
-                           &a.hdr->error))
+            if (!in_bounds(pidx, a.max_chunks * a.g, &a.hdr->error))
                 continue;
             const float Mb = (M == NEG_INF ? 0.f : M) - kQ8Shift;
             a.part_o[pidx * EA_HEAD_DIM + dd] = lsum == 0.f ? 0.f : osum / lsum;
@@ -564,8 +563,7 @@ __global__ void __launch_bounds__(kQ8MergeGroups * EA_HEAD_DIM, 2) decode_q8_mer
     const int u = b * a.Hkv + qh / a.g, hh = qh % a.g;
     const int first = a.unit_first[u];
     int ns = a.unit_splits[u];
-    if (!in_bounds(static_cast<int64_t>(first) + ns - 1,
-                   static_cast<int64_t>(a.B) * a.Hkv * a.max_splits, &a.hdr->error))
+    if (!in_bounds(static_cast<int64_t>(first) + ns - 1, a.max_chunks, &a.hdr->error))
         ns = 0;
     const int64_t base = static_cast<int64_t>(first) * a.g + hh;
     const int groups = blockDim.x / EA_HEAD_DIM;
@@ -672,36 +670,60 @@ __global__ void __launch_bounds__(kQ8WThreads) decode_q8_weights_kernel(const Q8
 }
 
 // ---------------------------------------------------------------- host
-// Keys per chunk when the split count is automatic (see decode_plan_kernel).
-constexpr int kQ8MinChunk = 2048;
+// Keys per chunk when the split count is automatic (see chunk_keys).  Measured on
+// one sequence of 32K with two full and six streaming heads: chunks of 2048 keys
+// 19.3 us, one chunk per SM 13.6.
+constexpr int kQ8MinChunk = 256;
 constexpr int kQ8MaxChunk = 8192;
+constexpr int kQ8Sms = 152;                  // the plan is for this GPU: a workspace's size depends on it
+constexpr int kQ8MaxSplits = 1024;
 
-static int q8_max_splits(int Lmax, int num_splits)
+// Chunks of a step at most: the caller's count per unit, or four per SM (or, in a
+// step too long for that, one per kQ8MaxChunk keys), one more for every unit's
+// remainder.
+static int64_t q8_max_chunks(int64_t units, int Lmax, int num_splits)
 {
     if (num_splits > 0)
-        return num_splits;
-    const int64_t s = ceil_div(Lmax, kQ8MinChunk);
-    return static_cast<int>(s < 1 ? 1 : (s > 1024 ? 1024 : s));
+        return units * num_splits;
+    const int64_t longest = ceil_div(Lmax, EA_TILE) * EA_TILE;     // whole tiles
+    const int64_t per_unit = ceil_div(longest, kQ8MinChunk) < kQ8MaxSplits ? ceil_div(longest, kQ8MinChunk)
+                                                                          : kQ8MaxSplits;
+    const int64_t n = 4 * kQ8Sms + units + units * ceil_div(longest, kQ8MaxChunk);
+    return n < units * per_unit ? n : units * per_unit;
 }
 
 struct Q8Ws {
     DecodeWs d;
     size_t lse2, scores, total;
+    int64_t max_chunks;
     int gp;
 };
 
 static Q8Ws q8_ws_layout(int B, int Hq, int Hkv, int Lmax, int num_splits, bool weights)
 {
     Q8Ws w{};
-    w.d = decode_ws_layout(B, Hq, Hkv, q8_max_splits(Lmax, num_splits), Lmax);
+    const size_t units = static_cast<size_t>(B) * Hkv;
     const int g = Hq / Hkv;
+    w.max_chunks = q8_max_chunks(static_cast<int64_t>(units), Lmax, num_splits);
+    const size_t chunks = static_cast<size_t>(w.max_chunks);
+    size_t off = sizeof(ea_ws_header);
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align_up(off + bytes, 256);
+        return at;
+    };
+    w.d.unit_first = take(sizeof(int32_t) * units);
+    w.d.unit_splits = take(sizeof(int32_t) * units);
+    w.d.chunks = take(sizeof(int32_t) * chunks);
+    w.d.partial_o = take(sizeof(float) * chunks * g * EA_HEAD_DIM);
+    w.d.partial_lse = take(sizeof(float) * chunks * g);
+    w.d.blk_count = take(sizeof(int32_t) * units);
+    w.d.blk_list = take(sizeof(uint16_t) * units * static_cast<size_t>(ceil_div(Lmax, EA_TILE)));
     w.gp = g == 1 ? 1 : g == 2 ? 2 : g <= 4 ? 4 : g <= 6 ? 6 : 8;
-    size_t off = w.d.total;
-    w.lse2 = off;
-    off = align_up(off + sizeof(float) * static_cast<size_t>(B) * Hq, 256);
+    w.lse2 = take(sizeof(float) * static_cast<size_t>(B) * Hq);
     w.scores = off;
     if (weights)
-        off = align_up(off + sizeof(float) * static_cast<size_t>(B) * Hkv * Lmax * w.gp, 256);
+        take(sizeof(float) * units * Lmax * w.gp);
     w.total = off;
     return w;
 }
@@ -790,9 +812,8 @@ extern "C" ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cac
         return EA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(O)) & 15u)
         return EA_ERR_INVALID_ARG;
-    const int max_splits = q8_max_splits(Lmax, num_splits);
     if (static_cast<int64_t>(B) * Hkv >= (int64_t(1) << (31 - kSplitBits)) ||
-        static_cast<int64_t>(B) * Hkv * max_splits >= (int64_t(1) << 31) ||
+        q8_max_chunks(static_cast<int64_t>(B) * Hkv, Lmax, num_splits) >= (int64_t(1) << 31) ||
         (key_weights && static_cast<int64_t>(B) * Hkv > 65535))
         return EA_ERR_UNSUPPORTED;
     const Q8Ws L = q8_ws_layout(B, Hq, Hkv, Lmax, num_splits, key_weights != nullptr);
@@ -829,7 +850,10 @@ extern "C" ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cac
     a.d.sink = sink < Lmax ? sink : Lmax;
     a.d.window = window < Lmax ? window : Lmax;
     a.d.num_splits = num_splits;
-    a.d.max_splits = max_splits;
+    a.d.max_splits = num_splits > 0 ? num_splits : kQ8MaxSplits;
+    a.d.max_chunks = L.max_chunks;
+    a.d.few_chunks = 1;
+    a.d.num_sms = kQ8Sms;
     a.d.scale_log2 = scale * 1.4426950408889634f;
     a.d.block_mask = block_mask;
     a.d.nBm = static_cast<int>(nBm);
@@ -860,9 +884,8 @@ extern "C" ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cac
     const int sms = num_sms(dev);
     if (sms <= 0)
         return EA_ERR_CUDA;
-    a.d.num_sms = sms;
     const int64_t units = static_cast<int64_t>(B) * Hkv;
-    const int grid = static_cast<int>(units * max_splits < sms ? units * max_splits : sms);
+    const int grid = static_cast<int>(L.max_chunks < sms ? L.max_chunks : sms);
     a.d.self_plan = units <= kSelfPlanUnits ? 1 : 0;
     if (block_mask)
         decode_blocks_kernel<<<static_cast<unsigned>(units), kBlkThreads, 0, st>>>(a.d);
