@@ -10,7 +10,7 @@
 // key and the sum over queries is a sum over the columns it reads: no reduction
 // across threads, no atomics, one order of summation.  Roles:
 //   warp 0     TMA: key tiles and query tiles
-//   warp 1     the MMAs, into two 256-column TMEM buffers (few rows: and warp 3)
+//   warp 1     the MMAs, into two 256-column TMEM buffers
 //   warp 2     the rows' LSE as a ninth k-step of the product: -LSE / scale in three
 //              bf16 parts (24 bits) in a query's row, against ones in a key's
 //   warps 4-19 four warpgroups, two to a buffer: each reads half of its columns
@@ -22,20 +22,21 @@
 // A query tile holds 128 rows of two heads (256 rows of one where the group is
 // one head), or fewer rows of more heads, each padded to a multiple of 16.
 //
-// Many rows (more than one query tile per key tile): an item is 256 keys, whose
-// two key tiles stay in shared memory, one per TMEM buffer, while query tiles
-// stream past both in halves of 64 dims (4 stages of 32 KB).  Two key tiles, so
-// that a query tile's 64 KB from L2 feed 2048 cycles of MMAs; with one, the MMAs
-// waited for them (2 stages of 64 KB: 1073 us for 16K x 16K and 32 heads).  256
-// columns, because with 128 the operands' reads from shared memory pace the
-// MMA (48 % of its cycles busy for 31 % of its rate).  Bound by the tensor core
-// (2^22 multiply-adds, 1024 cycles, per 128 x 256 tile) and as much by the SFUs
-// (32768 exponentials at 32 a cycle).
+// Key tiles go in pairs, one per TMEM buffer, so that a query tile's 64 KB from L2
+// feed 2048 cycles of MMAs and the sums over one buffer run under the MMAs into
+// the other.  256 columns, because with 128 the operands' reads from shared
+// memory pace the MMA (48 % of its cycles busy for 31 % of its rate).
 //
-// Few rows (a decode step, an observation window): one query tile serves all key
-// tiles of an item and stays in shared memory; key tiles pass through 4 stages of
-// 32 KB (2 were too few for HBM's latency: 3750 cycles a tile) and the two buffers
-// in turn.  Bound by reading K.
+// Many rows (more than one query tile per pair): an item is one pair, which stays
+// in shared memory while query tiles stream past it in halves of 64 dims (4 stages
+// of 32 KB).  Bound by the tensor core (2^22 multiply-adds, 1024 cycles, per 128 x
+// 256 tile) and as much by the SFUs (32768 exponentials at 32 a cycle); the chain
+// MMA - barrier - sums - barrier over two buffers leaves each at 55 - 60 %.
+//
+// Few rows (a decode step, an observation window): one query tile serves all pairs
+// of an item and stays in shared memory; pairs pass through two stages of 64 KB.
+// Bound by reading K, and by the roles' own code (at one warp's pace between the
+// sums' instructions).
 //
 // With few key tiles the queries of each are cut into `parts` shares, whose sums
 // go to the workspace and are added in order by a last kernel.
@@ -52,8 +53,9 @@ constexpr int kWCols = 256;                       // query columns per tile
 constexpr int kWKHalf = kWTile * 128;             // 64 dims of 128 keys: 16 KB
 constexpr int kWQHalf = kWCols * 128;             // 64 dims of 256 rows: 32 KB
 static_assert(2 * kWKHalf == kWQHalf, "a key tile is as large as half a query tile");
-constexpr int kWStages = 4;                       // many rows: halves of query tiles (32 KB);
-                                                  // few rows: key tiles (32 KB)
+constexpr int kWStages = 4;                       // of 32 KB: many rows, halves of query tiles;
+                                                  // few rows, key tiles (two stages of a pair)
+constexpr int kWKeys = 2 * kWTile;                // keys of a pair
 constexpr int kWXBytes = 32;                      // 16 bf16 of one row of the LSE k-step
 constexpr int kWBufs = 2;                         // TMEM and LSE buffers
 constexpr int kWGroups = 4;                       // warpgroups, two to a buffer
@@ -63,8 +65,8 @@ constexpr int kWSlots = 4;                        // items handed on, and key ti
 constexpr uint32_t kWTmemCols = kWBufs * kWCols;
 constexpr int kWMaxParts = 64;
 
-// An item: key tiles (many rows: pairs of them) [kt0, kt1) of one (sequence, KV
-// head) and one share of their queries.
+// An item: pairs of key tiles [kt0, kt1) of one (sequence, KV head) and one share
+// of their queries.
 struct KwItem {
     int valid;             // 0: none left
     int b, h, part, kt0, kt1;
@@ -77,14 +79,14 @@ struct __align__(1024) KwSmem {
     uint8_t ring[kWStages][kWQHalf];
     uint8_t qx[kWBufs][kWXBytes * kWCols];        // the LSE k-step: query rows
     uint8_t kx[kWXBytes * kWTile];                // and key rows (ones)
-    float red[kWSlots][kWGroups][kWTile];
+    float red[kWBufs][kWSlots][kWTile];
     uint64_t k_full[kWStages], k_empty[kWStages];
     uint64_t q_full[kWStages], q_empty[kWStages];
     uint64_t s_full[kWBufs], s_free[kWBufs];
     uint64_t lse_full[kWBufs], lse_empty[kWBufs];
-    uint64_t red_full[kWSlots], red_empty[kWSlots];
+    uint64_t red_full[kWBufs][kWSlots], red_empty[kWBufs][kWSlots];
     uint64_t item_full[kWSlots], item_empty[kWSlots];
-    uint64_t drain[2];
+    uint64_t drain;
     KwItem item[kWSlots];
     uint32_t tmem_base;
     int abort;
@@ -107,16 +109,8 @@ struct KwArgs {
     float inv_scale;
 };
 
-// Keys that share the query tiles.
-template <bool MANY>
-__host__ __device__ constexpr int kw_keys()
-{
-    return MANY ? 2 * kWTile : kWTile;
-}
-
-// Items: runs of key tiles outermost (the first ones are seen by the most
+// Items: runs of pairs outermost (the first ones are seen by the most
 // queries), then share, sequence, head.  False: the sequence has no such tile.
-template <bool MANY>
 __device__ __forceinline__ bool kw_item(const KwArgs &a, int item, KwItem &x)
 {
     const int units = a.B * a.Hkv;
@@ -128,24 +122,23 @@ __device__ __forceinline__ bool kw_item(const KwArgs &a, int item, KwItem &x)
     x.L = a.seqlens ? a.seqlens[x.b] : a.Lmax;
     if (x.L < 0 || x.L > a.Lmax)
         x.L = 0;
-    x.kt1 = min(x.kt0 + a.run, (x.L + kw_keys<MANY>() - 1) / kw_keys<MANY>());
+    x.kt1 = min(x.kt0 + a.run, (x.L + kWKeys - 1) / kWKeys);
     x.off = x.L - a.Tq;
     x.mode = a.m[u];
     x.valid = 1;
     return x.kt0 < x.kt1;
 }
 
-// The queries of one key tile that an item takes.
+// The queries of one pair that an item takes.
 struct KwRange {
-    int ta, te;            // query rows that see the tile (not EA_BLOCK: te)
+    int ta, te;            // query rows that see the pair (not EA_BLOCK: te)
     int s0, s1;            // this share's segments: a.seg rows from ta on, or (EA_BLOCK) query blocks
 };
 
-template <bool MANY>
 __device__ __forceinline__ KwRange kw_range(const KwArgs &a, const KwItem &x, int kt)
 {
     KwRange r;
-    const int k0 = kt * kw_keys<MANY>();
+    const int k0 = kt * kWKeys;
     r.ta = max(0, k0 - x.off);
     r.te = a.Tq;
     int n, first = 0;
@@ -154,7 +147,7 @@ __device__ __forceinline__ KwRange kw_range(const KwArgs &a, const KwItem &x, in
         n = a.block_mask ? (x.L - 1) / kWTile + 1 - first : 0;
     } else {
         if (x.mode == EA_SSA && k0 >= a.sink)                // the last key's window ends the rows
-            r.te = min(a.Tq, k0 + kw_keys<MANY>() - 1 + a.window - x.off);
+            r.te = min(a.Tq, k0 + kWKeys - 1 + a.window - x.off);
         n = x.mode > EA_BLOCK || r.te <= r.ta ? 0 : (r.te - r.ta + a.seg - 1) >> a.seg_log2;
     }
     r.s0 = first;
@@ -180,9 +173,9 @@ __device__ __forceinline__ int kw_heads(int nr)
     return static_cast<int>((0x1112347Full >> (nr / 4 - 4)) & 15u) + 1;
 }
 
-// Calls f(tile) for every column tile of a key tile, in order, until f returns
+// Calls f(tile) for every column tile of a pair, in order, until f returns
 // false; a whole warp calls it.
-template <bool MANY, class F>
+template <class F>
 __device__ __forceinline__ bool kw_tiles(const KwArgs &a, const KwItem &x, const KwRange &rg, int kt,
                                          int lane, F f)
 {
@@ -190,11 +183,11 @@ __device__ __forceinline__ bool kw_tiles(const KwArgs &a, const KwItem &x, const
         uint32_t bits = rg.s1 - s >= 32 ? 0xffffffffu : (1u << (rg.s1 - s)) - 1u;
         uint32_t bits0 = bits, bits1 = bits;
         if (x.mode == EA_BLOCK) {
-            const int qb = s + lane, kb = MANY ? 2 * kt : kt;
+            const int qb = s + lane, kb = 2 * kt;
             const uint8_t *row = a.block_mask +
                                  ((static_cast<int64_t>(x.b) * a.Hkv + x.h) * a.nB + qb) * a.nB + kb;
             bits0 = __ballot_sync(0xffffffffu, qb < rg.s1 && row[0] != 0);
-            bits1 = MANY ? __ballot_sync(0xffffffffu, qb < rg.s1 && kb + 1 < a.nB && row[1] != 0) : 0u;
+            bits1 = __ballot_sync(0xffffffffu, qb < rg.s1 && kb + 1 < a.nB && row[1] != 0);
             bits = bits0 | bits1;
         }
         while (bits) {
@@ -310,7 +303,7 @@ template <bool MANY>
 __device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const KwMaps &tm_q, const KwArgs &a, KwSmem &sm, int lane)
 {
     uint32_t *err = &a.hdr->error;
-    constexpr int KS = MANY ? 1 : kWStages, QS = MANY ? kWStages : 1;
+    constexpr int KS = MANY ? 1 : kWStages / 2, QS = MANY ? kWStages : 1;
     KwRing<KS> k;
     KwRing<QS> q;
     KwHeld held{};
@@ -327,7 +320,7 @@ __device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const KwMap
             if (v >= static_cast<uint32_t>(a.n_items))
                 break;
             next = draw();
-            if (kw_item<MANY>(a, static_cast<int>(v), x))
+            if (kw_item(a, static_cast<int>(v), x))
                 break;
         }
         if (!mbar_wait_warp(&sm.item_empty[slot], ((it / kWSlots) & 1) ^ 1, &sm.abort, err))
@@ -340,7 +333,7 @@ __device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const KwMap
         if (!x.valid)
             break;
         for (int kt = x.kt0; ok && kt < x.kt1; ++kt) {
-            const KwRange rg = kw_range<MANY>(a, x, kt);
+            const KwRange rg = kw_range(a, x, kt);
             if (rg.s0 >= rg.s1)
                 continue;
             if (!mbar_wait_warp(&sm.k_empty[k.s], k.phase ^ 1, &sm.abort, err)) {
@@ -348,19 +341,18 @@ __device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const KwMap
                 break;
             }
             if (lane == 0) {
-                constexpr int tiles = MANY ? 2 : 1;
-                mbar_arrive_expect_tx(&sm.k_full[k.s], tiles * 2 * kWKHalf);
+                mbar_arrive_expect_tx(&sm.k_full[k.s], 4 * kWKHalf);
 #pragma unroll
-                for (int p = 0; p < tiles; ++p) {
-                    uint8_t *dst = MANY ? sm.held + p * 2 * kWKHalf : sm.ring[k.s];
-                    const int row = (kt * tiles + p) * kWTile;
+                for (int p = 0; p < 2; ++p) {
+                    uint8_t *dst = MANY ? sm.held + p * 2 * kWKHalf : sm.ring[2 * k.s + p];
+                    const int row = kt * kWKeys + p * kWTile;
                     tma_load_4d(dst, tm_k, 0, x.h, row, x.b, &sm.k_full[k.s]);
                     tma_load_4d(dst + kWKHalf, tm_k, 64, x.h, row, x.b, &sm.k_full[k.s]);
                 }
             }
             __syncwarp();
             k.next();
-            ok = kw_tiles<MANY>(a, x, rg, kt, lane, [&](const KwTile &t) {
+            ok = kw_tiles(a, x, rg, kt, lane, [&](const KwTile &t) {
                 const int head = x.h * a.g + t.head0;
                 if constexpr (MANY) {
 #pragma unroll
@@ -414,30 +406,27 @@ __device__ __forceinline__ uint8_t *kw_row_x(uint8_t *base, int row)
     return base + (row >> 3) * 256 + (row & 7) * 16;
 }
 
-// Few rows: two warps, one per TMEM buffer, take every other query tile, so that
-// one does its waits and descriptors (about 1000 cycles a tile) while the other's
-// MMAs run.  Many rows: one warp (p = 0) for both key tiles of the pair, one after
-// the other, so that the first one's sums run under the second one's MMAs.
-// (Alternating between them every 64 dims ended both together and left MMAs and
-// exponentials to take turns: 1091 us for 16K x 16K and 32 heads against 890; a
-// warp each, in turns by a token: 945.)
+// The MMAs of both key tiles of a pair, one after the other, so that the first
+// one's sums run under the second one's MMAs.  (Alternating between them every 64
+// dims ended both together and left MMAs and exponentials to take turns: 1091 us
+// for 16K x 16K and 32 heads against 850; a warp each, in turns by a token: 945.)
 template <bool MANY>
-__device__ __forceinline__ void kw_mma(const KwArgs &a, KwSmem &sm, uint32_t tmem, int lane, int p)
+__device__ __forceinline__ void kw_mma(const KwArgs &a, KwSmem &sm, uint32_t tmem, int lane)
 {
     uint32_t *err = &a.hdr->error;
-    constexpr int KS = MANY ? 1 : kWStages, QS = MANY ? kWStages : 1;
+    constexpr int KS = MANY ? 1 : kWStages / 2, QS = MANY ? kWStages : 1;
     KwRing<KS> k;
     KwRing<QS> q;
-    uint32_t n = 0, uses = 0;                                // column tiles, and those of this warp
+    uint32_t n = 0;                                          // column tiles
     const uint32_t ring = smem_u32(sm.ring[0]), held_addr = smem_u32(sm.held);
     const uint64_t kx = kw_sdesc_x(smem_u32(sm.kx));
     KwHeld held{};
     bool ok = true;
     KwItem x;
     // the nine MMAs of a tile: 2 x 64 dims and the LSE
-    auto mma = [&](uint32_t d, uint32_t ka, uint32_t qa0, uint32_t qa1, uint32_t qx, uint32_t idesc) {
+    auto mma = [&](uint32_t d, uint32_t ka, uint32_t qa, uint32_t qx, uint32_t idesc) {
         const uint64_t k0 = sdesc_sw128(ka, 16, 1024), k1 = sdesc_sw128(ka + kWKHalf, 16, 1024);
-        const uint64_t q0 = sdesc_sw128(qa0, 16, 1024), q1 = sdesc_sw128(qa1, 16, 1024);
+        const uint64_t q0 = sdesc_sw128(qa, 16, 1024), q1 = sdesc_sw128(qa + kWQHalf, 16, 1024);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             tc_mma(d, k0 + 2 * i, q0 + 2 * i, idesc, i == 0 ? 0u : 1u);
@@ -448,67 +437,57 @@ __device__ __forceinline__ void kw_mma(const KwArgs &a, KwSmem &sm, uint32_t tme
     };
     for (int it = 0; ok && kw_take(a, sm, it, x) > 0; ++it) {
         for (int kt = x.kt0; ok && kt < x.kt1; ++kt) {
-            const KwRange rg = kw_range<MANY>(a, x, kt);
+            const KwRange rg = kw_range(a, x, kt);
             if (rg.s0 >= rg.s1)
                 continue;
             ok = mbar_wait_warp(&sm.k_full[k.s], k.phase, &sm.abort, err);
             if (!ok)
                 break;
-            const uint32_t kaddr = MANY ? held_addr : ring + k.s * kWQHalf;
-            ok = kw_tiles<MANY>(a, x, rg, kt, lane, [&](const KwTile &t) {
+            const uint32_t kaddr = MANY ? held_addr : ring + k.s * 2 * kWQHalf;
+            ok = kw_tiles(a, x, rg, kt, lane, [&](const KwTile &t) {
                 const uint32_t idesc = idesc_bf16_f32(kWTile, t.nh * t.nr, false, false);
                 const uint32_t mine = n++;
+                const int lb = mine % kWBufs;
+                const uint32_t qa = MANY ? ring + q.s * kWQHalf : held_addr, qx = smem_u32(sm.qx[lb]);
                 if constexpr (MANY) {
-                    const int lb = mine % kWBufs;
-                    const uint32_t q0 = ring + q.s * kWQHalf, qx = smem_u32(sm.qx[lb]);
-                    if (!mbar_wait_warp(&sm.lse_full[lb], (mine / kWBufs) & 1, &sm.abort, err) ||
-                        !mbar_wait_warp(&sm.q_full[q.s], q.phase, &sm.abort, err) ||
+                    if (!mbar_wait_warp(&sm.q_full[q.s], q.phase, &sm.abort, err) ||
                         !mbar_wait_warp(&sm.q_full[q.s + 1], q.phase, &sm.abort, err))
                         return false;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        if (!mbar_wait_warp(&sm.s_free[b], (mine & 1) ^ 1, &sm.abort, err))
-                            return false;
-                        tc_fence_after();
-                        if (lane == 0) {
-                            mma(tmem + b * kWCols, kaddr + b * 2 * kWKHalf, q0, q0 + kWQHalf, qx, idesc);
-                            tc_commit(&sm.s_full[b]);
-                            if (b == 1) {
-                                tc_commit(&sm.q_empty[q.s]);
-                                tc_commit(&sm.q_empty[q.s + 1]);
-                                tc_commit(&sm.lse_empty[lb]);
-                            }
-                        }
+                } else if (!held.same(x, t)) {
+                    // the tile before it is done with once the MMAs so far are
+                    if (held.n > 0) {
+                        if (lane == 0)
+                            tc_commit(&sm.q_empty[0]);
                         __syncwarp();
+                        q.next();
                     }
-                    q.next();
-                    q.next();                            // two halves: q.s is 0 or 2
-                } else {
-                    if (!held.same(x, t)) {
-                        // the tile before it is done with once this warp's MMAs so far are
-                        if (held.n > 0) {
-                            if (lane == 0)
-                                tc_commit(&sm.q_empty[q.s]);
-                            __syncwarp();
-                            q.next();
-                        }
-                        if (!mbar_wait_warp(&sm.q_full[q.s], q.phase, &sm.abort, err))
-                            return false;
-                        ++held.n;
-                    }
-                    if (static_cast<int>(mine % kWBufs) != p)
-                        return true;
-                    if (!mbar_wait_warp(&sm.lse_full[p], uses & 1, &sm.abort, err) ||
-                        !mbar_wait_warp(&sm.s_free[p], (uses & 1) ^ 1, &sm.abort, err))
+                    if (!mbar_wait_warp(&sm.q_full[0], q.phase, &sm.abort, err))
                         return false;
-                    ++uses;
+                    ++held.n;
+                }
+                if (!mbar_wait_warp(&sm.lse_full[lb], (mine / kWBufs) & 1, &sm.abort, err))
+                    return false;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    if (!mbar_wait_warp(&sm.s_free[b], (mine & 1) ^ 1, &sm.abort, err))
+                        return false;
                     tc_fence_after();
                     if (lane == 0) {
-                        mma(tmem + p * kWCols, kaddr, held_addr, held_addr + kWQHalf, smem_u32(sm.qx[p]), idesc);
-                        tc_commit(&sm.s_full[p]);
-                        tc_commit(&sm.lse_empty[p]);
+                        mma(tmem + b * kWCols, kaddr + b * 2 * kWKHalf, qa, qx, idesc);
+                        tc_commit(&sm.s_full[b]);
+                        if (b == 1) {
+                            if constexpr (MANY) {
+                                tc_commit(&sm.q_empty[q.s]);
+                                tc_commit(&sm.q_empty[q.s + 1]);
+                            }
+                            tc_commit(&sm.lse_empty[lb]);
+                        }
                     }
                     __syncwarp();
+                }
+                if constexpr (MANY) {
+                    q.next();
+                    q.next();                            // two halves: q.s is 0 or 2
                 }
                 return true;
             });
@@ -520,13 +499,13 @@ __device__ __forceinline__ void kw_mma(const KwArgs &a, KwSmem &sm, uint32_t tme
     }
     // Before leaving on an abort, let the MMAs already issued finish (their
     // operands and accumulators go with the CTA): a commit on a barrier of their
-    // own covers all of this warp's.
+    // own covers them.
     if (__any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort)) && n > 0) {
         volatile int no_abort = 0;
         if (lane == 0)
-            tc_commit(&sm.drain[p]);
+            tc_commit(&sm.drain);
         __syncwarp();
-        mbar_wait_warp(&sm.drain[p], 0, &no_abort, nullptr);
+        mbar_wait_warp(&sm.drain, 0, &no_abort, nullptr);
     }
 }
 
@@ -544,7 +523,7 @@ __device__ __forceinline__ void kw_lse(const KwArgs &a, KwSmem &sm, int lane)
     KwHeld held[kWBufs] = {};                                // n: 1 once the buffer holds a tile's
     for (int it = 0; ok && kw_take(a, sm, it, x) > 0; ++it)
         for (int kt = x.kt0; ok && kt < x.kt1; ++kt)
-            ok = kw_tiles<MANY>(a, x, kw_range<MANY>(a, x, kt), kt, lane, [&](const KwTile &t) {
+            ok = kw_tiles(a, x, kw_range(a, x, kt), kt, lane, [&](const KwTile &t) {
                 const bool same = !MANY && (buf.s ? held[1].same(x, t) : held[0].same(x, t));
                 float v[kWCols / 32];
                 if (!same) {
@@ -663,40 +642,35 @@ __device__ __forceinline__ float kw_columns(uint32_t ts, int c0, int c1, int nr,
     return p0 + p1;
 }
 
-template <bool MANY>
 __device__ __forceinline__ void kw_sum(const KwArgs &a, KwSmem &sm, uint32_t tmem, int warp, int lane)
 {
     uint32_t *err = &a.hdr->error;
     const int wg = (warp - kWFirstWarp) >> 2;
+    const int buf = wg >> 1, half = wg & 1;                  // key tile of the pair, half of the columns
     const int key = (warp & 3) * 32 + lane;                  // TMEM lane
-    const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t ts = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf * kWCols;
     const uint64_t c2 = f2_pack(a.c2, a.c2);
-    const int buf = wg >> 1, half = wg & 1;
-    uint32_t n = 0, kc = 0;                                  // column tiles and key tiles so far
+    uint32_t n = 0, kc = 0;                                  // column tiles and pairs so far
     bool ok = true;
     KwItem x;
     for (int it = 0; ok && kw_take(a, sm, it, x) > 0; ++it) {
         for (int kt = x.kt0; ok && kt < x.kt1; ++kt) {
-            const KwRange rg = kw_range<MANY>(a, x, kt);
-            const int j = (MANY ? 2 * kt + buf : kt) * kWTile + key;
+            const KwRange rg = kw_range(a, x, kt);
+            const int j = kt * kWKeys + buf * kWTile + key;
             const bool bounded = x.mode == EA_SSA && j >= a.sink;
             float total = 0.f;
-            ok = kw_tiles<MANY>(a, x, rg, kt, lane, [&](const KwTile &t) {
-                const uint32_t mine = n++;
-                // few rows: the two buffers take turns; many rows: both serve every tile
-                if (!MANY && static_cast<int>(mine % kWBufs) != buf)
-                    return true;
-                if (!mbar_wait_warp(&sm.s_full[buf], MANY ? mine & 1 : (mine / kWBufs) & 1, &sm.abort, err))
+            ok = kw_tiles(a, x, rg, kt, lane, [&](const KwTile &t) {
+                if (!mbar_wait_warp(&sm.s_full[buf], n & 1, &sm.abort, err))
                     return false;
+                ++n;
                 tc_fence_after();
                 const int q16 = t.nh * t.nr / 16, mid = 16 * ((q16 + 1) / 2);
                 // rows [lo, hi) of each head keep key j
                 const int lo = j - (x.off + t.t0);
                 int hi = bounded ? min(t.cnt, lo + a.window) : t.cnt;
-                if (MANY && !((t.keep >> buf) & 1u))
+                if (!((t.keep >> buf) & 1u))
                     hi = 0;
-                const float w = kw_columns(ts + buf * kWCols, half ? mid : 0, half ? 16 * q16 : mid, t.nr, lo,
-                                           hi, c2);
+                const float w = kw_columns(ts, half ? mid : 0, half ? 16 * q16 : mid, t.nr, lo, hi, c2);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
@@ -706,31 +680,27 @@ __device__ __forceinline__ void kw_sum(const KwArgs &a, KwSmem &sm, uint32_t tme
             });
             if (!ok)
                 break;
-            // the warpgroups' sums are joined: many rows, a buffer's two by the first of
-            // them; few rows, all four by each in turn
+            // the two warpgroups' sums are joined by the first
             const int slot = kc % kWSlots;
             const uint32_t phase = (kc / kWSlots) & 1;
             ++kc;
-            ok = mbar_wait_warp(&sm.red_empty[slot], phase ^ 1, &sm.abort, err);
-            if (!ok)
-                break;
-            sm.red[slot][wg][key] = total;
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.red_full[slot]);
-            if (MANY ? half != 0 : slot != wg)
+            if (half) {
+                ok = mbar_wait_warp(&sm.red_empty[buf][slot], phase ^ 1, &sm.abort, err);
+                if (!ok)
+                    break;
+                sm.red[buf][slot][key] = total;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.red_full[buf][slot]);
                 continue;
-            ok = mbar_wait_warp(&sm.red_full[slot], phase, &sm.abort, err);
+            }
+            ok = mbar_wait_warp(&sm.red_full[buf][slot], phase, &sm.abort, err);
             if (!ok)
                 break;
-            float w = 0.f;
-#pragma unroll
-            for (int k = 0; k < kWGroups; ++k)
-                if (!MANY || k / 2 == buf)
-                    w += sm.red[slot][k][key];
+            const float w = total + sm.red[buf][slot][key];
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&sm.red_empty[slot]);
+                mbar_arrive(&sm.red_empty[buf][slot]);
             if (j < x.L) {
                 const int64_t at = (static_cast<int64_t>(x.b) * a.Hkv + x.h) * a.Lmax + j;
                 if (a.parts > 1)
@@ -741,7 +711,6 @@ __device__ __forceinline__ void kw_sum(const KwArgs &a, KwSmem &sm, uint32_t tme
         }
     }
 }
-static_assert(kWSlots == kWGroups, "few rows: warpgroup w joins the key tiles of slot w");
 
 template <bool MANY>
 __global__ void __launch_bounds__(kWThreads, 1)
@@ -752,13 +721,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
     KwSmem &sm = *reinterpret_cast<KwSmem *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    constexpr int kMma = MANY ? 1 : 2;                        // MMA warps
     if (threadIdx.x == 0) {
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(&sm.k_full[s], 1);
-            mbar_init(&sm.k_empty[s], kMma);
+            mbar_init(&sm.k_empty[s], 1);
             mbar_init(&sm.q_full[s], 1);
-            mbar_init(&sm.q_empty[s], kMma);
+            mbar_init(&sm.q_empty[s], 1);
         }
         for (int s = 0; s < kWBufs; ++s) {
             mbar_init(&sm.s_full[s], 1);
@@ -767,13 +735,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
             mbar_init(&sm.lse_empty[s], 1);
         }
         for (int s = 0; s < kWSlots; ++s) {
-            mbar_init(&sm.red_full[s], 4 * kWGroups);
-            mbar_init(&sm.red_empty[s], MANY ? 8 : 4);        // the joining warpgroups' warps
+            for (int b = 0; b < kWBufs; ++b) {
+                mbar_init(&sm.red_full[b][s], 4);
+                mbar_init(&sm.red_empty[b][s], 4);
+            }
             mbar_init(&sm.item_full[s], 1);
-            mbar_init(&sm.item_empty[s], kMma + 1 + 4 * kWGroups);   // MMA, LSE and summing warps
+            mbar_init(&sm.item_empty[s], 2 + 4 * kWGroups);   // MMA, LSE and summing warps
         }
-        mbar_init(&sm.drain[0], 1);
-        mbar_init(&sm.drain[1], 1);
+        mbar_init(&sm.drain, 1);
         sm.abort = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -798,13 +767,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (warp == 0)
         kw_producer<MANY>(&tm_k, tm_q, a, sm, lane);
     else if (warp == 1)
-        kw_mma<MANY>(a, sm, tmem, lane, 0);
+        kw_mma<MANY>(a, sm, tmem, lane);
     else if (warp == 2)
         kw_lse<MANY>(a, sm, lane);
-    else if (!MANY && warp == 3)
-        kw_mma<MANY>(a, sm, tmem, lane, 1);
     else if (warp >= kWFirstWarp)
-        kw_sum<MANY>(a, sm, tmem, warp, lane);
+        kw_sum(a, sm, tmem, warp, lane);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -835,17 +802,16 @@ __global__ void __launch_bounds__(256) kw_join_kernel(const KwArgs a)
 
 // How the work is cut, from the sizes alone and for this GPU's 152 SMs, so that a
 // workspace and the result do not depend on where they are made.
-//   many   more query columns than one tile holds: pairs of key tiles share them
-//   parts  shares of a key tile's queries: enough items for about four per SM,
-//          none shorter than a tile's rows
-//   run    key tiles per item: one (pair), except where one query tile serves
-//          all of them, which costs about as much to load as three key tiles:
-//          one item per SM, of at most 16 tiles (17 GFLOP over 32K keys: 2 tiles
-//          an item 67 us, 4 55, 8 51)
+//   many   more query columns than one tile holds: query tiles stream
+//   parts  shares of a pair's queries: enough items for about four per SM, none
+//          shorter than a tile's rows
+//   run    pairs per item: one, except where one query tile serves all of them,
+//          which costs about as much to load as they do: one item per SM, of at
+//          most 8 pairs (17 GFLOP over 32K keys: 1 pair an item 67 us, 4 51)
 struct KwPlan {
     bool many;
     int seg, parts, run;
-    int64_t units;         // key tiles or pairs of one sequence
+    int64_t units;         // pairs of one sequence
 };
 
 static KwPlan kw_plan(int B, int Tq, int Lmax, int Hkv, int g)
@@ -853,13 +819,13 @@ static KwPlan kw_plan(int B, int Tq, int Lmax, int Hkv, int g)
     KwPlan p;
     p.seg = g == 1 ? kWCols : kWTile;
     p.many = ceil_div(Tq, 16) * 16 * g > kWCols;
-    p.units = ceil_div(Lmax, p.many ? 2 * kWTile : kWTile);
+    p.units = ceil_div(Lmax, kWKeys);
     const int64_t tiles = p.units * B * Hkv;
     const int64_t want = ceil_div(4 * 152, tiles), most = ceil_div(Tq, p.seg);
     const int64_t parts = want < most ? want : most;
     p.parts = static_cast<int>(parts < 1 ? 1 : parts > kWMaxParts ? kWMaxParts : parts);
     const int64_t run = p.many ? 1 : ceil_div(tiles, 152);
-    p.run = static_cast<int>(run > 16 ? 16 : run);
+    p.run = static_cast<int>(run > 8 ? 8 : run);
     return p;
 }
 
