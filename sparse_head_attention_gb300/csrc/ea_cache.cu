@@ -274,7 +274,7 @@ __device__ __forceinline__ void put_bf16(__nv_bfloat16 *dst, const uint4 &raw, f
 // known, K's and V's rows together, and registers are kept low enough for many
 // CTAs.
 template <int SB, int SRC, int DST>
-__global__ void __launch_bounds__(kCacheThreads, SB > 64 ? 3 : SRC == EA_CACHE_BF16 ? 5 : SB == 64 ? 6 : 10)
+__global__ void __launch_bounds__(kCacheThreads, SB > 64 ? 3 : SRC == EA_CACHE_BF16 ? 7 : SB == 64 ? 6 : 14)
     cache_compact_kernel(const CompactArgs a)
 {
     constexpr bool kE4M3 = DST == EA_CACHE_E4M3;
