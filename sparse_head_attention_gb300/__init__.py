@@ -735,10 +735,10 @@ def kv_cache_paged(num_pages, page_size, Hkv, block_table, *, dtype=torch.float8
 
 
 def _one_device(first, *tensors):
-    dev = first.device
+    dev = first.get_device()
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("tensors on several devices: %s and %s" % (dev, t.device))
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on several devices: %s and %s" % (first.device, t.device))
 
 
 class _at:
@@ -773,19 +773,15 @@ class _at:
 _I64 = {n: ctypes.c_int64 * n for n in (3, 4)}
 
 
-def _i32_vec(t, name, B):
-    if t is not None:
-        _dev(t, name, torch.int32)
-        if tuple(t.shape) != (B,) or not t.is_contiguous():
-            raise ValueError("%s must be a contiguous int32 [%d] tensor" % (name, B))
-    return t
-
-
 def _like(t, name, shape, dtype):
     _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s %s tensor" % (name, dtype, list(shape)))
     return t
+
+
+def _i32_vec(t, name, B):
+    return t if t is None else _like(t, name, (B,), torch.int32)
 
 
 def ea_cache_workspace_size():
@@ -864,17 +860,19 @@ def ea_hybrid_attn_decode_q8(q, cache, seqlens, m, *, sink, window, block_mask=N
     _one_device(cache.K, q, seqlens, m, bm, key_weights, O, LSE, workspace)
     with _at(cache.device, stream) as st:
         if O is None:
-            O = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            O = q.new_empty(q.shape)
         if LSE is None and want_lse:
-            LSE = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+            LSE = q.new_empty((B, Hq), dtype=torch.float32)
         if workspace is None:
             workspace = decode_q8_workspace(B, Hq, cache.Hkv, cache.capacity, num_splits,
                                             key_weights is not None, d, q.device)
         _check("ea_hybrid_attn_decode_q8", lib().ea_hybrid_attn_decode_q8(
-            q.data_ptr(), cache._ref, O.data_ptr(), _ptr(LSE), _I64[3](*q.stride()), _I64[3](*O.stride()),
-            seqlens.data_ptr(), B, Hq, 1.0 / math.sqrt(d) if scale is None else float(scale),
+            q.data_ptr(), cache._ref, O.data_ptr(), _ptr(LSE), _I64[3](*q.stride()),
+            _I64[3](*O.stride()), seqlens.data_ptr(), B, Hq,
+            1.0 / math.sqrt(d) if scale is None else float(scale),
             m.data_ptr(), int(sink), int(window), _ptr(bm), TILE, int(num_splits),
-            _ptr(key_weights), 1 if accumulate else 0, workspace.data_ptr(), workspace.numel(), st))
+            _ptr(key_weights), 1 if accumulate else 0, workspace.data_ptr(),
+            workspace.numel(), st))
     return O, LSE
 
 
