@@ -158,10 +158,12 @@ bool encode_tmap_u8_4d(void *tmap_out, const void *base, int d, int H, int S, in
                              static_cast<cuuint64_t>(strides_elems[0])};
     cuuint32_t box[4] = {128u, 1u, static_cast<cuuint32_t>(box_rows), 1u};
     cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    // A row of a box is 128 bytes: promoted to 256, a read would bring the next
+    // head's row with it, which may not be wanted (a streaming head) or not yet.
     CUresult r = fn(reinterpret_cast<CUtensorMap *>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                     const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
