@@ -145,6 +145,7 @@ static __global__ void __launch_bounds__(kBlkThreads) decode_blocks_kernel(Decod
     const int u = blockIdx.x, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int b = u / a.Hkv, h = u % a.Hkv;
     const int L = a.seqlens[b];
+    griddep_launch_dependents();
     int count = 0;
     if (a.m[u] == EA_BLOCK && L > 0 && L <= a.Lmax) {
         const int qb = (L - 1) / EA_TILE;
@@ -217,6 +218,7 @@ static __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(Decode
     __shared__ long long red_work[kPlanThreads / 32];
     __shared__ int red_chunks[kPlanThreads / 32];
     griddep_launch_dependents();   // the split kernel may start its prologue
+    griddep_wait();                // decode_blocks_kernel's lists, where it ran
     const int units = a.B * a.Hkv;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int per = (units + kPlanThreads - 1) / kPlanThreads;
@@ -280,7 +282,8 @@ static __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(Decode
         run += ns;
     }
     if (tid == 0) {
-        a.hdr->n_items = static_cast<uint32_t>(grand);
+        // (chunks that the list has no room for have been reported)
+        a.hdr->n_items = static_cast<uint32_t>(min(static_cast<int64_t>(grand), a.max_chunks));
         a.hdr->work_counter = 0;   // the split kernel's chunk queue
     }
 }

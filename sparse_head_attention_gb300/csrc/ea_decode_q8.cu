@@ -21,6 +21,11 @@
 //     kQ8Warps): no exchange between warps within a chunk of keys, the softmax's
 //     maximum is reduced once per 64 keys, and a warp has several tile times for
 //     the latency of its own tile.
+//   - Joining warps add the compute warps' results of a chunk up while those are
+//     at the next chunk, so that a chunk's end waits for nobody (nine ragged
+//     sequences of all head kinds 40.4 -> 37.6 us with key weights, nine of up to
+//     30000 keys and full heads 57 -> 51; with one such warp instead of four the
+//     end of a short step is its: one sequence of 32K 14.4 us, not 13.6).
 //   - Products are m16n8k16 f16 MMAs with the keys (then the head dims) as the 16
 //     rows and the group's up to eight query heads as the 8 columns, so no row is
 //     padding: S^T = C^K Q^T and O^T += C^V^T W^T.  e4m3 and int8 codes are exact
@@ -32,10 +37,18 @@
 //     gets 4 neighbouring codes: for S^T that is one k16 step of its row once Q's
 //     columns are taken in the same order; for V^T the transposed load gives 2
 //     dims of 2 keys, which pair up by key.
-// Planning, chunking and masks are those of the bf16 decode (ea_decode_plan.cuh)
-// with all tiles 64-key aligned; a merge joins the chunks of each (sequence,
-// head), and with key weights a last kernel turns the stored logits into
-// exp(x - LSE) and sums them over the group.
+// Chunks (runs of one unit's tiles, taken from a queue), their planning and the
+// masks are those of the bf16 decode (ea_decode_plan.cuh) with all tiles 64-key
+// aligned.  (One equal range of all units' tiles per SM instead leaves no SM idle,
+// but neighbouring heads' rows, neighbours in memory, are then no longer read at
+// the same time: 333 -> 371 us for 16 sequences of 64K.)  A merge joins the chunks
+// of each (sequence, head), and with key weights a last kernel turns the stored
+// logits into exp(x - LSE) and sums them over the group.
+//
+// Measured: 16 sequences of 64K, 8 KV heads, 317 - 333 us on different GPUs of
+// the kind (2.15 GB: 0.95 - 1.0 of the measured HBM rate); one of 32K with two full
+// and six streaming heads 13.6 us (20 MB, bound by the latency of a plan, a chunk
+// of nine tiles, two joins and a second launch).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -50,7 +63,8 @@ namespace ea {
 constexpr int kQ8Stages = 12;
 constexpr int kQ8TileBytes = kDecKeys * EA_HEAD_DIM;   // K or V codes of one tile: 8 KB
 constexpr int kQ8Warps = 6;                            // compute warps
-constexpr int kQ8Threads = (kQ8Warps + 1) * 32;        // + one producer warp
+constexpr int kQ8Joiners = 4;                          // warps that add the compute warps' results up
+constexpr int kQ8Threads = (kQ8Warps + 1 + kQ8Joiners) * 32;   // + one producer warp
 constexpr int kQ8Groups = kDecKeys / 16;               // 16-key groups of a tile: one scale each at most
 constexpr float kQ8Shift = 14.f;                       // w <= 2^14
 
@@ -63,6 +77,7 @@ struct __align__(1024) Q8Smem {
     uint64_t full[kQ8Stages];
     uint64_t empty[kQ8Stages];
     uint64_t chunk_full[2], chunk_empty[2];
+    uint64_t red_full, red_empty;             // the warps' results of a chunk
     int chunk[2];
     int abort;
     SelfPlan plan;
@@ -127,20 +142,6 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 
-// Barrier of the compute warps that also tells whether any of them failed.
-__device__ __forceinline__ bool compute_sync_or(bool failed)
-{
-    int any;
-    asm volatile("{\n\t.reg .pred p, q;\n\t"
-                 "setp.ne.s32 p, %1, 0;\n\t"
-                 "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
-                 "selp.s32 %0, 1, 0, q;\n\t}"
-                 : "=r"(any)
-                 : "r"(failed ? 1 : 0), "n"(kQ8Warps * 32)
-                 : "memory");
-    return any != 0;
-}
-
 __device__ __forceinline__ bool key_kept(const KeySegs &ks, int key)
 {
     return (key < ks.n0 || key >= ks.w0) && key < ks.L;
@@ -168,8 +169,10 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&sm.chunk_full[s], 1);
-            mbar_init(&sm.chunk_empty[s], kQ8Warps);
+            mbar_init(&sm.chunk_empty[s], kQ8Warps + kQ8Joiners);
         }
+        mbar_init(&sm.red_full, kQ8Warps);
+        mbar_init(&sm.red_empty, kQ8Joiners);
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -265,19 +268,68 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         return;
     }
 
-    // ---------------------------------------------------------------- compute
-    uint32_t base = 0;                          // tiles of the chunks before this one
-    for (int it = 0;; ++it) {
+    // The compute warps and the joining warps: chunk number `it` (-1: none left).
+    auto next_chunk = [&](int it) {
         const int slot = it & 1;
-        bool ok = mbar_wait_warp(&sm.chunk_full[slot], (it >> 1) & 1, abort, &a.hdr->error);
+        const bool ok = mbar_wait_warp(&sm.chunk_full[slot], (it >> 1) & 1, abort, &a.hdr->error);
         const int c = ok ? sm.chunk[slot] : -1;
         __syncwarp();
         if (ok && lane == 0)
             mbar_arrive(&sm.chunk_empty[slot]);
-        if (c < 0) {
-            compute_sync_or(!ok);               // a warp that failed waits for the others there
-            return;
+        return c;
+    };
+
+    if (warp > kQ8Warps) {
+        // ------------------------------------------------------------ joining warps
+        // add up the compute warps' results of a chunk while they go on to the next
+        for (int it = 0;; ++it) {
+            const int c = next_chunk(it);
+            if (c < 0 || !mbar_wait_warp(&sm.red_full, it & 1, abort, &a.hdr->error))
+                return;
+            for (int hh = warp - kQ8Warps - 1; hh < a.g; hh += kQ8Joiners) {
+                float M = NEG_INF;
+#pragma unroll
+                for (int w = 0; w < kQ8Warps; ++w)
+                    M = fmaxf(M, sm.red_m[w][hh]);
+                float lsum = 0.f;
+                float4 osum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kQ8Warps; ++w) {
+                    const float mw = sm.red_m[w][hh];
+                    // 1 where nothing but NaN (or no key) was met, so that a NaN stays
+                    const float f = mw == NEG_INF ? 1.f : ex2(mw - M);
+                    const float4 x = *reinterpret_cast<const float4 *>(&sm.red_o[w][hh][4 * lane]);
+                    lsum = fmaf(sm.red_l[w][hh], f, lsum);
+                    osum.x = fmaf(x.x, f, osum.x);
+                    osum.y = fmaf(x.y, f, osum.y);
+                    osum.z = fmaf(x.z, f, osum.z);
+                    osum.w = fmaf(x.w, f, osum.w);
+                }
+                const int64_t pidx = static_cast<int64_t>(c) * a.g + hh;
+                if (!in_bounds(pidx, a.max_chunks * a.g, &a.hdr->error))
+                    continue;
+                if (lsum == 0.f)
+                    osum = make_float4(0.f, 0.f, 0.f, 0.f);
+                else
+                    osum = make_float4(osum.x / lsum, osum.y / lsum, osum.z / lsum, osum.w / lsum);
+                *reinterpret_cast<float4 *>(a.part_o + pidx * EA_HEAD_DIM + 4 * lane) = osum;
+                const float Mb = (M == NEG_INF ? 0.f : M) - kQ8Shift;
+                if (lane == 0)
+                    a.part_lse[pidx] = lsum == 0.f ? NEG_INF : Mb + lg2(lsum);
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.red_empty);
         }
+    }
+
+    // ---------------------------------------------------------------- compute
+    uint32_t base = 0;                          // tiles of the chunks before this one
+    for (int it = 0;; ++it) {
+        const int c = next_chunk(it);
+        if (c < 0)
+            return;
+        bool ok = true;
         const ChunkInfo ci = chunk_info(a, c, sm.plan);
         // Q as the B operand: column n = head r of the group (heads >= g are
         // zero), k = 2q.. and 2q + 8.. are dims 16 j + 4 q .. + 3; times a power
@@ -498,7 +550,10 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         }
         base += ci.n_tiles;
 
-        // per-warp results -> shared memory, then merge the warps
+        // this warp's results -> shared memory, once those of the chunk before have
+        // been joined
+        if (!ok || !mbar_wait_warp(&sm.red_empty, (it & 1) ^ 1, abort, &a.hdr->error))
+            return;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             l_part[e] += __shfl_xor_sync(0xffffffffu, l_part[e], 4);
@@ -516,37 +571,14 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
                 }
             }
         }
-        if (compute_sync_or(!ok))
-            return;
-        for (int idx = tid; idx < a.g * EA_HEAD_DIM; idx += kQ8Warps * 32) {
-            const int hh = idx / EA_HEAD_DIM, dd = idx % EA_HEAD_DIM;
-            float M = NEG_INF;
-#pragma unroll
-            for (int w = 0; w < kQ8Warps; ++w)
-                M = fmaxf(M, sm.red_m[w][hh]);
-            float lsum = 0.f, osum = 0.f;
-#pragma unroll
-            for (int w = 0; w < kQ8Warps; ++w) {
-                const float mw = sm.red_m[w][hh];
-                // 1 where nothing but NaN (or no key) was met, so that a NaN stays
-                const float f = mw == NEG_INF ? 1.f : ex2(mw - M);
-                lsum = fmaf(sm.red_l[w][hh], f, lsum);
-                osum = fmaf(sm.red_o[w][hh][dd], f, osum);
-            }
-            const int64_t pidx = static_cast<int64_t>(c) * a.g + hh;
-            if (!in_bounds(pidx, a.max_chunks * a.g, &a.hdr->error))
-                continue;
-            const float Mb = (M == NEG_INF ? 0.f : M) - kQ8Shift;
-            a.part_o[pidx * EA_HEAD_DIM + dd] = lsum == 0.f ? 0.f : osum / lsum;
-            if (dd == 0)
-                a.part_lse[pidx] = lsum == 0.f ? NEG_INF : Mb + lg2(lsum);
-        }
-        asm volatile("bar.sync 2, %0;" ::"n"(kQ8Warps * 32) : "memory");   // the buffers are reused
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sm.red_full);
     }
 }
 
 // ---------------------------------------------------------------- merge
-// One CTA per (q head, b): joins the unit's chunks (partial O and log2 LSE) by
+// One CTA per (b, q head): joins the unit's chunks (partial O and log2 LSE) by
 // their weights 2^(lse - max).  A NaN partial makes the result NaN.  Groups of
 // 128 threads take a share of the chunks each, eight chunks' loads at a time.
 constexpr int kQ8MergeGroups = 4;
@@ -557,9 +589,10 @@ __global__ void __launch_bounds__(kQ8MergeGroups * EA_HEAD_DIM, 2) decode_q8_mer
     __shared__ float go[kQ8MergeGroups][EA_HEAD_DIM];
     const DecodeArgs &a = qa.d;
     const float NEG_INF = -__int_as_float(0x7f800000);
-    const int qh = blockIdx.x, b = blockIdx.y;
+    const int b = blockIdx.x, qh = blockIdx.y;
     const int dd = threadIdx.x % EA_HEAD_DIM, grp = threadIdx.x / EA_HEAD_DIM;
     griddep_wait();
+    griddep_launch_dependents();
     const int u = b * a.Hkv + qh / a.g, hh = qh % a.g;
     const int first = a.unit_first[u];
     int ns = a.unit_splits[u];
@@ -636,6 +669,7 @@ constexpr int kQ8WKeys = 4 * kQ8WThreads;
 __global__ void __launch_bounds__(kQ8WThreads) decode_q8_weights_kernel(const Q8Args qa)
 {
     const DecodeArgs &a = qa.d;
+    griddep_wait();
     const int u = blockIdx.y, b = u / a.Hkv, h = u % a.Hkv;
     const int L = a.seqlens[b];
     const int j0 = blockIdx.x * kQ8WKeys;
@@ -728,6 +762,22 @@ static Q8Ws q8_ws_layout(int B, int Hq, int Hkv, int Lmax, int num_splits, bool 
     return w;
 }
 
+// A kernel that starts its prologue under the end of the call's one before it.
+template <typename A>
+static cudaError_t launch_q8_after(void (*kernel)(A), const A &a, dim3 grid, int threads, cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <bool E4M3, bool WEIGHTS>
 static cudaError_t launch_q8(const CUtensorMap &tk, const CUtensorMap &tv, const Q8Args &a, int grid,
                              cudaStream_t st, int dev)
@@ -760,16 +810,7 @@ static cudaError_t launch_q8(const CUtensorMap &tk, const CUtensorMap &tv, const
 static cudaError_t launch_q8_merge(const Q8Args &a, cudaStream_t st)
 {
     const int groups = static_cast<int64_t>(a.d.B) * a.d.Hq >= 2ll * a.d.num_sms ? 1 : kQ8MergeGroups;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(a.d.Hq, a.d.B);
-    cfg.blockDim = dim3(groups * EA_HEAD_DIM);
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_q8_merge_kernel, a);
+    return launch_q8_after(decode_q8_merge_kernel, a, dim3(a.d.B, a.d.Hq), groups * EA_HEAD_DIM, st);
 }
 
 } // namespace ea
@@ -812,7 +853,7 @@ extern "C" ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cac
         return EA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(O)) & 15u)
         return EA_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(B) * Hkv >= (int64_t(1) << (31 - kSplitBits)) ||
+    if (Hq > 65535 || static_cast<int64_t>(B) * Hkv >= (int64_t(1) << (31 - kSplitBits)) ||
         q8_max_chunks(static_cast<int64_t>(B) * Hkv, Lmax, num_splits) >= (int64_t(1) << 31) ||
         (key_weights && static_cast<int64_t>(B) * Hkv > 65535))
         return EA_ERR_UNSUPPORTED;
@@ -889,22 +930,26 @@ extern "C" ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cac
     a.d.self_plan = units <= kSelfPlanUnits ? 1 : 0;
     if (block_mask)
         decode_blocks_kernel<<<static_cast<unsigned>(units), kBlkThreads, 0, st>>>(a.d);
-    if (!a.d.self_plan)
-        decode_plan_kernel<<<1, kPlanThreads, 0, st>>>(a.d);
-    cudaError_t e;
+    cudaError_t e = cudaSuccess;
+    if (!a.d.self_plan) {
+        if (block_mask)
+            e = launch_q8_after(decode_plan_kernel, a.d, dim3(1), kPlanThreads, st);
+        else
+            decode_plan_kernel<<<1, kPlanThreads, 0, st>>>(a.d);
+    }
+    if (e != cudaSuccess)
+        return EA_ERR_CUDA;
     if (c.format == EA_CACHE_E4M3)
         e = key_weights ? launch_q8<true, true>(tk, tv, a, grid, st, dev)
                         : launch_q8<true, false>(tk, tv, a, grid, st, dev);
     else
         e = key_weights ? launch_q8<false, true>(tk, tv, a, grid, st, dev)
                         : launch_q8<false, false>(tk, tv, a, grid, st, dev);
-    if (e != cudaSuccess)
-        return EA_ERR_CUDA;
-    if (launch_q8_merge(a, st) != cudaSuccess)
-        return EA_ERR_CUDA;
-    if (key_weights)
-        decode_q8_weights_kernel<<<dim3(static_cast<unsigned>(ceil_div(Lmax, kQ8WKeys)),
-                                        static_cast<unsigned>(units)),
-                                   kQ8WThreads, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? EA_OK : EA_ERR_CUDA;
+    if (e == cudaSuccess)
+        e = launch_q8_merge(a, st);
+    if (e == cudaSuccess && key_weights)
+        e = launch_q8_after(decode_q8_weights_kernel, a,
+                            dim3(static_cast<unsigned>(ceil_div(Lmax, kQ8WKeys)), static_cast<unsigned>(units)),
+                            kQ8WThreads, st);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? EA_OK : EA_ERR_CUDA;
 }
