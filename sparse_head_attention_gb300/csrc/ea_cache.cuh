@@ -105,12 +105,6 @@ __device__ __forceinline__ uint32_t encode4_f16(uint32_t lo, uint32_t hi, __half
     }
 }
 
-// Largest magnitude of four f16 numbers.
-__device__ __forceinline__ __half2 amax4_f16(uint32_t lo, uint32_t hi)
-{
-    return __hmax2(__habs2(*reinterpret_cast<const __half2 *>(&lo)), __habs2(*reinterpret_cast<const __half2 *>(&hi)));
-}
-
 __device__ __forceinline__ float2 f16_f32(uint32_t h)
 {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
