@@ -553,6 +553,11 @@ ea_status ea_xa_estimate(const void *Q, const void *K, const int64_t q_str[4],
  * Constraints: d == 128; K, V 16-byte aligned, the strides of the first three
  * dimensions multiples of 16 bytes, head-dim stride 1; a paged sequence's
  * capacity below 2^31.
+ *
+ * Calls that share a workspace of ea_hybrid_attn_decode_q8 or ea_key_weights
+ * must be ordered (one stream, or events), captured and replayed ones among
+ * them; the others only report errors in theirs, which calls in flight at once
+ * may share.
  */
 typedef enum {
     EA_CACHE_BF16 = 0,

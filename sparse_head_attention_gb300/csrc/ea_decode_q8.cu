@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kQ8MergeGroups * EA_HEAD_DIM, 2) decode_q8_mer
 // key_w[unit][j] (+)= sum over the group's heads of 2^(logit - lse) for the kept
 // keys j of the unit, 0 for the others below its length.  A thread per key, its
 // group's logits side by side.  They come from L2, where the split kernel left them:
-// 1.04M keys of 72 units, four heads each, 7.3 us (16.6 MB read).
+// 0.87M keys of 72 units, four heads each, 7.3 us (13.9 MB read).
 constexpr int kQ8WThreads = 256;
 constexpr int kQ8WKeys = 4 * kQ8WThreads;
 
