@@ -637,8 +637,8 @@ ea_status ea_evict_select(const float *weights, const int32_t *seqlens, int B, i
  *   index        device int32 [B][Hkv][keep]
  *   counts       device int32 [B], each in [0, keep] (else reported and skipped)
  *   weights, weights_out  device float [B][Hkv][src capacity] and
- *                [B][Hkv][dst capacity], contiguous, or both NULL: the tokens'
- *                accumulated weights move with them
+ *                [B][Hkv][dst capacity], contiguous and apart, or both NULL:
+ *                the tokens' accumulated weights move with them
  * Rows of dst at or behind counts[b] stay as they are.  An index outside the
  * source, or one whose page is outside it, is reported and reads zeros.  src
  * and dst may share pages of one pool as long as no page is read and written;
@@ -673,7 +673,8 @@ size_t ea_decode_q8_workspace_size(int B, int Hq, int Hkv, int d, int Lmax, int 
  * A kept key of a block with a NaN scale makes its head's O and LSE NaN.
  * Codes and scales behind seqlens[b] are not used, whatever they hold.  Other
  * arguments, modes, masks, constraints and errors as ea_hybrid_attn_decode;
- * pages hold a multiple of 64 rows.
+ * pages hold a multiple of 64 rows, and a given num_splits leaves splits of at
+ * most 2^24 rows (longer: EA_ERR_UNSUPPORTED).
  */
 ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cache, void *O, float *LSE,
                                    const int64_t q_str[3], const int64_t o_str[3],

@@ -872,7 +872,7 @@ extern "C" ea_status ea_cache_compact(const ea_cache *src, const ea_cache *dst,
                                       const float *weights, float *weights_out, void *workspace,
                                       size_t ws_bytes, void *stream)
 {
-    if (!index || !counts || keep < 1 || !weights != !weights_out || (weights && weights == weights_out))
+    if (!index || !counts || keep < 1 || !weights != !weights_out)
         return EA_ERR_INVALID_ARG;
     CompactArgs a{};
     ea_status why;
@@ -891,6 +891,13 @@ extern "C" ea_status ea_cache_compact(const ea_cache *src, const ea_cache *dst,
                 if (p0 < q1 && q0 < p1)
                     return EA_ERR_INVALID_ARG;
             }
+    }
+    if (weights) {
+        // a row's weight may be read after another row's has been written
+        const int64_t rows = static_cast<int64_t>(B) * a.src.Hkv * sizeof(float);
+        const uintptr_t w0 = reinterpret_cast<uintptr_t>(weights), o0 = reinterpret_cast<uintptr_t>(weights_out);
+        if (w0 < o0 + static_cast<uintptr_t>(rows * a.dst.cap) && o0 < w0 + static_cast<uintptr_t>(rows * a.src.cap))
+            return EA_ERR_INVALID_ARG;
     }
     if (!ws_ok(workspace, ws_bytes))
         return EA_ERR_WORKSPACE;

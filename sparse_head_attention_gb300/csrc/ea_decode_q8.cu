@@ -714,6 +714,7 @@ constexpr int kQ8MinChunk = 256;
 constexpr int kQ8MaxChunk = 8192;
 constexpr int kQ8Sms = 152;                  // the plan is for this GPU: a workspace's size depends on it
 constexpr int kQ8MaxSplits = 1024;
+constexpr int kQ8MaxSplitKeys = 1 << 24;     // a chunk's joining warps wait for all of it, 2 s at most
 
 // Chunks of a step at most: the caller's count per unit, or four per SM (or, in a
 // step too long for that, one per kQ8MaxChunk keys), one more for every unit's
@@ -849,7 +850,8 @@ extern "C" ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cac
         return EA_ERR_INVALID_ARG;
     const int64_t nBm = ceil_div(Lmax, EA_TILE);
     if (c.format == EA_CACHE_BF16 || Hq / Hkv > 8 || (block_mask && nBm > 65535) ||
-        (c.table && c.rows % kDecKeys))
+        (c.table && c.rows % kDecKeys) ||
+        (num_splits > 0 && ceil_div(Lmax, num_splits) > kQ8MaxSplitKeys))
         return EA_ERR_UNSUPPORTED;
     if (q_str[2] != 1 || o_str[2] != 1 || q_str[0] <= 0 || q_str[1] <= 0 || o_str[0] <= 0 ||
         o_str[1] <= 0 || q_str[0] % 8 || q_str[1] % 8)

@@ -219,3 +219,18 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         ea.ea_key_weights(x, x, torch.zeros(2, 4, 8), torch.zeros(2, 4, dtype=torch.uint8), sink=0, window=1)
     with pytest.raises(ValueError, match="CUDA"):
         ea.ea_evict_select(torch.zeros(1, 1, 8), torch.zeros(1, dtype=torch.int32), keep=4)
+
+
+def test_compact_refuses_weights_that_overlap(L):
+    # [4][8][4096] floats each (the caches' own sizes): 4 MB a byte short of apart, and one in the other's middle
+    n = 4 * 8 * 4096 * 4
+    W = 1 << 43
+    assert _compact(L, cache(), cache(**FAR), w=W, wo=W + n - 4) == INVALID
+    assert _compact(L, cache(), cache(**FAR), w=W, wo=W - n + 4) == INVALID
+    assert _compact(L, cache(), cache(**FAR), w=W, wo=W + n // 2) == INVALID
+
+
+def test_decode_refuses_splits_that_are_too_long(L):
+    long = dict(rows=1 << 20, max_pages=64, bt_stride=64, scale_block=64)
+    assert _decode(L, paged(**long), ns=3) == UNSUPPORTED
+    assert _decode(L, paged(**long), ns=4, wsb=1024) == WORKSPACE       # 2^24 rows each: as far as the workspace
