@@ -289,3 +289,59 @@ def test_two_streams_with_their_own_workspaces(dev):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, want[i]) for o in got[i])
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+def test_many_short_sequences_beside_a_few_long_ones(dev, dtype):
+    # more units than the planner has threads, most of them a chunk of one tile, some none
+    B, Hkv, cap = 150, 2, 4096
+    c = make_cache(B, cap, Hkv, dtype, 64, 64, seed=121)
+    rng = np.random.default_rng(122)
+    lens = [int(x) for x in rng.integers(0, 130, B)]
+    lens[0], lens[70], lens[149] = 4096, 4001, 3000
+    check(dev, c, tokens((B, 2 * Hkv, 128), seed=123), lens, [[FULL, SSA]] * B, 3, 60)
+
+
+def test_steps_one_after_another_share_a_workspace(dev):
+    # three steps with key weights, then without, in one stream and one graph: no step starts before the one before it has
+    # read its results
+    B, Hkv, g, L = 6, 4, 4, 3000
+    c = make_cache(B, L, Hkv, INT8, 32, 0, seed=131)
+    h = handle(c, dev)
+    sl = torch.tensor([3000, 0, 1, 64, 2111, 999], dtype=torch.int32, device=dev)
+    m = torch.tensor(all_modes(B, Hkv), dtype=torch.uint8, device=dev)
+    bm = torch.as_tensor(wl.block_mask(B, Hkv, L, density=0.3, seed=132)).to(dev)
+    qs = [tokens((B, Hkv * g, 128), seed=133 + i).to(dev) for i in range(3)]
+
+    def steps(ws):
+        out = []
+        for q in qs:
+            w = torch.zeros(B, Hkv, L, device=dev)
+            out += list(ea.ea_hybrid_attn_decode_q8(q, h, sl, m, sink=9, window=300, block_mask=bm, key_weights=w,
+                                                    workspace=None if ws is None else ws)) + [w]
+            out += list(ea.ea_hybrid_attn_decode_q8(q, h, sl, m, sink=9, window=300, block_mask=bm, num_splits=2,
+                                                    workspace=None if ws is None else ws))
+        return out
+
+    want = []
+    for q in qs:                                    # each alone, with workspaces of their own
+        w = torch.zeros(B, Hkv, L, device=dev)
+        want += list(ea.ea_hybrid_attn_decode_q8(q, h, sl, m, sink=9, window=300, block_mask=bm, key_weights=w)) + [w]
+        torch.cuda.synchronize()
+        want += list(ea.ea_hybrid_attn_decode_q8(q, h, sl, m, sink=9, window=300, block_mask=bm, num_splits=2))
+        torch.cuda.synchronize()
+    ws = torch.zeros(max(ea.ea_decode_q8_workspace_size(B, Hkv * g, Hkv, L, n, w) for n, w in ((0, True), (2, False))),
+                     dtype=torch.uint8, device=dev)
+    got = steps(ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = steps(ws)
+    for _ in range(3):
+        for t in captured:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, want))
+    check_no_device_error(ws)
