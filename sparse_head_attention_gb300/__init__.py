@@ -788,6 +788,13 @@ def ea_cache_workspace_size():
     return int(lib().ea_cache_workspace_size())
 
 
+def _clear_workspace(n, device):
+    # only the header has to be zero, and the decode's stored logits may be large
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
 def cache_workspace(device="cuda"):
     """A zeroed workspace of ea_cache_write, ea_evict_select and ea_cache_compact
     (their error word)."""
@@ -821,11 +828,12 @@ def ea_decode_q8_workspace_size(B, Hq, Hkv, Lmax, num_splits=0, weights=False, d
 
 
 def decode_q8_workspace(B, Hq, Hkv, Lmax, num_splits=0, weights=False, d=128, device="cuda"):
-    """A zeroed workspace of ea_hybrid_attn_decode_q8 (weights: with key_weights)."""
+    """A workspace of ea_hybrid_attn_decode_q8 (weights: with key_weights), its
+    error word zero."""
     n = ea_decode_q8_workspace_size(B, Hq, Hkv, Lmax, num_splits, weights, d)
     if n == 0:
         raise ValueError("unsupported decode sizes")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return _clear_workspace(n, device)
 
 
 def ea_hybrid_attn_decode_q8(q, cache, seqlens, m, *, sink, window, block_mask=None, num_splits=0,
@@ -881,11 +889,11 @@ def ea_key_weights_workspace_size(B, Tq, Lmax, Hq, Hkv, d=128):
 
 
 def key_weights_workspace(B, Tq, Lmax, Hq, Hkv, d=128, device="cuda"):
-    """A zeroed workspace of ea_key_weights."""
+    """A workspace of ea_key_weights, its error word zero."""
     n = ea_key_weights_workspace_size(B, Tq, Lmax, Hq, Hkv, d)
     if n == 0:
         raise ValueError("unsupported key weight sizes")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return _clear_workspace(n, device)
 
 
 def ea_key_weights(Q, K, LSE, m, *, sink, window, seqlens=None, block_mask=None, scale=None,
