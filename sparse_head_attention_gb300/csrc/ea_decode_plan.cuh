@@ -41,7 +41,7 @@ struct DecodeArgs {
     // launch and no queue
     int self_plan;
     int chunk_min, chunk_max;   // automatic chunk size (kept keys)
-    int few_chunks;             // a short step takes fewer chunks per SM (chunk_keys)
+    int whole_waves;            // the chunks are to fill whole waves of the SMs (see Waves)
     int64_t max_chunks;         // chunks that the workspace has room for
 };
 
@@ -190,20 +190,51 @@ static __global__ void __launch_bounds__(kBlkThreads) decode_blocks_kernel(Decod
 }
 
 // Kept keys per chunk when the split count is automatic: about four chunks per SM
-// over the step, between chunk_min and chunk_max keys.  With few_chunks a step of
-// fewer than 4096 (2048) keys per SM takes two (one) per SM, less one for every
-// unit (each rounds its chunks up), so that a short step is one even wave.
+// over the step, between chunk_min and chunk_max keys.
 __device__ __forceinline__ long long chunk_keys(const DecodeArgs &a, long long work)
 {
     const long long sms = a.num_sms > 0 ? a.num_sms : 1;
-    long long target = 4 * sms;
-    if (a.few_chunks && work < 4096 * sms) {
-        const long long units = static_cast<long long>(a.B) * a.Hkv;
-        target = work < 2048 * sms ? sms : 2 * sms;
-        target -= units < target / 2 ? units : target / 2;
-    }
+    const long long target = 4 * sms;
     const long long chunk = (work + target - 1) / target;
     return chunk < a.chunk_min ? a.chunk_min : (chunk > a.chunk_max ? a.chunk_max : chunk);
+}
+
+// The same for a step whose chunks are to fill whole waves: one or two per SM in a
+// step of fewer than 2048 or 4096 keys per SM, else four, or as many as chunk_max
+// takes.  As each unit rounds its chunks up, candidate i of kWaveTries is i eighths
+// longer than the work over that number, and the first with no more chunks than it
+// is taken, else the last.  (Nine sequences of 30000 keys, full heads: 98.6 -> 92.8
+// us; nine ragged ones 50.0 -> 47.4, with streaming heads among them 33.9 -> 30.4.
+// The least chunk is work / (4 SMs) or that of chunk_max in whole waves: a step has
+// at most 4 SMs + units + units * longest / chunk_max.)
+constexpr int kWaveTries = 8;
+
+struct Waves {
+    long long target;
+    int chunk;               // candidate 0
+    __device__ __forceinline__ int candidate(const DecodeArgs &a, int i) const
+    {
+        const long long c = chunk + static_cast<long long>(chunk) * i / kWaveTries;
+        return static_cast<int>(c < a.chunk_max ? c : a.chunk_max);
+    }
+};
+
+__device__ __forceinline__ Waves waves(const DecodeArgs &a, long long work)
+{
+    const int sms = a.num_sms > 0 ? a.num_sms : 1;
+    // (fp32 quotients, rounded up by one: 64-bit divisions cost the planner 1 us)
+    const float each = static_cast<float>(work) / static_cast<float>(sms);
+    const int per = each < 2048.f ? 1 : each < 4096.f ? 2 : max(4, static_cast<int>(each / a.chunk_max) + 1);
+    Waves w;
+    w.target = static_cast<long long>(sms) * per;
+    w.chunk = max(static_cast<int>(each / per) + 1, a.chunk_min);
+    return w;
+}
+
+// Chunks of a unit that count: a short rest runs beside the others.
+__device__ __forceinline__ int unit_chunks(int work, int chunk)
+{
+    return 4ll * work > chunk ? (work + chunk - 1) / chunk : 0;
 }
 
 // One CTA: per-unit chunk counts, their prefix sum, and the chunk list.  The
@@ -212,6 +243,7 @@ __device__ __forceinline__ long long chunk_keys(const DecodeArgs &a, long long w
 // a.chunk_min and a.chunk_max kept keys, so that a small
 // batch still spreads over every SM.
 constexpr int kPlanThreads = 256;
+static_assert(kPlanThreads / 32 == kWaveTries, "a warp counts the chunks of one candidate");
 
 static __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(DecodeArgs a)
 {
@@ -245,7 +277,28 @@ static __global__ void __launch_bounds__(kPlanThreads) decode_plan_kernel(Decode
 #pragma unroll
     for (int w = 0; w < kPlanThreads / 32; ++w)
         total_work += red_work[w];
-    const long long chunk = chunk_keys(a, total_work);
+    long long chunk;
+    if (a.whole_waves) {
+        // warp i counts the chunks of candidate i (the units' work is in unit_splits:
+        // the barrier above ordered its stores)
+        const Waves wv = waves(a, total_work);
+        const int c = wv.candidate(a, warp);
+        int n = 0;
+        if (units <= 32 * kPlanThreads)
+            for (int u = lane; u < units; u += 32)
+                n += unit_chunks(a.unit_splits[u], c);
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0)
+            red_chunks[warp] = n;
+        __syncthreads();
+        int i = 0;
+        while (i < kWaveTries - 1 && red_chunks[i] > wv.target)
+            ++i;
+        chunk = wv.candidate(a, i);
+        __syncthreads();                      // red_chunks is written again
+    } else {
+        chunk = chunk_keys(a, total_work);
+    }
     int local = 0;
     for (int u = lo; u < hi; ++u) {
         const int work = a.unit_splits[u];
@@ -416,7 +469,16 @@ __device__ __forceinline__ void self_plan(const DecodeArgs &a, SelfPlan &plan, i
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    const long long chunk = chunk_keys(a, mine);
+    long long chunk;
+    if (a.whole_waves) {
+        // few units: room for each one's last chunk
+        const Waves wv = waves(a, mine);
+        const float t = static_cast<float>(wv.target);
+        chunk = min(static_cast<int>(wv.chunk * (t / (t - min(static_cast<float>(units), t / 2.f)))) + 1,
+                    a.chunk_max);
+    } else {
+        chunk = chunk_keys(a, mine);
+    }
     int ns[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < 2; ++k)

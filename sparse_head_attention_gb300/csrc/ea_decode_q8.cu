@@ -707,9 +707,9 @@ __global__ void __launch_bounds__(kQ8WThreads) decode_q8_weights_kernel(const Q8
 }
 
 // ---------------------------------------------------------------- host
-// Keys per chunk when the split count is automatic (see chunk_keys).  Measured on
-// one sequence of 32K with two full and six streaming heads: chunks of 2048 keys
-// 19.3 us, one chunk per SM 13.6.
+// Keys per chunk when the split count is automatic (see Waves).  Measured on one
+// sequence of 32K with two full and six streaming heads: chunks of 2048 keys 19.3
+// us, one chunk per SM 13.6.
 constexpr int kQ8MinChunk = 256;
 constexpr int kQ8MaxChunk = 8192;
 constexpr int kQ8Sms = 152;                  // the plan is for this GPU: a workspace's size depends on it
@@ -898,7 +898,7 @@ extern "C" ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cac
     a.d.num_splits = num_splits;
     a.d.max_splits = num_splits > 0 ? num_splits : kQ8MaxSplits;
     a.d.max_chunks = L.max_chunks;
-    a.d.few_chunks = 1;
+    a.d.whole_waves = 1;
     a.d.num_sms = kQ8Sms;
     a.d.scale_log2 = scale * 1.4426950408889634f;
     a.d.block_mask = block_mask;
