@@ -293,22 +293,25 @@ __device__ __forceinline__ void put_bf16(__nv_bfloat16 *dst, const uint4 &raw, f
 
 // Three dependent loads deep (index, page, data) with little work behind them, so
 // what counts is how many are in flight: the index is read before the count is
-// known, K's and V's rows together, and registers are kept low enough for many
-// CTAs (16 per SM with blocks of 32: 31 us, ten: 34).  After that it is instructions
-// (64 % of the issue slots taken): magnitudes are compared as codes, not as
-// numbers (34 -> 31 us), and a row whose scale stays is copied (31 -> 30).
+// known, K's and V's rows are read together (8 bits) or by a CTA each (bf16), and
+// registers are kept low enough for many CTAs (16 per SM with blocks of 32: 31 us,
+// ten: 34).  After that it is instructions (64 % of the issue slots taken):
+// magnitudes are compared as codes, not as numbers (34 -> 31 us), and a row whose
+// scale stays is copied (31 -> 30).
 // Measured: 16 paged int8 caches, 4000 of up to 16384 tokens kept, blocks of 32, 30
 // us (119 MB, 4.0 TB/s; the floor at the measured HBM rate is 17.6); 8192 of 32K
-// bf16 tokens to e4m3, 51 MB, 9.7 us out of L2 and 16.3 out of HBM (floor 7.5).
+// bf16 tokens to e4m3, 51 MB, 9.7 us out of L2 and 14.4 out of HBM (floor 7.5; K and
+// V by one CTA 16.3).
 template <int SB, int SRC, int DST>
-__global__ void __launch_bounds__(kCacheThreads, SB > 64 ? 3 : SRC == EA_CACHE_BF16 ? 7 : SB == 64 ? 6 : 14)
+__global__ void __launch_bounds__(kCacheThreads, SB > 64 ? 3 : SRC == EA_CACHE_BF16 ? 10 : SB == 64 ? 6 : 14)
     cache_compact_kernel(const CompactArgs a)
 {
     constexpr bool kE4M3 = DST == EA_CACHE_E4M3;
     constexpr int kRowThreads = EA_HEAD_DIM / kElems<SRC>, kRowsPerPass = kCacheThreads / kRowThreads;
     constexpr int kPasses = SB / kRowsPerPass;         // 1 at least: 16 rows a pass
-    // K and V at once, unless that takes too many registers
+    // K and V at once, or, where that takes too many registers, by a CTA each
     constexpr int KV = SRC == EA_CACHE_BF16 ? 1 : 2;
+    const int kv0 = KV == 1 ? blockIdx.z : 0;
     using Elem = typename std::conditional<SRC == EA_CACHE_BF16, uint16_t, uint8_t>::type;
     __shared__ uint32_t red[2][4];
     const int h = blockIdx.x % a.dst.Hkv, blk = blockIdx.x / a.dst.Hkv;
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(kCacheThreads, SB > 64 ? 3 : SRC == EA_CACHE_B
                 raise_error(a.err, EA_DEVERR_CHECK);
                 at[i] = -1;
             }
-            if (a.w && e0 == 0)
+            if (a.w && e0 == 0 && kv0 == 0)
                 a.w_out[unit * a.dst.cap + p] = at[i] >= 0 ? __ldg(a.w + unit * a.src.cap + at[i]) : 0.f;
         }
         so[i] = b;
@@ -378,9 +381,10 @@ __global__ void __launch_bounds__(kCacheThreads, SB > 64 ? 3 : SRC == EA_CACHE_B
         load(1, raw[1], sc[1]);
     }
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-        uint4 (&rw)[kPasses] = raw[kv % KV];
-        float (&s_row)[kPasses] = sc[kv % KV];
+    for (int j = 0; j < KV; ++j) {
+        const int kv = KV == 1 ? kv0 : j;
+        uint4 (&rw)[kPasses] = raw[j];
+        float (&s_row)[kPasses] = sc[j];
         if constexpr (KV == 1)
             load(kv, rw, s_row);
         if constexpr (DST == EA_CACHE_BF16) {
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(kCacheThreads, SB > 64 ? 3 : SRC == EA_CACHE_B
 #pragma unroll
             for (int i = 0; i < kPasses; ++i)
                 mx = max(mx, row_amax<SRC>(rw[i], s_row[i]));
-            const float s = block_scale(cta_max(mx, red[kv]), kE4M3);
+            const float s = block_scale(cta_max(mx, red[j]), kE4M3);
             if (threadIdx.x == 0)
                 a.dst.scale[kv][(static_cast<int64_t>(outer) * a.dst.Hkv + h) * a.dst.nsb + row0 / SB] = s;
             const bool dead = isnan(s);
@@ -911,7 +915,8 @@ extern "C" ea_status ea_cache_compact(const ea_cache *src, const ea_cache *dst,
     a.w_out = weights_out;
     a.err = &static_cast<ea_ws_header *>(workspace)->error;
     a.keep = keep;
-    const dim3 grid(static_cast<unsigned>(blocks * a.dst.Hkv), static_cast<unsigned>(B));
+    const dim3 grid(static_cast<unsigned>(blocks * a.dst.Hkv), static_cast<unsigned>(B),
+                    a.src.format == EA_CACHE_BF16 ? 2 : 1);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (sb == 16)
         launch_compact<16>(a, grid, st);
