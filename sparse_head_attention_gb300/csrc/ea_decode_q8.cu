@@ -551,7 +551,9 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
         base += ci.n_tiles;
 
         // this warp's results -> shared memory, once those of the chunk before have
-        // been joined
+        // been joined.  They are placed by the chunk's tiles that they hold (first,
+        // first + kQ8Warps, ...): which warp that is depends on the chunks its CTA took
+        // before, and the order of the sums must not.
         if (!ok || !mbar_wait_warp(&sm.red_empty, (it & 1) ^ 1, abort, &a.hdr->error))
             return;
 #pragma unroll
@@ -563,11 +565,11 @@ __global__ void __launch_bounds__(kQ8Threads, 1)
             if (head < a.g) {
 #pragma unroll
                 for (int n = 0; n < 8; ++n)
-                    *reinterpret_cast<float2 *>(&sm.red_o[warp][head][16 * n + 2 * r]) =
+                    *reinterpret_cast<float2 *>(&sm.red_o[first][head][16 * n + 2 * r]) =
                         make_float2(o[n][e], o[n][e + 2]);
                 if (r == 0) {
-                    sm.red_m[warp][head] = m_run[e];
-                    sm.red_l[warp][head] = l_part[e];
+                    sm.red_m[first][head] = m_run[e];
+                    sm.red_l[first][head] = l_part[e];
                 }
             }
         }

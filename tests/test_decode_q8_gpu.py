@@ -345,3 +345,25 @@ def test_steps_one_after_another_share_a_workspace(dev):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(captured, want))
     check_no_device_error(ws)
+
+
+def test_equal_calls_give_equal_bits_whatever_cta_takes_a_chunk(dev):
+    # several chunks of many lengths for each SM, taken from a queue in another order every time
+    B, Hkv, g, L = 7, 8, 2, 20000
+    gen = torch.Generator(device=dev).manual_seed(141)
+    c = ea.kv_cache(B, L, Hkv, dtype=INT8, scale_block=32, device=dev)
+    for x in (c.K, c.V):
+        x.copy_(torch.randint(-127, 128, x.shape, generator=gen, device=dev, dtype=torch.int8))
+    for x in (c.k_scale, c.v_scale):
+        x.copy_(torch.exp2(torch.randint(-9, -5, x.shape, generator=gen, device=dev).float()))
+    sl = torch.tensor([20000, 19999, 17777, 12345, 9000, 64, 15001], dtype=torch.int32, device=dev)
+    m = torch.tensor(all_modes(B, Hkv), dtype=torch.uint8, device=dev)
+    bm = torch.as_tensor(wl.block_mask(B, Hkv, L, density=0.5, seed=142)).to(dev)
+    q = tokens((B, Hkv * g, 128), seed=143).to(dev)
+    ws = ea.decode_q8_workspace(B, Hkv * g, Hkv, L, device=dev)
+    run = lambda: ea.ea_hybrid_attn_decode_q8(q, c, sl, m, sink=100, window=5000, block_mask=bm, workspace=ws)
+    o, l = run()
+    for _ in range(60):
+        got = [run() for _ in range(10)]
+        assert all(torch.equal(o, a) and torch.equal(l, b) for a, b in got)
+    check_no_device_error(ws)
