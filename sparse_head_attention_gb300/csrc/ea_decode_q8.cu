@@ -11,7 +11,7 @@
 // A step reads each kept key's 256 bytes once and is bound by HBM: at the
 // measured 6.79 TB/s an SM receives 45 bytes a ns, one 64-key tile of K and V
 // (16 KB) every 0.37 us.
-//   - The producer warp keeps kStages tiles in flight by TMA (one 128-byte
+//   - The producer warp keeps kQ8Stages tiles in flight by TMA (one 128-byte
 //     swizzled box of 64 rows per K or V); its own time per tile counts (700 cycles
 //     at that rate), so its lanes work out 32 tiles' places at once, and the
 //     compute warps load the scales themselves, a tile ahead.  (Scales as 4-byte

@@ -38,7 +38,7 @@
 // Few rows (a decode step, an observation window): one query tile serves all pairs
 // of an item and stays in shared memory; pairs pass through two stages of 64 KB.
 // Bound by the same chain, a pair of tiles at a time (about 2 us each), and by the
-// launch: 64 rows over 32768 keys, 8 KV heads, 26.7 us (69 MB, 2.6 TB/s).
+// launch: 64 rows over 32768 keys, 8 KV heads, 24.5 us (69 MB, 2.8 TB/s).
 //
 // With few key tiles the queries of each are cut into `parts` shares, whose sums
 // go to the workspace and are added in order by a last kernel.
@@ -107,6 +107,7 @@ struct KwArgs {
     int seg, seg_log2;     // query rows of one head in a tile: 128, or 256 for groups of one head
     int box;               // rows of a query box: 128, or all of Tq (rounded up to 16)
     int n_items;
+    int one_each;          // an item or none for each CTA: no queue
     float c2;              // scale * log2(e)
     float inv_scale;
 };
@@ -236,18 +237,25 @@ struct KwHeld {
 };
 
 // ------------------------------------------------------------ setup
-// Re-arms the queue and reports modes, masks and lengths that cannot be used.
-__global__ void __launch_bounds__(256) kw_setup_kernel(const KwArgs a)
+// Reports modes, masks and lengths that cannot be used (threads first, first + step, ...).
+__device__ __forceinline__ void kw_check(const KwArgs &a, int first, int step)
 {
-    griddep_launch_dependents();   // the products' kernel may start its prologue
     bool bad = false;
-    for (int u = threadIdx.x; u < a.B * a.Hkv; u += 256) {
+    for (int u = first; u < a.B * a.Hkv; u += step) {
         const int mode = a.m[u];
         const int L = a.seqlens ? a.seqlens[u / a.Hkv] : a.Lmax;
         bad |= mode > EA_BLOCK || (mode == EA_BLOCK && !a.block_mask) || L < 0 || L > a.Lmax;
     }
-    if (__syncthreads_or(bad) && threadIdx.x == 0)
+    if (bad)
         raise_error(&a.hdr->error, EA_DEVERR_CHECK);
+}
+
+// Re-arms the queue.  With an item for each CTA at most there is none, and a warp of
+// the first CTA checks (64 rows over 32K keys 26.9 -> 24.5 us).
+__global__ void __launch_bounds__(256) kw_setup_kernel(const KwArgs a)
+{
+    griddep_launch_dependents();   // the products' kernel may start its prologue
+    kw_check(a, threadIdx.x, 256);
     if (threadIdx.x == 0)
         a.hdr->work_counter = 0;
 }
@@ -311,7 +319,15 @@ __device__ __forceinline__ void kw_producer(const CUtensorMap *tm_k, const KwMap
     KwRing<QS> q;
     KwHeld held{};
     bool ok = true;
-    auto draw = [&]() { return lane == 0 ? atomicAdd(&a.hdr->work_counter, 1u) : 0u; };
+    uint32_t own = blockIdx.x;                               // one_each: this CTA's item, then none
+    auto draw = [&]() {
+        if (a.one_each) {
+            const uint32_t v = own;
+            own = 0xffffffffu;
+            return v;
+        }
+        return lane == 0 ? atomicAdd(&a.hdr->work_counter, 1u) : 0u;
+    };
     uint32_t next = draw();                                  // drawn an item ahead
     for (int it = 0; ok; ++it) {
         const int slot = it % kWSlots;
@@ -774,6 +790,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
         kw_mma<MANY>(a, sm, tmem, lane);
     else if (warp == 2)
         kw_lse<MANY>(a, sm, lane);
+    else if (warp == 3 && a.one_each && blockIdx.x == 0)
+        kw_check(a, lane, 32);
     else if (warp >= kWFirstWarp)
         kw_sum(a, sm, tmem, warp, lane);
     __syncwarp();
@@ -834,10 +852,11 @@ static KwPlan kw_plan(int B, int Tq, int Lmax, int Hkv, int g)
     return p;
 }
 
-// A kernel whose prologue may run under the end of the call's one before it.
+// A kernel whose prologue may run under the end of the call's one before it, if
+// there is one.
 template <typename... A>
 static cudaError_t launch_kw_after(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t st,
-                                   const A &...args)
+                                   bool follows, const A &...args)
 {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];
@@ -848,7 +867,7 @@ static cudaError_t launch_kw_after(void (*kernel)(A...), dim3 grid, int threads,
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = follows ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -866,7 +885,7 @@ static cudaError_t launch_kw(const CUtensorMap &tk, const KwMaps &tq, const KwAr
             attr_done[dev] = true;
     }
     return launch_kw_after(key_weights_kernel<MANY>, dim3(static_cast<unsigned>(a.n_items < sms ? a.n_items : sms)),
-                           kWThreads, kKwSmemBytes, st, tk, tq, a);
+                           kWThreads, kKwSmemBytes, st, !a.one_each, tk, tq, a);
 }
 
 } // namespace ea
@@ -954,13 +973,15 @@ extern "C" ea_status ea_key_weights(const void *Q, const void *K, const float *L
     if (sms <= 0)
         return EA_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    kw_setup_kernel<<<1, 256, 0, st>>>(a);
+    a.one_each = items <= sms;
+    if (!a.one_each)
+        kw_setup_kernel<<<1, 256, 0, st>>>(a);
     if ((plan.many ? launch_kw<true>(tk, tq, a, sms, dev, st)
                    : launch_kw<false>(tk, tq, a, sms, dev, st)) != cudaSuccess)
         return EA_ERR_CUDA;
     if (a.parts > 1 &&
         launch_kw_after(kw_join_kernel, dim3(static_cast<unsigned>(ceil_div(Lmax, 256)), static_cast<unsigned>(B * Hkv)),
-                        256, 0, st, a) != cudaSuccess)
+                        256, 0, st, true, a) != cudaSuccess)
         return EA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? EA_OK : EA_ERR_CUDA;
 }
