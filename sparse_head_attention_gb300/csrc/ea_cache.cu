@@ -238,6 +238,12 @@ __device__ __forceinline__ uint32_t row_amax(const uint4 &raw, float s)
     }
 }
 
+__device__ __forceinline__ uint32_t times512(uint32_t h)
+{
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(&h), __float2half2_rn(512.f));
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+
 // Stores them as codes of a block of scale 1 / inv (zeros for a NaN scale).
 template <int SRC, bool E4M3>
 __device__ __forceinline__ void put_codes(uint8_t *dst, const uint4 &raw, float s, float inv, bool dead)
@@ -255,13 +261,23 @@ __device__ __forceinline__ void put_codes(uint8_t *dst, const uint4 &raw, float 
             *reinterpret_cast<uint4 *>(dst) = raw;
             return;
         }
-        // the ratio of the scales; it is at most qmax where a code is not 0
-        const __half2 f = __float2half2_rn(fminf(s * inv, 512.f));
+        // The ratio of the scales.  The block's scale is set by its largest value, so no
+        // code times the ratio is beyond qmax, and f16 holds every product.  Int8's codes
+        // are 1 at least, and the ratio 2^8 at most; e4m3's go down to 2^-9, and the ratio
+        // up to 2^17, more than f16 holds: it is then applied as 2^9 and the rest, both
+        // exact.  What is capped is the ratio of a row of zeros.
+        const float ratio = s * inv;
+        const bool two = SRC == EA_CACHE_E4M3 && ratio > 512.f;
+        const __half2 f = __float2half2_rn(fminf(two ? ratio * 0x1p-9f : ratio, 512.f));
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t lo, hi;
             codes_f16<SRC == EA_CACHE_E4M3>(word(raw, i), lo, hi);
+            if (two) {
+                lo = times512(lo);
+                hi = times512(hi);
+            }
             w[i] = dead ? 0u : encode4_f16<E4M3>(lo, hi, f);
         }
         *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);

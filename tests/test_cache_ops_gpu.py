@@ -245,6 +245,35 @@ def test_compact_scale_blocks(dev, sb):
     same_cache(hd, d)
 
 
+@pytest.mark.parametrize("src", [E4M3, INT8])
+@pytest.mark.parametrize("dst", [E4M3, INT8, BF16])
+@pytest.mark.parametrize("outlier", [600.0, 2000.0, 1e4, 3e4, 2e5])
+@pytest.mark.parametrize("sb_dst", [16, 64])
+def test_compact_of_rows_far_below_their_blocks_largest(dev, src, dst, outlier, sb_dst):
+    # every block of the source holds one row `outlier` times larger than the others, which from 3e4 on are all below
+    # e4m3's normal codes and at 2e5 its least one: gathered without that row, their block's scale is up to 2^17 smaller
+    B, Hkv, sb, L = 3, 3, 32, 256
+    s, d = make_cache(B, L, Hkv, src, sb, 64, seed=23), make_cache(B, L, Hkv, dst, sb_dst, 0, seed=24)
+    g = torch.Generator().manual_seed(25)
+    K, V = (torch.randn(B, L, Hkv, 128, generator=g) for _ in range(2))
+    for x in (K, V):
+        x[:, sb - 1 :: sb] *= outlier
+    write_ref(s, K.to(BF16), V.to(BF16), [0] * B, [L] * B)
+    small = torch.arange(L)[torch.arange(L) % sb != sb - 1]
+    index = torch.full((B, Hkv, 193), -1, dtype=torch.int32)
+    index[:] = small[:193]                        # the small rows alone
+    index[1] = small[torch.randperm(len(small), generator=g)[:193]]
+    index[:, 1, 70] = 2 * sb - 1                  # head 1: one block with a large row among them
+    # counts: the last block of a single small row, whole blocks, one row in all
+    counts = [193, 128, 1]
+    hs, hd = handle(s, dev), handle(d, dev)
+    ws = ea.cache_workspace(dev)
+    ea.ea_cache_compact(hs, hd, index.to(dev), torch.tensor(counts, dtype=torch.int32, device=dev), workspace=ws)
+    check_no_device_error(ws)
+    compact_ref(s, d, index, counts, None, None)
+    same_cache(hd, d)
+
+
 def test_compact_of_everything_keeps_the_values(dev):
     # an e4m3 block whose largest value was rounded down to 224 * s gets half the scale: other codes, the same values
     for dtype in (E4M3, INT8):
