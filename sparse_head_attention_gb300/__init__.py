@@ -666,6 +666,8 @@ class KVCache:
 
     K, V: [B, Lmax, Hkv, 128], or with a block_table (int32 [B, max_pages])
     pages [num_pages, page_size, Hkv, 128]; bfloat16, float8_e4m3fn or int8.
+    Sequences may name the same pages, each in a block_table row of its own (an
+    expanded row is refused).
     k_scale, v_scale (8-bit formats): float32 [B or num_pages, Hkv,
     ceil(rows / scale_block)], one scale per block of scale_block tokens and
     head.  ``kv_cache`` and ``kv_cache_paged`` allocate an empty one."""
@@ -696,6 +698,9 @@ class KVCache:
             if block_table.dim() != 2 or block_table.shape[1] < 1 or (
                     block_table.shape[1] > 1 and block_table.stride(1) != 1):
                 raise ValueError("block_table must be [B, max_pages] with unit column stride")
+            if block_table.shape[0] > 1 and block_table.stride(0) < block_table.shape[1]:
+                raise ValueError("block_table's rows overlap: sequences that share pages need a row each "
+                                 "(block_table.contiguous())")
             if self.quantized and rows % scale_block:
                 raise ValueError("pages must hold a multiple of scale_block rows")
         _one_device(K, V, k_scale, v_scale, block_table)
@@ -709,7 +714,8 @@ class KVCache:
                          0 if v_scale is None else v_scale.data_ptr(),
                          (ctypes.c_int64 * 4)(*K.stride()),
                          0 if block_table is None else block_table.data_ptr(),
-                         0 if block_table is None else max(block_table.stride(0), self.max_pages),
+                         # (the row stride of a single row means nothing)
+                         block_table.stride(0) if self.B > 1 and block_table is not None else self.max_pages,
                          outer, rows, self.max_pages, Hkv, d, CACHE_FORMATS[K.dtype], scale_block)
         self._ref = ctypes.byref(self._c)
 

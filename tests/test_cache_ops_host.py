@@ -234,3 +234,33 @@ def test_decode_refuses_splits_that_are_too_long(L):
     long = dict(rows=1 << 20, max_pages=64, bt_stride=64, scale_block=64)
     assert _decode(L, paged(**long), ns=3) == UNSUPPORTED
     assert _decode(L, paged(**long), ns=4, wsb=1024) == WORKSPACE       # 2^24 rows each: as far as the workspace
+
+
+def _pages_on_the_cpu(monkeypatch, table):
+    # the handle alone, over CPU tensors: nothing is launched
+    monkeypatch.setattr(ea, "_dev", lambda t, name, dtype=None: t)
+    K = torch.zeros(8, 64, 2, 128, dtype=torch.int8)
+    s = torch.ones(8, 2, 1)
+    return ea.KVCache(K, K.clone(), s, s.clone(), block_table=table)
+
+
+@pytest.mark.parametrize("B,pages", [(2, 4), (3, 1), (5, 2)])
+def test_binding_refuses_block_tables_whose_rows_overlap(monkeypatch, B, pages):
+    # one prompt's row for all sequences (row stride 0), and rows that begin inside the one before them: sequence b's
+    # row is not b * max_pages entries on, and reading there leaves the tensor
+    row = torch.arange(pages, dtype=torch.int32)
+    with pytest.raises(ValueError, match="block_table"):
+        _pages_on_the_cpu(monkeypatch, row[None].expand(B, -1))
+    if pages > 1:
+        with pytest.raises(ValueError, match="block_table"):
+            _pages_on_the_cpu(monkeypatch, torch.arange(B + pages, dtype=torch.int32).as_strided((B, pages), (1, 1)))
+
+
+def test_binding_passes_the_block_tables_row_stride(monkeypatch):
+    wide = torch.zeros(6, 9, dtype=torch.int32)
+    for table, stride in ((wide, 9), (wide[:, :4], 9), (wide[::2, 3:], 18), (wide[:, :1], 9), (wide.new_zeros(6, 1), 1),
+                          (wide.new_zeros(4)[None], 4), (wide.new_zeros(4).expand(1, -1), 4),
+                          (wide.as_strided((1, 4), (0, 1)), 4), (wide.new_zeros(1, 1).expand(1, 1), 1)):
+        c = _pages_on_the_cpu(monkeypatch, table)
+        assert c._c.bt_stride == stride and c._c.max_pages == table.shape[1]
+        assert all(c._c.bt_stride * b == table[b].storage_offset() - table.storage_offset() for b in range(c.B))
