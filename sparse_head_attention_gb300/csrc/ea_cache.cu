@@ -416,7 +416,12 @@ __global__ void __launch_bounds__(kCacheThreads, SB > 64 ? 3 : SRC == EA_CACHE_B
 #pragma unroll
             for (int i = 0; i < kPasses; ++i)
                 mx = max(mx, row_amax<SRC>(rw[i], s_row[i]));
-            const float s = block_scale(cta_max(mx, red[j]), kE4M3);
+            mx = cta_max(mx, red[j]);
+            // A code whose value was rounded up to 2^128 has a finite scale (a block with a
+            // NaN scale gives a NaN here): the largest fp32 gives the scale that it needs.
+            if (SRC != EA_CACHE_BF16 && mx == 0x7f800000u)
+                mx = 0x7f7fffffu;
+            const float s = block_scale(mx, kE4M3);
             if (threadIdx.x == 0)
                 a.dst.scale[kv][(static_cast<int64_t>(outer) * a.dst.Hkv + h) * a.dst.nsb + row0 / SB] = s;
             const bool dead = isnan(s);

@@ -274,6 +274,25 @@ def test_compact_of_rows_far_below_their_blocks_largest(dev, src, dst, outlier, 
     same_cache(hd, d)
 
 
+@pytest.mark.parametrize("src", [E4M3, INT8])
+@pytest.mark.parametrize("dst", [E4M3, INT8, BF16])
+def test_compact_of_values_that_rounded_up_to_two_to_the_128(dev, src, dst):
+    # the largest bf16 is 255 / 256 of 2^128 and its code stands for 2^128, beyond fp32, with a finite scale: the block of
+    # the destination gets one too (bf16 has no such number and rounds it to infinity)
+    top = float(torch.finfo(BF16).max)
+    s, d = make_cache(1, 64, 2, src, 32, 0, seed=26), make_cache(1, 64, 2, dst, 16, 0, seed=27)
+    K, V = tokens((1, 64, 2, 128), seed=28), tokens((1, 64, 2, 128), seed=29)
+    K[0, 3, 0, 5], V[0, 40, 1, 6] = top, -top
+    write_ref(s, K, V, [0], [64])
+    code = s["K"][0, 3, 0, 5].double() * s["ks"][0, 0, 0].double()
+    assert code == 2.0 ** 128 and torch.isfinite(s["ks"]).all()
+    index = torch.randperm(64, generator=torch.Generator().manual_seed(30)).to(torch.int32).expand(1, 2, 64).contiguous()
+    hs, hd = handle(s, dev), handle(d, dev)
+    ea.ea_cache_compact(hs, hd, index.to(dev), torch.tensor([64], dtype=torch.int32, device=dev))
+    compact_ref(s, d, index, [64], None, None)
+    same_cache(hd, d)
+
+
 def test_compact_of_everything_keeps_the_values(dev):
     # an e4m3 block whose largest value was rounded down to 224 * s gets half the scale: other codes, the same values
     for dtype in (E4M3, INT8):
