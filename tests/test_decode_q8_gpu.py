@@ -367,3 +367,30 @@ def test_equal_calls_give_equal_bits_whatever_cta_takes_a_chunk(dev):
         got = [run() for _ in range(10)]
         assert all(torch.equal(o, a) and torch.equal(l, b) for a, b in got)
     check_no_device_error(ws)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("page", [64, 192])
+def test_keys_of_missing_pages_count_as_zeros(dev, dtype, page):
+    # reported, and read as zeros with a scale of 1: logits of 0, nothing added to the output
+    B, Hkv, g, cap = 5, 3, 4, 768
+    c = make_cache(B, cap, Hkv, dtype, 32, page, seed=151)
+    n = c["table"].shape[1]
+    c["table"][0, 1], c["table"][1, n - 1], c["table"][2] = 12345, -1, c["K"].shape[0]
+    c["table"][3, 0] = -(1 << 31)
+    lens, modes = [768, 768, 700, 200, 500], all_modes(B, Hkv)
+    q = tokens((B, Hkv * g, 128), seed=152)
+    bm = wl.block_mask(B, Hkv, cap, density=0.5, seed=153).numpy()
+    K, V = logical(c)
+    O, LSE, W, (tO, tL, tW) = decode_ref(q, K, V, value_scales(c), lens, modes, 20, 300, SCALE, bm)
+    ws = ea.decode_q8_workspace(B, Hkv * g, Hkv, cap, 0, True, device=dev)
+    kw = torch.zeros(B, Hkv, cap, device=dev)
+    o, l = ea.ea_hybrid_attn_decode_q8(q.to(dev), handle(c, dev), torch.tensor(lens, dtype=torch.int32, device=dev),
+                                       torch.tensor(modes, dtype=torch.uint8, device=dev), sink=20, window=300,
+                                       block_mask=torch.as_tensor(bm).to(dev), key_weights=kw, workspace=ws)
+    assert ea.ea_check_errors(ws) == 6
+    assert (np.abs(o.double().cpu().numpy() - O) <= tO).all()
+    gl = l.double().cpu().numpy()
+    fin = np.isfinite(LSE)
+    assert (np.isneginf(gl) == ~fin).all() and (np.abs(gl[fin] - LSE[fin]) <= tL[fin]).all()
+    assert (np.abs(kw.double().cpu().numpy() - W) <= tW + 2.0 ** -23 * W).all()
