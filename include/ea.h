@@ -545,14 +545,18 @@ ea_status ea_xa_estimate(const void *Q, const void *K, const int64_t q_str[4],
  *   block_table  NULL for a contiguous cache; else device int32 [B][bt_stride]:
  *                row p of sequence b is row p % rows of page
  *                block_table[b][p / rows]; a sequence holds at most
- *                max_pages * rows tokens
- *   scale_block  16, 32, 64 or 128 (ignored for EA_CACHE_BF16); pages hold a
- *                multiple of it
+ *                max_pages * rows tokens.  bt_stride >= max_pages (also
+ *                for one sequence): sequences that share pages to read have
+ *                a row each
+ *   scale_block  16, 32, 64 or 128 (ignored for EA_CACHE_BF16); 8-bit pages
+ *                hold a multiple of it; bf16 pages that ea_cache_write or
+ *                ea_cache_compact write to hold a multiple of 64 rows (else
+ *                EA_ERR_UNSUPPORTED; as a compaction's source any number)
  * Codes and scales are as the operators here write them (powers of two, 2^-64 at
  * least; no NaN code of E4M3): ea_cache_write and ea_cache_compact rely on it.
  * Constraints: d == 128; K, V 16-byte aligned, the strides of the first three
- * dimensions multiples of 16 bytes, head-dim stride 1; a paged sequence's
- * capacity below 2^31.
+ * dimensions multiples of 16 bytes, head-dim stride 1; B and Hkv at most 65535;
+ * a sequence's capacity at most 2^31 - 256.
  *
  * Calls that share a workspace of ea_hybrid_attn_decode_q8 or ea_key_weights
  * must be ordered (one stream, or events), captured and replayed ones among
@@ -597,8 +601,9 @@ size_t ea_cache_workspace_size(void);
  *                NULL: T for all
  * A block that already holds tokens below `start` keeps them: its scale is the
  * larger of the stored one and the new tokens'; if it grows, the codes below
- * `start` are rounded to it in the same launch.  Rows at or behind
- * start + n_new stay as they are.  A sequence whose rows do not fit its
+ * `start` are rounded to it in the same launch.  The codes of rows at or behind
+ * start + n_new stay as they are (in the last block written, under its new
+ * scale: they are no tokens of the sequence).  A sequence whose rows do not fit its
  * capacity, or whose page is outside the cache, is reported by ea_check_errors
  * and nothing is written for it (for a bad page: for the blocks in it).  Pages
  * that receive tokens must belong to one sequence only.  B is c->outer for a
@@ -639,7 +644,8 @@ ea_status ea_evict_select(const float *weights, const int32_t *seqlens, int B, i
  *   weights, weights_out  device float [B][Hkv][src capacity] and
  *                [B][Hkv][dst capacity], contiguous and apart, or both NULL:
  *                the tokens' accumulated weights move with them
- * Rows of dst at or behind counts[b] stay as they are.  An index outside the
+ * The codes of dst's rows at or behind counts[b] stay as they are (in the last
+ * block written, under its new scale).  An index outside the
  * source, or one whose page is outside it, is reported and reads zeros.  src
  * and dst may share pages of one pool as long as no page is read and written;
  * contiguous ones must not overlap (EA_ERR_INVALID_ARG).  keep is at most
@@ -673,8 +679,9 @@ size_t ea_decode_q8_workspace_size(int B, int Hq, int Hkv, int d, int Lmax, int 
  * A kept key of a block with a NaN scale makes its head's O and LSE NaN.
  * Codes and scales behind seqlens[b] are not used, whatever they hold.  Other
  * arguments, modes, masks, constraints and errors as ea_hybrid_attn_decode;
- * pages hold a multiple of 64 rows, and a given num_splits leaves splits of at
- * most 2^24 rows (longer: EA_ERR_UNSUPPORTED).
+ * pages hold a multiple of 64 rows, a given num_splits leaves splits of at
+ * most 2^24 rows, and with key_weights B * Hkv is at most 65535 (else
+ * EA_ERR_UNSUPPORTED).
  */
 ea_status ea_hybrid_attn_decode_q8(const void *q, const ea_cache *cache, void *O, float *LSE,
                                    const int64_t q_str[3], const int64_t o_str[3],
@@ -711,8 +718,8 @@ size_t ea_key_weights_workspace_size(int B, int Tq, int Lmax, int Hq, int Hkv, i
  *   block_mask   device uint8 [B][Hkv][nB][nB], nB = ceil(Lmax / 128), or NULL
  *                if no head is EA_BLOCK
  *   weights      device float [B][Hkv][Lmax] contiguous
- * Constraints: d == 128, Hq % Hkv == 0, Hq / Hkv <= 64, 1 <= Tq,
- * 1 <= Lmax <= 2^21, sink >= 0, window >= 1, scale > 0, block_size == 128;
+ * Constraints: d == 128, Hq % Hkv == 0, Hq / Hkv <= 64, B * Hkv <= 65535,
+ * 1 <= Tq, Lmax <= 2^21, sink >= 0, window >= 1, scale > 0, block_size == 128;
  * base pointers of Q and K 16-byte aligned, their strides multiples of 8
  * elements, head-dim strides 1; the workspace 256-byte aligned.
  */

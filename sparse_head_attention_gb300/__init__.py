@@ -667,7 +667,8 @@ class KVCache:
     K, V: [B, Lmax, Hkv, 128], or with a block_table (int32 [B, max_pages])
     pages [num_pages, page_size, Hkv, 128]; bfloat16, float8_e4m3fn or int8.
     Sequences may name the same pages, each in a block_table row of its own (an
-    expanded row is refused).
+    expanded row is refused).  Pages hold a multiple of scale_block rows; of 64
+    for the decode and, where they are written to, for bfloat16.
     k_scale, v_scale (8-bit formats): float32 [B or num_pages, Hkv,
     ceil(rows / scale_block)], one scale per block of scale_block tokens and
     head.  ``kv_cache`` and ``kv_cache_paged`` allocate an empty one."""

@@ -264,3 +264,12 @@ def test_binding_passes_the_block_tables_row_stride(monkeypatch):
         c = _pages_on_the_cpu(monkeypatch, table)
         assert c._c.bt_stride == stride and c._c.max_pages == table.shape[1]
         assert all(c._c.bt_stride * b == table[b].storage_offset() - table.storage_offset() for b in range(c.B))
+
+
+@pytest.mark.parametrize("rows", [16, 80, 96])
+def test_bf16_pages_of_odd_size_are_read_but_not_written(L, rows):
+    odd = dict(format=BF16, rows=rows, k_scale=None, v_scale=None, max_pages=100, bt_stride=100,
+               kv_str=_str(rows * 8 * 128, 8 * 128, 128, 1))
+    assert _write(L, paged(**odd)) == UNSUPPORTED
+    assert _compact(L, cache(), paged(**odd, **FAR)) == UNSUPPORTED
+    assert _compact(L, paged(**odd), cache(**FAR), ws=None) == WORKSPACE      # accepted as a source, as far as the workspace
