@@ -311,11 +311,11 @@ __device__ __forceinline__ void put_bf16(__nv_bfloat16 *dst, const uint4 &raw, f
 // what counts is how many are in flight: the index is read before the count is
 // known, K's and V's rows are read together (8 bits) or by a CTA each (bf16), and
 // registers are kept low enough for many CTAs (16 per SM with blocks of 32: 31 us,
-// ten: 34).  After that it is instructions (64 % of the issue slots taken):
+// ten: 34).  After that it is instructions (67 % of the issue slots taken):
 // magnitudes are compared as codes, not as numbers (34 -> 31 us), and a row whose
 // scale stays is copied (31 -> 30).
-// Measured: 16 paged int8 caches, 4000 of up to 16384 tokens kept, blocks of 32, 30
-// us (119 MB, 4.0 TB/s; the floor at the measured HBM rate is 17.6); 8192 of 32K
+// Measured: 16 paged int8 caches, 4000 of up to 16384 tokens kept, blocks of 32,
+// 30.6 us (119 MB, 3.9 TB/s; the floor at the measured HBM rate is 17.6); 8192 of 32K
 // bf16 tokens to e4m3, 51 MB, 9.7 us out of L2 and 14.4 out of HBM (floor 7.5; K and
 // V by one CTA 16.3).
 template <int SB, int SRC, int DST>
