@@ -33,7 +33,8 @@
  *   - ea_route, ea_hybrid_attn_prefill, ea_hybrid_attn_prefill_varlen,
  *     ea_hybrid_attn_decode, ea_xa_estimate and the KV cache operators
  *     (ea_cache_write, ea_hybrid_attn_decode_q8, ea_key_weights,
- *     ea_evict_select, ea_cache_compact) enqueue kernels only (no
+ *     ea_evict_select, ea_cache_compact) and those for drafted tokens (ea_rope,
+ *     ea_cache_write_rope, ea_tree_plan, ea_tree_accept) enqueue kernels only (no
  *     allocation, no host synchronisation): after one call on the device
  *     (which raises the kernels' shared-memory limits), a call can be captured
  *     into a CUDA graph and replayed with new contents in the same buffers.
@@ -729,6 +730,118 @@ ea_status ea_key_weights(const void *Q, const void *K, const float *LSE, const i
                          const uint8_t *m, int sink, int window, const uint8_t *block_mask,
                          int block_size, float *weights, int accumulate, void *workspace,
                          size_t ws_bytes, void *stream);
+
+/*
+ * ---------------------------------------------------------- drafted tokens
+ * The operators of a decode step that checks several drafted tokens at once
+ * (speculative decoding), and the position rotation that every step needs.  The
+ * pages have no counterpart: the router's decision, taken once per request,
+ * holds for the drafted tokens as it does for single ones.
+ *
+ * A sequence's T (at most EA_MAX_TREE) drafted tokens form a tree: parents[t] is
+ * the node that t continues (below t), or -1 for a root.  Node t stands at
+ * position seqlens[b] + depth(t).  A step is
+ *   ea_tree_plan       once: depths and ancestors from the parents
+ *   ea_rope            per layer: queries and keys rotated by those positions
+ *   ea_hybrid_attn_tree  per layer: every node attends to the cache and its ancestors
+ *   ea_tree_accept     once: the path whose tokens the model agrees with
+ *   ea_cache_write_rope  per layer: that path's keys and values into the cache
+ * so that a token which is not accepted never reaches the cache.
+ */
+#define EA_MAX_TREE 128
+
+/*
+ * ea_rope - rotate queries and keys by their positions.  For the pairs (i, j) of
+ * the first `rot` dims, (i, i + rot / 2) or (interleaved) (2i, 2i + 1), and
+ * a = p * inv_freq[i]:
+ *   out_i = rope_scale * (x_i cos a - x_j sin a)
+ *   out_j = rope_scale * (x_j cos a + x_i sin a)
+ * and the dims from rot on are copied.  Angles are exact to 2^-31 of a turn at every
+ * position; products and sums are fp32, rounded once.
+ *
+ *   Q, Q_out     device bf16 [B][T][Hq][d], strides q_str / qo_str; Hq = 0: none
+ *   K, K_out     device bf16 [B][T][Hkv][d], strides k_str / ko_str; Hkv = 0: none
+ *   inv_freq     device float [rot / 2], 16-byte aligned, in radians per position,
+ *                each below 2^24 in magnitude (another makes its pair NaN)
+ *   rot          16 .. 128, a multiple of 16
+ *   positions    device int32 [B][T] contiguous, any value
+ *   n_new        device int32 [B], each in [0, T] (else reported by ea_check_errors
+ *                and counted as 0), or NULL: T for all.  Rows at or behind it stay
+ *                as they are.
+ *   workspace    ea_cache_workspace_size() bytes
+ * Q_out may be Q and K_out may be K (with the same strides); other overlaps are
+ * not allowed.  Constraints: d == 128, B <= 65535, base pointers 16-byte aligned,
+ * strides multiples of 8 elements, head-dim strides 1.
+ */
+ea_status ea_rope(const void *Q, void *Q_out, const int64_t q_str[4], const int64_t qo_str[4], int Hq,
+                  const void *K, void *K_out, const int64_t k_str[4], const int64_t ko_str[4], int Hkv,
+                  int B, int T, int d, const float *inv_freq, int rot, int interleaved, float rope_scale,
+                  const int32_t *positions, const int32_t *n_new, void *workspace, size_t ws_bytes,
+                  void *stream);
+
+/*
+ * ea_cache_write_rope - ea_cache_write with the rotation on the way: new token i of
+ * sequence b goes to row start[b] + i of its cache, its key rotated (and, for an 8-bit
+ * cache, quantised from fp32: one rounding), its value as it is.  The new queries are
+ * rotated beside it.
+ *
+ *   c            bf16 or 8-bit cache, as for ea_cache_write, with its rules for blocks
+ *                that already hold tokens
+ *   K_new, V_new device bf16 [B][T][Hkv][d], strides n_str (shared), unrotated
+ *   Q, Q_out     device bf16 [B][T][Hq][d], rows below n_new are rotated into Q_out
+ *                (which may be Q); Hq = 0: none.  Not together with rows.
+ *   rows         device int32 [B][T] or NULL.  Given, new token i is row rows[b][i] of
+ *                K_new and V_new (an accepted path of drafted tokens); one outside
+ *                [0, T) is reported and written as zeros.
+ *   positions    device int32 [B][T]: the position of row t of K_new (and Q), or NULL:
+ *                start[b] + i for new token i
+ *   start, n_new as for ea_cache_write
+ * Rotation, inv_freq, rot, interleaved and rope_scale as for ea_rope; other
+ * constraints and errors as for ea_cache_write.
+ */
+ea_status ea_cache_write_rope(const ea_cache *c, const void *K_new, const void *V_new,
+                              const int64_t n_str[4], const void *Q, void *Q_out,
+                              const int64_t q_str[4], const int64_t qo_str[4], int Hq,
+                              const float *inv_freq, int rot, int interleaved, float rope_scale,
+                              const int32_t *positions, const int32_t *start, const int32_t *n_new,
+                              const int32_t *rows, int B, int T, void *workspace, size_t ws_bytes,
+                              void *stream);
+
+/*
+ * ea_tree_plan - the depth and the ancestors of every node.
+ *
+ *   parents      device int32 [B][T]; one that is not in [-1, t) is reported by
+ *                ea_check_errors and counts as -1
+ *   n_nodes      device int32 [B], each in [0, T] (else reported and counted as 0),
+ *                or NULL: T for all
+ *   depth        device int32 [B][T] (output): 0 for a root
+ *   mask         device int32 [B][T][4] (output), 16-byte aligned: bit u % 32 of word
+ *                u / 32 is set if u is t or an ancestor of it
+ *   workspace    ea_cache_workspace_size() bytes
+ * Entries behind a sequence's last node are 0.  T is at most EA_MAX_TREE.
+ */
+ea_status ea_tree_plan(const int32_t *parents, const int32_t *n_nodes, int B, int T, int32_t *depth,
+                       int32_t *mask, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * ea_tree_accept - the path of a tree that the model agrees with, by its own choice of
+ * token after every node (greedy decoding, or tokens sampled beforehand).
+ *
+ *   tokens       device int32 [B][T]: the token of each node.  Node 0 is the token
+ *                sampled last, whose key is not in the cache yet: always accepted.
+ *   parents      as for ea_tree_plan
+ *   targets      device int32 [B][T]: the model's token after each node
+ *   path         device int32 [B][T] (output): the accepted nodes from node 0 on: each
+ *                is the first child (lowest number) of the one before whose token is
+ *                the target there; -1 behind the last
+ *   n_accepted   device int32 [B] (output): how many, 0 for a sequence without nodes
+ *   next_token   device int32 [B] (output): the target of the last one (the next
+ *                step's node 0), -1 for a sequence without nodes
+ *   n_nodes, workspace, T  as for ea_tree_plan
+ */
+ea_status ea_tree_accept(const int32_t *tokens, const int32_t *parents, const int32_t *targets,
+                         const int32_t *n_nodes, int B, int T, int32_t *path, int32_t *n_accepted,
+                         int32_t *next_token, void *workspace, size_t ws_bytes, void *stream);
 
 /*
  * ea_sparsity_ratios - model sparsity ratio and effective sparsity ratio of one

@@ -18,6 +18,10 @@ present, the device entry points raise instead of computing anything else.
     ea_key_weights           the attention weight that a prefill's queries give its keys
     ea_evict_select          which tokens stay when a cache is cut by those weights
     ea_cache_compact         gathers them into another cache
+    ea_rope                  queries and keys rotated by their positions
+    ea_cache_write_rope      new tokens into a KV cache, rotated on the way
+    ea_tree_plan             depths and ancestors of a tree of drafted tokens
+    ea_tree_accept           the path of the tree that the model agrees with
     ea_sparsity_ratios       Omega_MSR / Omega_ESR (host)
     ea_check_errors          read back the device error word of a workspace
 """
@@ -47,7 +51,8 @@ EXPORTS = ("ea_status_string", "ea_route", "ea_route_layers", "ea_prefill_worksp
            "ea_hybrid_attn_decode", "ea_hybrid_attn_decode_paged", "ea_xa_workspace_size",
            "ea_xa_estimate", "ea_cache_workspace_size", "ea_cache_write", "ea_evict_select",
            "ea_cache_compact", "ea_decode_q8_workspace_size", "ea_hybrid_attn_decode_q8",
-           "ea_key_weights_workspace_size", "ea_key_weights", "ea_sparsity_ratios",
+           "ea_key_weights_workspace_size", "ea_key_weights", "ea_rope", "ea_cache_write_rope",
+           "ea_tree_plan", "ea_tree_accept", "ea_sparsity_ratios",
            "ea_check_errors")
 
 
@@ -160,12 +165,18 @@ def lib():
         L.ea_key_weights_workspace_size.restype = sz
         L.ea_key_weights.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, f32, P, i32,
                                      i32, P, i32, P, i32, P, sz, P]
+        L.ea_rope.argtypes = [P, P, P, P, i32, P, P, P, P, i32, i32, i32, i32, P, i32, i32, f32, P, P, P, sz, P]
+        L.ea_cache_write_rope.argtypes = [P, P, P, P, P, P, P, P, i32, P, i32, i32, f32, P, P, P, P, i32, i32,
+                                          P, sz, P]
+        L.ea_tree_plan.argtypes = [P, P, i32, i32, P, P, P, sz, P]
+        L.ea_tree_accept.argtypes = [P, P, P, P, i32, i32, P, P, P, P, sz, P]
         L.ea_sparsity_ratios.argtypes = [P, P, i32, i32, i32, i32, i32, P, i32,
                                          ctypes.POINTER(f64), ctypes.POINTER(f64)]
         L.ea_check_errors.argtypes = [P, P]
         for f in ("ea_route", "ea_route_layers", "ea_hybrid_attn_prefill", "ea_prefill_plan", "ea_prefill_attend",
                   "ea_hybrid_attn_decode", "ea_cache_write", "ea_evict_select", "ea_cache_compact",
-                  "ea_hybrid_attn_decode_q8", "ea_key_weights", "ea_sparsity_ratios", "ea_check_errors"):
+                  "ea_hybrid_attn_decode_q8", "ea_key_weights", "ea_rope", "ea_cache_write_rope", "ea_tree_plan",
+                  "ea_tree_accept", "ea_sparsity_ratios", "ea_check_errors"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -803,8 +814,9 @@ def _clear_workspace(n, device):
 
 
 def cache_workspace(device="cuda"):
-    """A zeroed workspace of ea_cache_write, ea_evict_select and ea_cache_compact
-    (their error word)."""
+    """A zeroed workspace of ea_cache_write, ea_evict_select, ea_cache_compact,
+    ea_rope, ea_cache_write_rope, ea_tree_plan and ea_tree_accept (their error
+    word)."""
     return torch.zeros(ea_cache_workspace_size(), dtype=torch.uint8, device=device)
 
 
@@ -998,6 +1010,180 @@ def ea_cache_compact(src, dst, index, counts, *, weights=None, weights_out=None,
         _check("ea_cache_compact", lib().ea_cache_compact(
             src._ref, dst._ref, index.data_ptr(), counts.data_ptr(), B, index.shape[2], _ptr(weights),
             _ptr(weights_out), workspace.data_ptr(), workspace.numel(), st))
+
+
+def _rows4(t, name, shape):
+    _dev(t, name, torch.bfloat16)
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must be a %s tensor, got %s" % (name, list(shape), list(t.shape)))
+    return t
+
+
+def _i32_rows(t, name, B, T):
+    return t if t is None else _like(t, name, (B, T), torch.int32)
+
+
+def _strides4(t):
+    return None if t is None else _I64[4](*t.stride())
+
+
+MAX_TREE = 128
+
+
+def ea_rope(Q, K, positions, inv_freq, *, n_new=None, interleaved=False, rope_scale=1.0, Q_out=None,
+            K_out=None, workspace=None, stream=None):
+    """Rotate queries Q [B, T, Hq, 128] and keys K [B, T, Hkv, 128] (bf16, CUDA;
+    either may be None) by positions (int32 [B, T]): the first rot = 2 *
+    len(inv_freq) dims in pairs (i, i + rot / 2), or neighbours (interleaved),
+    by positions * inv_freq (float32, radians per position), times rope_scale.
+    n_new (int32 [B]): rows at or behind it are not written.  Q_out and K_out
+    may be Q and K.  Returns (Q_out, K_out)."""
+    if Q is None and K is None:
+        raise ValueError("Q or K is needed")
+    x = Q if Q is not None else K
+    _dev(x, "Q" if Q is not None else "K", torch.bfloat16)
+    if x.dim() != 4 or x.shape[3] != 128:
+        raise ValueError("Q and K must be [B, T, heads, 128]")
+    B, T = x.shape[:2]
+    if positions is None:
+        raise ValueError("positions is needed")
+    _i32_rows(positions, "positions", B, T)
+    rot = 2 * _like(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32).numel()
+    _i32_vec(n_new, "n_new", B)
+    heads = [0, 0]
+    for k, (t, o, nm) in enumerate(((Q, Q_out, "Q"), (K, K_out, "K"))):
+        if t is None:
+            if o is not None:
+                raise ValueError("%s_out without %s" % (nm, nm))
+            continue
+        if t.dim() != 4:
+            raise ValueError("%s must be [B, T, heads, 128]" % nm)
+        heads[k] = t.shape[2]
+        _rows4(t, nm, (B, T, heads[k], 128))
+        if o is not None:
+            _rows4(o, nm + "_out", (B, T, heads[k], 128))
+    _one_device(x, Q, K, positions, inv_freq, n_new, Q_out, K_out, workspace)
+    with _at(x.device, stream) as st:
+        if Q is not None and Q_out is None:
+            Q_out = Q.new_empty(Q.shape)
+        if K is not None and K_out is None:
+            K_out = K.new_empty(K.shape)
+        if workspace is None:
+            workspace = cache_workspace(x.device)
+        _check("ea_rope", lib().ea_rope(
+            _ptr(Q), _ptr(Q_out), _strides4(Q), _strides4(Q_out), heads[0], _ptr(K), _ptr(K_out),
+            _strides4(K), _strides4(K_out), heads[1], B, T, 128, inv_freq.data_ptr(), rot,
+            1 if interleaved else 0, float(rope_scale), positions.data_ptr(), _ptr(n_new),
+            workspace.data_ptr(), workspace.numel(), st))
+    return Q_out, K_out
+
+
+def ea_cache_write_rope(cache, K, V, inv_freq, *, Q=None, Q_out=None, start=None, n_new=None, rows=None,
+                        positions=None, interleaved=False, rope_scale=1.0, workspace=None, stream=None):
+    """ea_cache_write with the rotation of ea_rope on the way: K, V [B, T, Hkv,
+    128] (bf16, CUDA, unrotated) go to rows start[b] + i of a KVCache of any
+    format, K rotated.  rows (int32 [B, T]): new token i is row rows[b, i] of K
+    and V (an accepted path).  positions (int32 [B, T]) of the rows of K (and
+    Q); None: start[b] + i.  Q [B, T, Hq, 128] (not with rows) is rotated into
+    Q_out (may be Q; allocated if None), which is returned."""
+    _dev(K, "K", torch.bfloat16)
+    _dev(V, "V", torch.bfloat16)
+    if K.dim() != 4 or V.shape != K.shape or V.stride() != K.stride():
+        raise ValueError("K and V must share 4-dimensional shapes and strides")
+    B, T, Hkv, d = K.shape
+    if (B, Hkv, d) != (cache.B, cache.Hkv, 128):
+        raise ValueError("K and V must be [%d, T, %d, 128]" % (cache.B, cache.Hkv))
+    rot = 2 * _like(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32).numel()
+    _i32_vec(start, "start", B)
+    _i32_vec(n_new, "n_new", B)
+    _i32_rows(rows, "rows", B, T)
+    _i32_rows(positions, "positions", B, T)
+    Hq = 0
+    if Q is not None:
+        if rows is not None:
+            raise ValueError("Q and rows do not go together")
+        if Q.dim() != 4:
+            raise ValueError("Q must be [B, T, Hq, 128]")
+        Hq = Q.shape[2]
+        _rows4(Q, "Q", (B, T, Hq, 128))
+        if Q_out is not None:
+            _rows4(Q_out, "Q_out", (B, T, Hq, 128))
+    elif Q_out is not None:
+        raise ValueError("Q_out without Q")
+    _one_device(cache.K, K, V, inv_freq, Q, Q_out, start, n_new, rows, positions, workspace)
+    with _at(cache.device, stream) as st:
+        if Q is not None and Q_out is None:
+            Q_out = Q.new_empty(Q.shape)
+        if workspace is None:
+            workspace = cache_workspace(cache.device)
+        _check("ea_cache_write_rope", lib().ea_cache_write_rope(
+            cache._ref, K.data_ptr(), V.data_ptr(), _I64[4](*K.stride()), _ptr(Q), _ptr(Q_out), _strides4(Q),
+            _strides4(Q_out), Hq, inv_freq.data_ptr(), rot, 1 if interleaved else 0, float(rope_scale),
+            _ptr(positions), _ptr(start), _ptr(n_new), _ptr(rows), B, T, workspace.data_ptr(),
+            workspace.numel(), st))
+    return Q_out
+
+
+def _tree_shape(t, name):
+    _dev(t, name, torch.int32)
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous [B, T] tensor" % name)
+    return t.shape
+
+
+def ea_tree_plan(parents, n_nodes=None, *, depth=None, mask=None, workspace=None, stream=None):
+    """Depth and ancestors of the nodes of drafted trees: parents int32 [B, T]
+    (-1 for a root, else a node before it; T <= 128), n_nodes int32 [B] (None:
+    T).  Returns (depth int32 [B, T], mask int32 [B, T, 4]: bit u % 32 of word
+    u // 32 for the node itself and every ancestor u); zeros behind a
+    sequence's last node."""
+    B, T = _tree_shape(parents, "parents")
+    _i32_vec(n_nodes, "n_nodes", B)
+    _i32_rows(depth, "depth", B, T)
+    if mask is not None:
+        _like(mask, "mask", (B, T, 4), torch.int32)
+    _one_device(parents, n_nodes, depth, mask, workspace)
+    with _at(parents.device, stream) as st:
+        if depth is None:
+            depth = parents.new_empty((B, T))
+        if mask is None:
+            mask = parents.new_empty((B, T, 4))
+        if workspace is None:
+            workspace = cache_workspace(parents.device)
+        _check("ea_tree_plan", lib().ea_tree_plan(
+            parents.data_ptr(), _ptr(n_nodes), B, T, depth.data_ptr(), mask.data_ptr(), workspace.data_ptr(),
+            workspace.numel(), st))
+    return depth, mask
+
+
+def ea_tree_accept(tokens, parents, targets, n_nodes=None, *, path=None, n_accepted=None, next_token=None,
+                   workspace=None, stream=None):
+    """The path of each drafted tree that the model agrees with.  tokens, parents
+    and targets int32 [B, T]: each node's token, its parent, and the model's
+    token after it; node 0 is the token sampled last.  Returns (path int32 [B,
+    T], -1 behind the accepted nodes; n_accepted int32 [B]; next_token int32
+    [B])."""
+    B, T = _tree_shape(tokens, "tokens")
+    for t, nm in ((parents, "parents"), (targets, "targets"), (path, "path")):
+        if t is None and nm != "path":
+            raise ValueError("%s is needed" % nm)
+        _i32_rows(t, nm, B, T)
+    for t, nm in ((n_nodes, "n_nodes"), (n_accepted, "n_accepted"), (next_token, "next_token")):
+        _i32_vec(t, nm, B)
+    _one_device(tokens, parents, targets, n_nodes, path, n_accepted, next_token, workspace)
+    with _at(tokens.device, stream) as st:
+        if path is None:
+            path = tokens.new_empty((B, T))
+        if n_accepted is None:
+            n_accepted = tokens.new_empty(B)
+        if next_token is None:
+            next_token = tokens.new_empty(B)
+        if workspace is None:
+            workspace = cache_workspace(tokens.device)
+        _check("ea_tree_accept", lib().ea_tree_accept(
+            tokens.data_ptr(), parents.data_ptr(), targets.data_ptr(), _ptr(n_nodes), B, T, path.data_ptr(),
+            n_accepted.data_ptr(), next_token.data_ptr(), workspace.data_ptr(), workspace.numel(), st))
+    return path, n_accepted, next_token
 
 
 def ea_sparsity_ratios(r, m, S, *, sink, window, block_masks=None):

@@ -32,26 +32,6 @@ constexpr int kCacheThreads = 128;
 constexpr int kRowThreads = 16;                            // threads of one row: 8 elements each
 constexpr int kRowsPerPass = kCacheThreads / kRowThreads;  // 8
 
-// Row p of sequence b: the cache's outer index and row in it; false (reported)
-// if its page is outside the cache.
-__device__ __forceinline__ bool locate(const CacheDev &c, int b, int p, int &outer, int &row,
-                                       uint32_t *err)
-{
-    if (!c.table) {
-        outer = b;
-        row = p;
-        return true;
-    }
-    const int pg = p / c.rows;
-    row = p - pg * c.rows;
-    outer = c.table[b * c.bt_stride + pg];
-    if (outer >= 0 && outer < c.outer)
-        return true;
-    raise_error(err, EA_DEVERR_CHECK);
-    outer = 0;
-    return false;
-}
-
 // Maximum over the CTA (128 threads).
 __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t *red)
 {
@@ -60,26 +40,6 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t *red)
         red[threadIdx.x / 32] = v;
     __syncthreads();
     return max(max(red[0], red[1]), max(red[2], red[3]));
-}
-
-// Eight bf16 as floats.
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8])
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-
-__device__ __forceinline__ uint32_t amax8(const float (&x)[8])
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-    return m;
 }
 
 struct WriteArgs {

@@ -1,0 +1,97 @@
+"""Plain CPU implementations of the operators for drafted tokens, in 64 bits, written
+from their definitions (imported by those operators' tests)."""
+import math
+
+import numpy as np
+
+FULL, SSA, BLOCK = 0, 1, 2
+
+
+def inv_freq(rot, base=500000.0):
+    """float32 frequencies of a rotation, as a model holds them."""
+    return (base ** (-2.0 * np.arange(rot // 2) / rot)).astype(np.float32)
+
+
+def turn_fraction(pos, f):
+    """pos * f / 2 pi mod 1 of integers and float32 frequencies: exact integers times 1 / 2 pi to 192 bits."""
+    inv2pi = 0x28be60db9391054a7f09d5f47d4d377036d8a5664f10e410  # 1 / 2 pi in units of 2^-192
+    out = np.zeros((len(pos), len(f)))
+    for j, x in enumerate(f):
+        m, e = math.frexp(float(x))
+        m = int(m * 2 ** 24)                        # x = m 2^(e - 24)
+        for i, p in enumerate(pos):
+            shift = 192 + 24 - e
+            v = (int(p) * m * inv2pi) % (1 << shift)
+            out[i, j] = (v >> (shift - 60)) / 2.0 ** 60
+    return out
+
+
+def rotate(x, pos, f, interleaved, scale=1.0):
+    """x float64 [n, H, 128] at positions [n]; f float32 [rot / 2]."""
+    rot = 2 * len(f)
+    a = 2 * math.pi * turn_fraction(pos, f)[:, None, :]
+    c, s = np.cos(a) * scale, np.sin(a) * scale
+    y = x.copy()
+    i = slice(0, rot, 2) if interleaved else slice(0, rot // 2)
+    j = slice(1, rot, 2) if interleaved else slice(rot // 2, rot)
+    y[..., i] = x[..., i] * c - x[..., j] * s
+    y[..., j] = x[..., j] * c + x[..., i] * s
+    return y
+
+
+def rotate_error(x, f, interleaved, scale=1.0):
+    """How far an fp32 rotation may be off: the angle is off by pi 2^-31 of truncation and pi 2^-24 of rounding, the sine
+    and cosine by 2 ulp (2^-23), each product and sum by 2^-24: in all below 2^-21 of |x_i| + |x_j|."""
+    rot = 2 * len(f)
+    e = np.zeros_like(x)
+    i = slice(0, rot, 2) if interleaved else slice(0, rot // 2)
+    j = slice(1, rot, 2) if interleaved else slice(rot // 2, rot)
+    e[..., i] = e[..., j] = (np.abs(x[..., i]) + np.abs(x[..., j])) * 2.0 ** -21 * abs(scale)
+    return e
+
+
+def plan(parents, n):
+    """depth [B, T], mask int32 [B, T, 4]."""
+    B, T = parents.shape
+    depth, mask = np.zeros((B, T), np.int32), np.zeros((B, T, 4), np.uint32)
+    for b in range(B):
+        for t in range(n[b]):
+            u = t
+            while True:
+                mask[b, t, u // 32] |= np.uint32(1 << (u % 32))
+                p = int(parents[b, u])
+                if not 0 <= p < u:
+                    break
+                u = p
+                depth[b, t] += 1
+    return depth, mask.view(np.int32)
+
+
+def accept(tokens, parents, targets, n):
+    B, T = parents.shape
+    path, count, nxt = np.full((B, T), -1, np.int32), np.zeros(B, np.int32), np.full(B, -1, np.int32)
+    for b in range(B):
+        at = 0 if n[b] else None
+        while at is not None:
+            path[b, count[b]] = at
+            count[b] += 1
+            nxt[b] = targets[b, at]
+            kids = [t for t in range(at + 1, n[b]) if parents[b, t] == at and tokens[b, t] == targets[b, at]]
+            at = kids[0] if kids else None
+    return path, count, nxt
+
+
+def random_tree(B, T, seed, kind="tree"):
+    r = np.random.RandomState(seed)
+    p = np.full((B, T), -1, np.int32)
+    for b in range(B):
+        for t in range(1, T):
+            if kind == "chain":
+                p[b, t] = t - 1
+            elif kind == "star":
+                p[b, t] = 0
+            elif kind == "forest":
+                p[b, t] = r.randint(-1, t)
+            else:
+                p[b, t] = r.randint(0, t)
+    return p
