@@ -34,7 +34,7 @@
  *     ea_hybrid_attn_decode, ea_xa_estimate and the KV cache operators
  *     (ea_cache_write, ea_hybrid_attn_decode_q8, ea_key_weights,
  *     ea_evict_select, ea_cache_compact) and those for drafted tokens (ea_rope,
- *     ea_cache_write_rope, ea_tree_plan, ea_tree_accept) enqueue kernels only (no
+ *     ea_cache_write_rope, ea_tree_plan, ea_hybrid_attn_tree, ea_tree_accept) enqueue kernels only (no
  *     allocation, no host synchronisation): after one call on the device
  *     (which raises the kernels' shared-memory limits), a call can be captured
  *     into a CUDA graph and replayed with new contents in the same buffers.
@@ -822,6 +822,57 @@ ea_status ea_cache_write_rope(const ea_cache *c, const void *K_new, const void *
  */
 ea_status ea_tree_plan(const int32_t *parents, const int32_t *n_nodes, int B, int T, int32_t *depth,
                        int32_t *mask, void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of device workspace ea_hybrid_attn_tree needs (0 on invalid sizes). */
+size_t ea_tree_workspace_size(int B, int T, int Hq, int Hkv, int d, int Lmax);
+
+/*
+ * ea_hybrid_attn_tree - hybrid-head attention of every sequence's drafted tokens over
+ * its cache and over one another (T = 1: a decode step whose token is not in the cache
+ * yet).
+ *
+ * Node t of sequence b stands at position i = seqlens[b] + depth[b][t].  It keeps
+ *   - key j < seqlens[b] of the cache if the head's mode keeps it at position i
+ *     (EA_FULL: all; EA_SSA: j < sink or i - j < window; EA_BLOCK:
+ *     block_mask[b][h][i / 128][j / 128] != 0), and
+ *   - the tree's node u if bit u of mask[b][t] is set, u < n_nodes[b], and the mode
+ *     keeps position seqlens[b] + depth[b][u] at i by the same rule,
+ * so that a node's output is the decode's on a cache that holds its path.
+ * O[b][t][qh][:] = softmax(scale * q . k) V over the kept keys, LSE[b][qh][t] their
+ * natural log-sum-exp; none kept: O = 0, LSE = -inf.  What a row does not keep never
+ * reaches it, infinities and NaN among them.
+ *
+ *   Q, O         device bf16 [B][T][Hq][d], strides q_str / o_str
+ *   K, V         device bf16 [B][T][Hkv][d], strides kv_str (shared): the drafted
+ *                tokens' keys (rotated) and values
+ *   cache        bf16 or 8-bit, contiguous or paged (pages hold a multiple of 64 rows);
+ *                Lmax below is its capacity per sequence
+ *   LSE          device float [B][Hq][T] contiguous, or NULL
+ *   seqlens      device int32 [B], each in [0, Lmax]: tokens in the cache, the drafted
+ *                ones not among them
+ *   n_nodes      device int32 [B], each in [0, T], or NULL: T for all.  Rows at or
+ *                behind it stay as they are.
+ *   depth        device int32 [B][T], below n_nodes[b]; mask device int32 [B][T][4],
+ *                16-byte aligned (ea_tree_plan's)
+ *   block_mask   device uint8 [B][Hkv][nB][nB], nB = ceil(Lmax / 128), or NULL if no head
+ *                is EA_BLOCK; such a head needs seqlens[b] + n_nodes[b] <= 128 nB
+ *   workspace    ea_tree_workspace_size(B, T, Hq, Hkv, d, Lmax) bytes; calls that share
+ *                it must be ordered, captured and replayed ones among them
+ * A length, count, depth, mode or mask that is out of range is reported by
+ * ea_check_errors (a bad length, mode or mask: its head's rows get O = 0, LSE = -inf; a
+ * bad count: no rows; a bad depth: the nearest valid one); a page outside the cache reads
+ * zeros.  Equal calls give equal bits.
+ * Constraints: d == 128, 1 <= T <= EA_MAX_TREE, Hq % Hkv == 0, Hq / Hkv <= 64, B and Hkv
+ * at most 65535, sink >= 0, window >= 1, scale > 0, block_size == 128; base pointers
+ * 16-byte aligned, strides multiples of 8 elements, head-dim strides 1.
+ */
+ea_status ea_hybrid_attn_tree(const void *Q, const void *K, const void *V, const ea_cache *cache,
+                              void *O, float *LSE, const int64_t q_str[4], const int64_t kv_str[4],
+                              const int64_t o_str[4], const int32_t *seqlens,
+                              const int32_t *n_nodes, const int32_t *depth, const int32_t *mask,
+                              int B, int T, int Hq, float scale, const uint8_t *m, int sink,
+                              int window, const uint8_t *block_mask, int block_size,
+                              void *workspace, size_t ws_bytes, void *stream);
 
 /*
  * ea_tree_accept - the path of a tree that the model agrees with, by its own choice of

@@ -21,6 +21,7 @@ present, the device entry points raise instead of computing anything else.
     ea_rope                  queries and keys rotated by their positions
     ea_cache_write_rope      new tokens into a KV cache, rotated on the way
     ea_tree_plan             depths and ancestors of a tree of drafted tokens
+    ea_hybrid_attn_tree      the tree's attention over a cache and over itself
     ea_tree_accept           the path of the tree that the model agrees with
     ea_sparsity_ratios       Omega_MSR / Omega_ESR (host)
     ea_check_errors          read back the device error word of a workspace
@@ -52,7 +53,7 @@ EXPORTS = ("ea_status_string", "ea_route", "ea_route_layers", "ea_prefill_worksp
            "ea_xa_estimate", "ea_cache_workspace_size", "ea_cache_write", "ea_evict_select",
            "ea_cache_compact", "ea_decode_q8_workspace_size", "ea_hybrid_attn_decode_q8",
            "ea_key_weights_workspace_size", "ea_key_weights", "ea_rope", "ea_cache_write_rope",
-           "ea_tree_plan", "ea_tree_accept", "ea_sparsity_ratios",
+           "ea_tree_plan", "ea_tree_workspace_size", "ea_hybrid_attn_tree", "ea_tree_accept", "ea_sparsity_ratios",
            "ea_check_errors")
 
 
@@ -169,6 +170,10 @@ def lib():
         L.ea_cache_write_rope.argtypes = [P, P, P, P, P, P, P, P, i32, P, i32, i32, f32, P, P, P, P, i32, i32,
                                           P, sz, P]
         L.ea_tree_plan.argtypes = [P, P, i32, i32, P, P, P, sz, P]
+        L.ea_tree_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+        L.ea_tree_workspace_size.restype = sz
+        L.ea_hybrid_attn_tree.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, P, i32, i32, i32, f32, P, i32, i32, P,
+                                          i32, P, sz, P]
         L.ea_tree_accept.argtypes = [P, P, P, P, i32, i32, P, P, P, P, sz, P]
         L.ea_sparsity_ratios.argtypes = [P, P, i32, i32, i32, i32, i32, P, i32,
                                          ctypes.POINTER(f64), ctypes.POINTER(f64)]
@@ -176,7 +181,7 @@ def lib():
         for f in ("ea_route", "ea_route_layers", "ea_hybrid_attn_prefill", "ea_prefill_plan", "ea_prefill_attend",
                   "ea_hybrid_attn_decode", "ea_cache_write", "ea_evict_select", "ea_cache_compact",
                   "ea_hybrid_attn_decode_q8", "ea_key_weights", "ea_rope", "ea_cache_write_rope", "ea_tree_plan",
-                  "ea_tree_accept", "ea_sparsity_ratios", "ea_check_errors"):
+                  "ea_hybrid_attn_tree", "ea_tree_accept", "ea_sparsity_ratios", "ea_check_errors"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -1154,6 +1159,64 @@ def ea_tree_plan(parents, n_nodes=None, *, depth=None, mask=None, workspace=None
             parents.data_ptr(), _ptr(n_nodes), B, T, depth.data_ptr(), mask.data_ptr(), workspace.data_ptr(),
             workspace.numel(), st))
     return depth, mask
+
+
+def ea_tree_workspace_size(B, T, Hq, Hkv, Lmax, d=128):
+    return int(lib().ea_tree_workspace_size(B, T, Hq, Hkv, d, Lmax))
+
+
+def tree_workspace(B, T, Hq, Hkv, Lmax, d=128, device="cuda"):
+    """A workspace of ea_hybrid_attn_tree for a cache of Lmax rows a sequence, its
+    error word zero."""
+    n = ea_tree_workspace_size(B, T, Hq, Hkv, Lmax, d)
+    if n == 0:
+        raise ValueError("unsupported tree sizes")
+    return _clear_workspace(n, device)
+
+
+def ea_hybrid_attn_tree(Q, K, V, cache, seqlens, depth, mask, m, *, sink, window, n_nodes=None, block_mask=None,
+                        scale=None, O=None, LSE=None, workspace=None, stream=None, want_lse=True):
+    """Attention of every sequence's drafted tokens over its KVCache and over one
+    another: Q [B, T, Hq, 128], K, V [B, T, Hkv, 128] bf16 (the drafted tokens',
+    rotated; T <= 128), seqlens int32 [B] (tokens in the cache), depth int32 [B,
+    T] and mask int32 [B, T, 4] of ea_tree_plan, m uint8 [B, Hkv], n_nodes int32
+    [B] (None: T; rows at or behind it are not written), block_mask uint8 [B,
+    Hkv, nB, nB] (nB = ceil(capacity / 128)) when a head is BLOCK; all CUDA.
+    Returns (O [B, T, Hq, 128], LSE float32 [B, Hq, T])."""
+    for t, nm in ((Q, "Q"), (K, "K"), (V, "V")):
+        _dev(t, nm, torch.bfloat16)
+    if Q.dim() != 4 or Q.shape[0] != cache.B or Q.shape[3] != 128:
+        raise ValueError("Q must be [%d, T, Hq, 128]" % cache.B)
+    B, T, Hq, d = Q.shape
+    if tuple(K.shape) != (B, T, cache.Hkv, 128) or V.shape != K.shape or V.stride() != K.stride():
+        raise ValueError("K and V must be [%d, %d, %d, 128] and share strides" % (B, T, cache.Hkv))
+    for t, nm in ((seqlens, "seqlens"), (depth, "depth"), (mask, "mask")):
+        if t is None:
+            raise ValueError("%s is needed" % nm)
+    _i32_vec(seqlens, "seqlens", B)
+    _i32_vec(n_nodes, "n_nodes", B)
+    _i32_rows(depth, "depth", B, T)
+    _like(mask, "mask", (B, T, 4), torch.int32)
+    _like(m, "m", (B, cache.Hkv), torch.uint8)
+    bm = _block_mask_arg(block_mask, B, cache.Hkv, cache.capacity)
+    if O is not None:
+        _rows4(O, "O", (B, T, Hq, 128))
+    if LSE is not None:
+        _like(LSE, "LSE", (B, Hq, T), torch.float32)
+    _one_device(cache.K, Q, K, V, seqlens, n_nodes, depth, mask, m, bm, O, LSE, workspace)
+    with _at(cache.device, stream) as st:
+        if O is None:
+            O = Q.new_empty(Q.shape)
+        if LSE is None and want_lse:
+            LSE = Q.new_empty((B, Hq, T), dtype=torch.float32)
+        if workspace is None:
+            workspace = tree_workspace(B, T, Hq, cache.Hkv, cache.capacity, d, Q.device)
+        _check("ea_hybrid_attn_tree", lib().ea_hybrid_attn_tree(
+            Q.data_ptr(), K.data_ptr(), V.data_ptr(), cache._ref, O.data_ptr(), _ptr(LSE), _I64[4](*Q.stride()),
+            _I64[4](*K.stride()), _I64[4](*O.stride()), seqlens.data_ptr(), _ptr(n_nodes), depth.data_ptr(),
+            mask.data_ptr(), B, T, Hq, 1.0 / math.sqrt(d) if scale is None else float(scale), m.data_ptr(), int(sink),
+            int(window), _ptr(bm), TILE, workspace.data_ptr(), workspace.numel(), st))
+    return O, LSE
 
 
 def ea_tree_accept(tokens, parents, targets, n_nodes=None, *, path=None, n_accepted=None, next_token=None,

@@ -145,6 +145,26 @@ bool encode_tmap_bf16_4d(void *tmap_out, const void *base, int d, int H, int S, 
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_bf16_rows(void *tmap_out, const void *base, int H, int S, int B,
+                           const int64_t strides_elems[4], int box_heads, int box_rows)
+{
+    auto fn = get_encode_fn();
+    if (!fn)
+        return false;
+    cuuint64_t dims[4] = {EA_HEAD_DIM, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(S),
+                          static_cast<cuuint64_t>(B)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(strides_elems[2]) * 2,
+                             static_cast<cuuint64_t>(strides_elems[1]) * 2,
+                             static_cast<cuuint64_t>(strides_elems[0]) * 2};
+    cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows), 1u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    CUresult r = fn(reinterpret_cast<CUtensorMap *>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                    const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool encode_tmap_u8_4d(void *tmap_out, const void *base, int d, int H, int S, int B,
                        const int64_t strides_elems[4], int box_rows)
 {

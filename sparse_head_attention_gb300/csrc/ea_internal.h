@@ -86,6 +86,11 @@ bool encode_tmap_bf16_4d(void *tmap_out, const void *base, int d, int H, int S, 
                          const int64_t strides_elems[4], int box_inner, int box_rows,
                          bool swizzle128);
 
+// The same dims with a 64 x box_heads x box_rows x 1 box and 128-byte swizzle: rows of
+// several neighbouring heads, token by token.
+bool encode_tmap_bf16_rows(void *tmap_out, const void *base, int H, int S, int B,
+                           const int64_t strides_elems[4], int box_heads, int box_rows);
+
 // Encodes a 4-D map of 8-bit elements (same dims) with a 128 x 1 x box_rows x 1
 // box and 128-byte swizzle; d must be 128.
 bool encode_tmap_u8_4d(void *tmap_out, const void *base, int d, int H, int S, int B,

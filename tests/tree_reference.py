@@ -95,3 +95,47 @@ def random_tree(B, T, seed, kind="tree"):
             else:
                 p[b, t] = r.randint(0, t)
     return p
+
+
+def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, scale, bm=None):
+    """ea_hybrid_attn_tree in 64 bits.  Q [B, T, Hq, 128], K, V [B, T, Hkv, 128], Kc, Vc [B, cap, Hkv, 128] float64.
+    Returns O [B, T, Hq, 128], LSE [B, Hq, T] and how far an fp32 kernel with bf16 probabilities may be off:
+      a product q . k sums 128 fp32 terms: 2^-17 of sum |q k|, times scale: a logit's error; its exponent is one fused
+      multiply-add of up to 2^6 (2^-18 relative to p) and the exponential 2^-22;
+      a probability is rounded to bf16 (2^-8), the output too; sums over keys are fp32 in tiles of 128 (2^-17) that are
+      joined by weights of 2^-20."""
+    B, T, Hq, D = Q.shape
+    Hkv = K.shape[2]
+    g = Hq // Hkv
+    O, LSE = np.zeros((B, T, Hq, D)), np.full((B, Hq, T), -np.inf)
+    tO, tL = np.zeros((B, T, Hq, D)), np.zeros((B, Hq, T))
+    for b in range(B):
+        L, nb = lens[b], n[b]
+        pos = L + depth[b, :nb].astype(np.int64)
+        at = np.concatenate([np.arange(L), pos])
+        up = ((mask[b, :nb].view(np.uint32)[:, :, None] >> np.arange(32, dtype=np.uint32)) & 1).reshape(nb, 128)[:, :nb].astype(bool)
+        for h in range(Hkv):
+            k = np.concatenate([Kc[b, :L, h], K[b, :nb, h]])
+            v = np.concatenate([Vc[b, :L, h], V[b, :nb, h]])
+            keep = np.concatenate([np.ones((nb, L), bool), up], 1)
+            if modes[b][h] == SSA:
+                keep &= (at[None] < sink) | (pos[:, None] - at[None] < window)
+            elif modes[b][h] == BLOCK:
+                keep &= bm[b, h][pos // 128][:, at // 128] != 0
+            for t in range(nb):
+                j = np.flatnonzero(keep[t])
+                if not len(j):
+                    continue
+                q = Q[b, t, h * g : (h + 1) * g]
+                x = q @ k[j].T * scale
+                e = (np.abs(q) @ np.abs(k[j]).T * scale).max(1) * 2.0 ** -17 + 2.0 ** -17
+                top = x.max(1, keepdims=True)
+                p = np.exp(x - top)
+                s = p.sum(1, keepdims=True)
+                p /= s
+                hs = slice(h * g, (h + 1) * g)
+                O[b, t, hs] = p @ v[j]
+                LSE[b, hs, t] = (top + np.log(s))[:, 0]
+                tO[b, t, hs] = (p @ np.abs(v[j])) * (2.0 ** -8 + 2 * e[:, None]) + np.abs(O[b, t, hs]) * 2.0 ** -8
+                tL[b, hs, t] = e + np.abs(LSE[b, hs, t]) * 2.0 ** -20
+    return O, LSE, tO, tL
