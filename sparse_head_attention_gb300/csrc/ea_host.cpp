@@ -165,8 +165,8 @@ bool encode_tmap_bf16_rows(void *tmap_out, const void *base, int H, int S, int B
     return r == CUDA_SUCCESS;
 }
 
-bool encode_tmap_u8_4d(void *tmap_out, const void *base, int d, int H, int S, int B,
-                       const int64_t strides_elems[4], int box_rows)
+static bool encode_tmap_u8(void *tmap_out, const void *base, int d, int H, int S, int B,
+                           const int64_t strides_elems[4], int box_rows, CUtensorMapSwizzle swizzle)
 {
     auto fn = get_encode_fn();
     if (!fn || d != 128)
@@ -182,9 +182,21 @@ bool encode_tmap_u8_4d(void *tmap_out, const void *base, int d, int H, int S, in
     // head's row with it, which may not be wanted (a streaming head) or not yet.
     CUresult r = fn(reinterpret_cast<CUtensorMap *>(tmap_out), CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                     const_cast<void *>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
+}
+
+bool encode_tmap_u8_4d(void *tmap_out, const void *base, int d, int H, int S, int B,
+                       const int64_t strides_elems[4], int box_rows)
+{
+    return encode_tmap_u8(tmap_out, base, d, H, S, B, strides_elems, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+bool encode_tmap_u8_plain(void *tmap_out, const void *base, int H, int S, int B,
+                          const int64_t strides_elems[4], int box_rows)
+{
+    return encode_tmap_u8(tmap_out, base, EA_HEAD_DIM, H, S, B, strides_elems, box_rows, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 bool encode_tmap_bf16_cells(void *tmap_out, const void *base, int d, int H, int stride, int nA,

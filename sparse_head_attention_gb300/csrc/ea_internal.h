@@ -96,6 +96,10 @@ bool encode_tmap_bf16_rows(void *tmap_out, const void *base, int H, int S, int B
 bool encode_tmap_u8_4d(void *tmap_out, const void *base, int d, int H, int S, int B,
                        const int64_t strides_elems[4], int box_rows);
 
+// Encodes a 4-D map of 8-bit elements with a 128 x 1 x box_rows x 1 box, not swizzled.
+bool encode_tmap_u8_plain(void *tmap_out, const void *base, int H, int S, int B,
+                          const int64_t strides_elems[4], int box_rows);
+
 // Encodes a 5-D bf16 TMA tensor map that reads tokens as cells of `stride`
 // consecutive tokens: dims (head dim, heads, offset u in the cell, cell a,
 // batch), token a * stride + u; the sequence length must be nA * stride.  Box:

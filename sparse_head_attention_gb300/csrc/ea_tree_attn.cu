@@ -23,7 +23,7 @@
 //   warps 0-7    two softmax warpgroups.  With two M tiles each has one; with one they take
 //                key tiles in turn, each with its own O, m and l, joined at the range's end.
 //   warp 8       ranges, Q, and by TMA the K and V tiles into a ring of 32 KB entries
-//   warp 9       the MMAs, whichever product is ready first: S up to two tiles ahead
+//   warp 9       the MMAs: S two tiles ahead of the products that use them
 //   warps 10-11  V's rows that no query row keeps are zeroed before the product (0 * NaN is
 //                NaN), and tiles of which some rows keep a key and others do not are searched
 //                for infinities and NaN; such a tile's product is taken by the softmax warps,
@@ -41,8 +41,7 @@ namespace ea {
 constexpr int kTTile = 128;
 constexpr int kTBytes = kTTile * EA_HEAD_DIM * 2;     // a tile of K, V or Q: 32 KB
 constexpr int kTHalf = kTBytes / 2;                   // 64 dims of 128 rows
-constexpr int kTStages = 5;
-constexpr int kTInfos = 16;                           // tile descriptions in flight: the ring holds three tiles
+constexpr int kTInfos = 8;                            // tile descriptions in flight: the rings and S hold six tiles at most
 constexpr int kTReady = 8;
 constexpr int kTSegs = 4;
 constexpr int kTProducerWarp = 8, kTMmaWarp = 9, kTFixWarp = 10, kTFixWarps = 2, kTConvWarp = 12, kTConvWarps = 8;
@@ -51,9 +50,10 @@ constexpr uint32_t kTColO = 256;                      // TMEM: S0, S1, O0, O1
 constexpr uint32_t kTIdescQK = idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t kTIdescPV = idesc_bf16_f32(128, 128, false, true);
 constexpr float kTGrow = 8.f;                         // the maximum is followed once it grew by 2^8: p <= 2^8
+constexpr int kTMinTiles = 2;                         // of a range at least (a power of two)
 constexpr int kTSms = 152;                            // a workspace's size depends on the grid
 
-enum { kEdge = 1, kDraft = 2, kRow0 = 4, kRow1 = 8, kMixed = 16 };
+enum { kEdge = 1, kDraft = 2, kRow0 = 4, kRow1 = 8, kMixed = 16, kGroups = 8 };   // (from bit 8 on: 16-key groups)
 
 struct TreeArgs {
     __nv_bfloat16 *O;
@@ -68,7 +68,7 @@ struct TreeArgs {
     float *part_o, *part_lse;            // [2 * grid][rows_slot][128], [2 * grid][rows_slot]
     ea_ws_header *hdr;
     CacheDev c;
-    int B, T, Hq, Hkv, g, tpt, pairs, nBm, sink, window, min_tiles, box128, rows_slot;
+    int B, T, Hq, Hkv, g, tpt, pairs, nBm, sink, window, box128, rows_slot;
     float scale_log2, grow;
 };
 
@@ -119,7 +119,7 @@ __device__ __forceinline__ TreeUnit tree_unit(const TreeArgs &a, int u)
         x.need = (x.L + x.n - 1) / EA_TILE > x.L / EA_TILE ? kRow0 | kRow1 : kRow0;
     }
     x.nt = tiles + 1;
-    x.pairs = x.n > 0 ? ((x.n + a.tpt - 1) / a.tpt + 1) / 2 : 0;
+    x.pairs = x.n <= 0 ? 0 : a.pairs == 1 ? 1 : ((x.n + a.tpt - 1) / a.tpt + 1) / 2;
     return x;
 }
 
@@ -135,16 +135,20 @@ struct TreeSeg {
 
 struct TreeTile {
     int key0, flags;
+    int outer[2], row[2];                // where its halves lie in the cache (row < 0: not read; outer < 0: zeros)
 };
+
+// The tile of the tree's own keys.
+__device__ __forceinline__ TreeTile tree_own_tile(int L, int n)
+{
+    return TreeTile{L, kEdge | kDraft | kMixed | ((n + 15) / 16) << kGroups, {0, 0}, {0, 0}};
+}
 
 __device__ __forceinline__ TreeTile tree_tile(const TreeArgs &a, const TreeUnit &x, int u, int t)
 {
-    TreeTile r;
-    if (t >= x.nt - 1) {
-        r.key0 = x.L;
-        r.flags = kEdge | kDraft | kMixed;
-        return r;
-    }
+    TreeTile r{};
+    if (t >= x.nt - 1)
+        return tree_own_tile(x.L, x.n);
     r.flags = 0;
     if (x.mode == EA_BLOCK) {
         const int64_t at = static_cast<int64_t>(u) * a.nBm + t;
@@ -161,14 +165,23 @@ __device__ __forceinline__ TreeTile tree_tile(const TreeArgs &a, const TreeUnit 
     }
     if (r.key0 + kTTile > x.L)
         r.flags |= kEdge;
+    r.flags |= ((min(kTTile, x.L - r.key0) + 15) / 16) << kGroups;
     return r;
 }
 
+// Shared memory is what bounds the bytes on their way: a second M tile's queries take one
+// ring entry's place, and an 8-bit cache's codes two.
+template <bool Q8_, bool TWO>
 struct __align__(1024) TreeSmem {
-    uint8_t q[2][kTBytes];
-    uint8_t ring[kTStages][kTBytes];
+    static constexpr bool Q8 = Q8_;
+    static constexpr int kStages = Q8 ? 4 : TWO ? 5 : 6;       // ring entries: K or V tiles, in turn
+    static constexpr int kCodes = Q8 ? (TWO ? 2 : 4) : 1;      // tiles of codes, K and V in turn
+    uint8_t q[TWO ? 2 : 1][kTBytes];
+    uint8_t ring[kStages][kTBytes];
+    uint8_t code[kCodes][Q8 ? kTBytes / 2 : 16];
     float2 ml[2][kTTile];                // a warpgroup's maximum and sum of each row; before: the scan
-    uint64_t full[kTStages], empty[kTStages];
+    uint64_t full[kStages], empty[kStages];
+    uint64_t code_full[kCodes], code_empty[kCodes];
     uint64_t ready[kTReady];             // V has been looked over
     uint64_t seg_full[kTSegs], seg_empty[kTSegs];
     uint64_t q_full, q_empty;
@@ -177,35 +190,70 @@ struct __align__(1024) TreeSmem {
     TreeSeg seg[kTSegs];
     TreeTile tile[kTInfos];
     int odd[kTReady][kTFixWarps];        // V holds an infinity or a NaN
-    int64_t count, off;                  // this CTA's range: tiles, and its start in the first unit
-    int unit;
+    TreeUnit unit;                       // this CTA's range: its first unit,
+    int u, off, count;                   // where it starts in it, and its tiles
     uint32_t tmem_base;
     int abort;
 };
-constexpr size_t kTSmemBytes = sizeof(TreeSmem);
-static_assert(kTSmemBytes <= 232448, "shared memory of one CTA");
+static_assert(sizeof(TreeSmem<false, false>) <= 232448 && sizeof(TreeSmem<false, true>) <= 232448 &&
+                  sizeof(TreeSmem<true, false>) <= 232448 && sizeof(TreeSmem<true, true>) <= 232448,
+              "shared memory of one CTA");
 
-__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+// The tensor core's instructions where `go` is set (one thread of the warp): predicated, not
+// branched around, so that the warp's flow stays uniform.
+__device__ __forceinline__ void mma_ss(uint32_t go, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate)
 {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity)
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(go)
                  : "memory");
-    return ok != 0;
 }
 
-// D[tmem] (+)= A[tmem] * B[smem].
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t go, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate)
 {
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(go)
                  : "memory");
+}
+
+__device__ __forceinline__ void commit_if(uint32_t go, uint64_t *bar)
+{
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+                 "r"(go)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
+// 32 lanes x 16 columns of 32-bit TMEM -> 16 registers per thread.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// Keeps the registers of a TMEM load behind the wait for it (the compiler sees no
+// dependence between the two).
+__device__ __forceinline__ void tie32(uint32_t (&r)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        asm volatile("" : "+r"(r[i]));
 }
 
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr)
@@ -230,7 +278,8 @@ __device__ __forceinline__ uint32_t cols_below(int n, int c)
 }
 
 // Segment number `it` (slot it % kTSegs), by a whole warp; false: gave up.
-__device__ __forceinline__ bool tree_take(const TreeArgs &a, TreeSmem &sm, uint32_t it, TreeSeg &s)
+template <class Smem>
+__device__ __forceinline__ bool tree_take(const TreeArgs &a, Smem &sm, uint32_t it, TreeSeg &s)
 {
     const int slot = it % kTSegs;
     if (!mbar_wait_warp(&sm.seg_full[slot], (it / kTSegs) & 1, &sm.abort, &a.hdr->error))
@@ -242,7 +291,72 @@ __device__ __forceinline__ bool tree_take(const TreeArgs &a, TreeSmem &sm, uint3
     return s.valid != 0;
 }
 
-// ------------------------------------------------------------ ranges, Q, K and V
+// ------------------------------------------------------------ ranges
+// This CTA's range of the line of tiles: an equal share of its W tiles among G CTAs (fewer than
+// the grid where a share would be shorter than min_tiles).  Found by one warp where there are few
+// units, so that the others' set-up runs beside it; by all of them (ahead of their roles) else.
+constexpr int kTWarpUnits = 256;
+
+template <class Smem>
+__device__ __forceinline__ void tree_range(const TreeArgs &a, Smem &sm, int tid, int warps)
+{
+    const int lane = tid & 31, warp = tid / 32, units = a.B * a.Hkv;
+    const int per = units <= 32 ? 1 : (units + 32 * warps - 1) / (32 * warps);
+    const int lo = min(tid * per, units), hi = min(lo + per, units);
+    int mine = 0;
+    bool bad = false;
+    TreeUnit x{};
+    for (int u = lo; u < hi; ++u) {
+        x = tree_unit(a, u);
+        mine += x.nt * x.pairs;
+        bad |= x.bad;
+    }
+    if (bad && blockIdx.x == 0)
+        raise_error(&a.hdr->error, EA_DEVERR_CHECK);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += v;
+    }
+    int before = 0, W = __shfl_sync(0xffffffffu, incl, 31);
+    if (tid == 0)
+        sm.count = 0;
+    if (warps > 1) {
+        int *tot = reinterpret_cast<int *>(sm.ml);
+        if (lane == 31)
+            tot[warp] = incl;
+        __syncthreads();
+        W = 0;
+        for (int w = 0; w < warps; ++w) {
+            before += w < warp ? tot[w] : 0;
+            W += tot[w];
+        }
+    } else {
+        __syncwarp();
+    }
+    int base = before + incl - mine;
+    const int G = max(1, min(static_cast<int>(gridDim.x), W / kTMinTiles));
+    const int i = blockIdx.x, share = W / G, rest = W - share * G;
+    const int start = i * share + min(i, rest), count = share + (i < rest ? 1 : 0);
+    if (i < G && count > 0 && start >= base && start < base + mine)
+        for (int u = lo; u < hi; ++u) {
+            if (per > 1)
+                x = tree_unit(a, u);
+            const int w = x.nt * x.pairs;
+            if (start < base + w) {
+                sm.unit = x;
+                sm.u = u;
+                sm.off = start - base;
+                sm.count = count;
+                break;
+            }
+            base += w;
+        }
+}
+
+// ------------------------------------------------------------ K and V
 // Where 64 keys of a tile lie in the cache; row < 0: behind the sequence (not read).
 __device__ __forceinline__ void tree_place(const TreeArgs &a, int b, int L, int key, int &outer, int &row)
 {
@@ -259,15 +373,29 @@ __device__ __forceinline__ void tree_place(const TreeArgs &a, int b, int L, int 
     }
 }
 
-template <bool Q8>
-__device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs &a, TreeSmem &sm, int lane)
+// K or V of the tree's own tokens (rows behind the tensor read zeros).
+__device__ __forceinline__ void tree_load_draft(const TreeMaps &tm, uint8_t *dst, int kv, const TreeSeg &s, uint64_t *bar)
 {
+    mbar_arrive_expect_tx(bar, kTBytes);
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+        tma_load_4d(dst + hf * kTHalf, kv ? &tm.vd : &tm.kd, 64 * hf, s.h, 0, s.b, bar);
+}
+
+template <class Smem>
+__device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs &a, Smem &sm, int lane)
+{
+    constexpr bool Q8 = Smem::Q8;
+    constexpr int kStages = Smem::kStages, kCodes = Smem::kCodes;
     uint32_t *err = &a.hdr->error;
-    int u = sm.unit;
-    int64_t off = sm.off, left = sm.count;
-    uint32_t it = 0, entry = 0, tile = 0;
+    if (a.B * a.Hkv <= kTWarpUnits) {
+        tree_range(a, sm, lane, 1);
+        __syncwarp();
+    }
+    int u = sm.u, off = sm.off, left = sm.count;
+    TreeUnit &x = sm.unit;               // the unit at hand
+    uint32_t it = 0, entry = 0, codes = 0, tile = 0;
     bool ok = true;
-    const uint32_t qbytes = static_cast<uint32_t>(a.g * a.tpt) * 256u;
     auto publish = [&](const TreeSeg &s) {
         const int slot = it % kTSegs;
         if (!mbar_wait_warp(&sm.seg_empty[slot], ((it / kTSegs) & 1) ^ 1, &sm.abort, err))
@@ -280,17 +408,20 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
         return true;
     };
     while (ok && left > 0) {
-        const TreeUnit x = tree_unit(a, u);
-        if (off >= static_cast<int64_t>(x.nt) * x.pairs) {
-            ++u;
+        if (off >= x.nt * x.pairs) {
+            const TreeUnit next = tree_unit(a, ++u);
+            __syncwarp();
+            if (lane == 0)
+                x = next;
+            __syncwarp();
             off = 0;
             continue;
         }
         TreeSeg s;
-        const int pair = static_cast<int>(off) / x.nt;
+        const int pair = x.pairs == 1 ? 0 : off / x.nt;
         s.valid = 1;
         s.b = u / a.Hkv;
-        s.h = u % a.Hkv;
+        s.h = u - s.b * a.Hkv;
         s.v = u * a.pairs + pair;
         s.mode = x.mode;
         s.L = x.L;
@@ -298,8 +429,8 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
         s.dead = x.dead;
         s.tok0 = 2 * pair * a.tpt;
         s.two = s.tok0 + a.tpt < x.n;
-        s.t0 = static_cast<int>(off) - pair * x.nt;
-        s.t1 = left < x.nt - s.t0 ? s.t0 + static_cast<int>(left) : x.nt;
+        s.t0 = off - pair * x.nt;
+        s.t1 = left < x.nt - s.t0 ? s.t0 + left : x.nt;
         s.nt = x.nt;
         // a range holds one part that continues a unit (its first) and one that is continued at most
         s.slot = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
@@ -313,43 +444,64 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
             if (s.t1 == s.nt)
                 a.last[s.v] = blockIdx.x;
         }
-        if (!mbar_wait_warp(&sm.q_empty, (it & 1) ^ 1, &sm.abort, err))
-            break;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.q_full, s.two ? 2 * qbytes : qbytes);
-            for (int w = 0; w <= s.two; ++w)
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf)
-                    tma_load_4d(sm.q[w] + hf * kTHalf, &tm.q, 64 * hf, s.h * a.g, s.tok0 + w * a.tpt, s.b, &sm.q_full);
-        }
         __syncwarp();
         ++it;
         // Lanes 2 i and 2 i + 1 hold the places of the halves of tile i of sixteen.
         TreeTile mine{};
         int row = -1, outer = 0;
-        for (int t = s.t0; t < s.t1; ++t) {
+        for (int t = s.t0; t < s.t1; ++t, ++tile) {
             const int i = (t - s.t0) & 15;
             if (i == 0) {
                 const int tt = t + (lane >> 1);
                 if (tt < s.t1) {
                     mine = tree_tile(a, x, u, tt);
-                    if (!Q8 && !(mine.flags & kDraft))
+                    if (!(mine.flags & kDraft)) {
                         tree_place(a, s.b, s.L, mine.key0 + 64 * (lane & 1), outer, row);
+                        if (Q8 && row >= 0 && outer >= 0) {
+                            // their scales, which the converting warps will ask for
+#pragma unroll
+                            for (int kv = 0; kv < 2; ++kv)
+                                asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                                    a.c.scale[kv] + (static_cast<int64_t>(outer) * a.c.Hkv + s.h) * a.c.nsb + (row >> a.c.log2sb)));
+                        }
+                    }
                 }
+                __syncwarp();
             }
             TreeTile ti;
             ti.key0 = __shfl_sync(0xffffffffu, mine.key0, 2 * i);
             ti.flags = __shfl_sync(0xffffffffu, mine.flags, 2 * i);
-            int rw[2], ou[2];
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                rw[hf] = __shfl_sync(0xffffffffu, row, 2 * i + hf);
-                ou[hf] = __shfl_sync(0xffffffffu, outer, 2 * i + hf);
+                ti.row[hf] = __shfl_sync(0xffffffffu, row, 2 * i + hf);
+                ti.outer[hf] = __shfl_sync(0xffffffffu, outer, 2 * i + hf);
             }
+            if constexpr (Q8) {
+                // the codes; the converting warps fill the ring (with the tree's own keys too)
+#pragma unroll
+                for (int kv = 0; kv < 2 && !(ti.flags & kDraft); ++kv, ++codes) {
+                    const int cs = codes % kCodes;
+                    if (!mbar_wait_warp(&sm.code_empty[cs], ((codes / kCodes) & 1) ^ 1, &sm.abort, err)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        if (kv == 0)
+                            sm.tile[tile % kTInfos] = ti;
+                        uint64_t *bar = &sm.code_full[cs];
+                        const CUtensorMap *map = kv ? &tm.v : &tm.k;
+                        mbar_arrive_expect_tx(bar, (a.box128 || ti.row[1] >= 0) ? kTBytes / 2 : kTBytes / 4);
+                        tma_load_4d(sm.code[cs], map, 0, s.h, ti.row[0], ti.outer[0], bar);
+                        if (!a.box128 && ti.row[1] >= 0)
+                            tma_load_4d(sm.code[cs] + kTBytes / 4, map, 0, s.h, ti.row[1], ti.outer[1], bar);
+                    }
+                    __syncwarp();
+                }
+            } else {
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, ++entry) {
-                const int st = entry % kTStages;
-                if (!mbar_wait_warp(&sm.empty[st], ((entry / kTStages) & 1) ^ 1, &sm.abort, err)) {
+                const int st = entry % kStages;
+                if (!mbar_wait_warp(&sm.empty[st], ((entry / kStages) & 1) ^ 1, &sm.abort, err)) {
                     ok = false;
                     break;
                 }
@@ -359,33 +511,28 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
                     if (kv == 0)
                         sm.tile[tile % kTInfos] = ti;
                     if (ti.flags & kDraft) {
-                        mbar_arrive_expect_tx(bar, kTBytes);
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf)
-                            tma_load_4d(dst + hf * kTHalf, kv ? &tm.vd : &tm.kd, 64 * hf, s.h, 0, s.b, bar);
-                    } else if (Q8) {
-                        mbar_arrive(bar);
+                        tree_load_draft(tm, dst, kv, s, bar);
                     } else if (a.box128) {
                         mbar_arrive_expect_tx(bar, kTBytes);
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf)
-                            tma_load_4d(dst + hf * kTHalf, kv ? &tm.v : &tm.k, 64 * hf, s.h, rw[0], ou[0], bar);
+                            tma_load_4d(dst + hf * kTHalf, kv ? &tm.v : &tm.k, 64 * hf, s.h, ti.row[0], ti.outer[0], bar);
                     } else {
-                        mbar_arrive_expect_tx(bar, rw[1] >= 0 ? kTBytes : kTHalf);
+                        mbar_arrive_expect_tx(bar, ti.row[1] >= 0 ? kTBytes : kTHalf);
 #pragma unroll
                         for (int p = 0; p < 2; ++p)
-                            if (rw[p] >= 0)
+                            if (ti.row[p] >= 0)
 #pragma unroll
                                 for (int hf = 0; hf < 2; ++hf)
                                     tma_load_4d(dst + hf * kTHalf + p * (kTHalf / 2), kv ? &tm.v : &tm.k, 64 * hf, s.h,
-                                                rw[p], ou[p], bar);
+                                                ti.row[p], ti.outer[p], bar);
                     }
                 }
                 __syncwarp();
             }
+            }
             if (!ok)
                 break;
-            ++tile;
         }
     }
     TreeSeg none{};
@@ -394,109 +541,118 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
     // Before leaving on an abort, let the copies already issued land.
     if (__any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
         volatile int no_abort = 0;
-        for (uint32_t n = entry > kTStages ? entry - kTStages : 0; n < entry; ++n)
-            mbar_wait_warp(&sm.full[n % kTStages], (n / kTStages) & 1, &no_abort, nullptr);
-        if (it > 0)
-            mbar_wait_warp(&sm.q_full, (it - 1) & 1, &no_abort, nullptr);
+        if constexpr (Q8)
+            for (uint32_t n = codes > kCodes ? codes - kCodes : 0; n < codes; ++n)
+                mbar_wait_warp(&sm.code_full[n % kCodes], (n / kCodes) & 1, &no_abort, nullptr);
+        for (uint32_t n = entry > kStages ? entry - kStages : 0; n < entry; ++n)
+            mbar_wait_warp(&sm.full[n % kStages], (n / kStages) & 1, &no_abort, nullptr);
     }
 }
 
 // ------------------------------------------------------------ products
-// One thread.  Takes whichever is ready: the next S = Q K^T (at most two ahead of the
-// products that have consumed theirs), or the next O += P V.
-__device__ __forceinline__ void tree_mma(const TreeArgs &a, TreeSmem &sm, uint32_t tmem)
+// One warp, one thread of it for the MMAs: S = Q K^T of a step once O += P V of the step two before
+// (the last user of that S) is issued.  The warp stays whole and its values uniform, so that the
+// operands' descriptors are worked out in uniform registers: by one thread alone, eight MMAs took 750
+// cycles to issue, more than they take.  (Taking whichever product is ready first, by polling, costs
+// the softmax warps beside it their issue slots.)
+template <class Smem>
+__device__ __forceinline__ void tree_mma(const TreeArgs &a, Smem &sm, uint32_t tmem_base, int lane)
 {
+    constexpr int kStages = Smem::kStages;
+    constexpr bool TWO = sizeof(sm.q) > kTBytes;
     volatile int *abort = &sm.abort;
     uint32_t *err = &a.hdr->error;
-    uint32_t it = 0, tile0 = 0, p_cnt[2] = {0, 0};
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+    const uint64_t q0 = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), ring0 = sdesc_sw128(smem_u32(sm.ring[0]), 16, 1024);
+    const uint64_t vring0 = sdesc_sw128(smem_u32(sm.ring[0]), kTHalf, 1024);
+    const uint32_t go = elect_one();
+    uint32_t tile0 = 0, p_cnt[2] = {0, 0};
     bool ok = true;
-    for (; ok; ++it) {
+    for (uint32_t it = 0; ok; ++it) {
         const int slot = it % kTSegs;
-        if (!mbar_wait(&sm.seg_full[slot], (it / kTSegs) & 1, abort, err))
+        if (!mbar_wait_warp(&sm.seg_full[slot], (it / kTSegs) & 1, abort, err))
             break;
-        const int valid = sm.seg[slot].valid, two = sm.seg[slot].two, nt = sm.seg[slot].t1 - sm.seg[slot].t0;
-        mbar_arrive(&sm.seg_empty[slot]);
+        const int valid = __shfl_sync(0xffffffffu, sm.seg[slot].valid, 0);
+        const int two = TWO ? __shfl_sync(0xffffffffu, sm.seg[slot].two, 0) : 0;
+        const int nt = __shfl_sync(0xffffffffu, sm.seg[slot].t1 - sm.seg[slot].t0, 0);
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&sm.seg_empty[slot]);
         if (!valid)
             break;
-        if (!mbar_wait(&sm.q_full, it & 1, abort, err))
+        if (!mbar_wait_warp(&sm.q_full, it & 1, abort, err))
             break;
         const int N = nt << two;
-        int qk = 0, pv = 0;
-        bool o_free = it == 0;
-        uint64_t t0 = 0;
-        while (pv < N) {
-            bool did = false;
-            if (qk < N && qk < pv + 2) {
-                const int t = qk >> two, w = qk & 1;
-                const uint32_t e = 2 * (tile0 + t);
-                const int st = e % kTStages;
-                if (mbar_test(&sm.full[st], (e / kTStages) & 1)) {
-                    tc_fence_after();
-                    const uint32_t qa = smem_u32(sm.q[two ? w : 0]), ka = smem_u32(sm.ring[st]);
-#pragma unroll
-                    for (int k = 0; k < EA_HEAD_DIM / 16; ++k) {
-                        const uint32_t o = (k >> 2) * kTHalf + (k & 3) * 32;
-                        tc_mma(tmem + 128 * w, sdesc_sw128(qa + o, 16, 1024), sdesc_sw128(ka + o, 16, 1024), kTIdescQK, k > 0);
-                    }
-                    tc_commit(&sm.s_full[w]);
-                    if (!two || w == 1)
-                        tc_commit(&sm.empty[st]);
-                    if (++qk == N)
-                        tc_commit(&sm.q_empty);
-                    did = true;
+        for (int n = 0; n < N + 2; ++n) {
+            const int w = n & 1;
+            if (n >= 2) {
+                const int pv = n - 2;
+                const uint32_t tile = tile0 + (pv >> two), e = 2 * tile + 1;
+                const int st = e % kStages;
+                // (O is still read for the range's part before)
+                if ((pv == 0 && it > 0 && !mbar_wait_warp(&sm.o_free, (it - 1) & 1, abort, err)) ||
+                    !mbar_wait_warp(&sm.ready[tile % kTReady], (tile / kTReady) & 1, abort, err) ||
+                    !mbar_wait_warp(&sm.p_full[w], p_cnt[w] & 1, abort, err)) {
+                    ok = false;
+                    break;
                 }
-            }
-            if (pv < qk) {
-                const int t = pv >> two, w = pv & 1;
-                const uint32_t tile = tile0 + t, e = 2 * tile + 1;
-                const int st = e % kTStages;
-                if (!o_free)
-                    o_free = mbar_test(&sm.o_free, (it - 1) & 1);
-                if (o_free && mbar_test(&sm.p_full[w], p_cnt[w] & 1) && mbar_test(&sm.ready[tile % kTReady], (tile / kTReady) & 1)) {
-                    tc_fence_after();
-                    const int *odd = sm.odd[tile % kTReady];
-                    if (!(odd[0] | odd[1])) {
-                        const uint32_t va = smem_u32(sm.ring[st]);
-                        // (a warpgroup's first product of the range overwrites what its O held)
-                        const bool first = pv < 2;
+                ++p_cnt[w];
+                tc_fence_after();
+                const int odd = __shfl_sync(0xffffffffu, sm.odd[tile % kTReady][0] | sm.odd[tile % kTReady][1], 0);
+                const int groups = __shfl_sync(0xffffffffu, sm.tile[tile % kTInfos].flags >> kGroups, 0);
+                const uint64_t vd = vring0 + static_cast<uint64_t>(st * (kTBytes >> 4));
+                const uint32_t tp = tmem + 128 * w, to = tmem + kTColO + 128 * w;
+                // (a warpgroup's first product of the range overwrites what its O held)
+                const uint32_t more = pv >= 2;
+                if (!odd) {
+                    if (groups == 8) {
 #pragma unroll
-                        for (int k = 0; k < kTTile / 16; ++k)
-                            tc_mma_ts(tmem + kTColO + 128 * w, tmem + 128 * w + 8 * k, sdesc_sw128(va + k * 2048, kTHalf, 1024),
-                                      kTIdescPV, !first || k > 0);
+                        for (int k = 0; k < 8; ++k)
+                            mma_ts(go, to, tp + (k < 4 ? 8 * k : 32 + 8 * k), vd + k * (2048 >> 4), kTIdescPV, k ? 1u : more);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < groups; ++k)
+                            mma_ts(go, to, tp + (k < 4 ? 8 * k : 32 + 8 * k), vd + k * (2048 >> 4), kTIdescPV, k ? 1u : more);
                     }
-                    tc_commit(&sm.o_done[w]);
-                    if (!two || w == 1)
-                        tc_commit(&sm.empty[st]);
-                    ++p_cnt[w];
-                    if (++pv == N)
-                        tc_commit(&sm.seg_done);
-                    did = true;
                 }
+                commit_if(go, &sm.o_done[w]);
+                if (!two || w == 1)
+                    commit_if(go, &sm.empty[st]);
+                if (pv == N - 1)
+                    commit_if(go, &sm.seg_done);
             }
-            if (did) {
-                t0 = 0;
-                continue;
-            }
-            if (*abort) {
-                ok = false;
-                break;
-            }
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0) {
-                t0 = now;
-            } else if (now - t0 > EA_WAIT_TIMEOUT_NS) {
-                raise_error(err, EA_DEVERR_TIMEOUT);
-                *abort = 1;
-                ok = false;
-                break;
+            if (n < N) {
+                const uint32_t tile = tile0 + (n >> two), e = 2 * tile;
+                const int st = e % kStages;
+                if (!mbar_wait_warp(&sm.full[st], (e / kStages) & 1, abort, err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t qd = q0 + static_cast<uint64_t>((two & w) * (kTBytes >> 4));
+                const uint64_t kd = ring0 + static_cast<uint64_t>(st * (kTBytes >> 4));
+                // (a tile with fewer keys: the columns behind them are masked)
+                const int groups = __shfl_sync(0xffffffffu, sm.tile[tile % kTInfos].flags >> kGroups, 0);
+                const uint32_t id = (kTIdescQK & ~(63u << 17)) | static_cast<uint32_t>(groups) << 18;
+                const uint32_t ts = tmem + 128 * w;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint64_t o = ((k >> 2) * kTHalf + (k & 3) * 32) >> 4;
+                    mma_ss(go, ts, qd + o, kd + o, id, k > 0);
+                }
+                commit_if(go, &sm.s_full[w]);
+                if (!two || w == 1)
+                    commit_if(go, &sm.empty[st]);
+                if (n == N - 1)
+                    commit_if(go, &sm.q_empty);
             }
         }
         tile0 += nt;
     }
-    // All of this thread's MMAs must have completed before TMEM is released.
-    tc_commit(&sm.drain);
+    // All of this warp's MMAs must have completed before TMEM is released.
+    commit_if(go, &sm.drain);
     volatile int no_abort = 0;
-    mbar_wait(&sm.drain, 0, &no_abort, err);
+    mbar_wait_warp(&sm.drain, 0, &no_abort, err);
 }
 
 // ------------------------------------------------------------ V's rows
@@ -505,27 +661,43 @@ __device__ __forceinline__ uint32_t odd_bf16x2(uint32_t w)
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-__device__ __forceinline__ void tree_fix(const TreeArgs &a, TreeSmem &sm, int warp, int lane)
+template <class Smem>
+__device__ __forceinline__ void tree_fix(const TreeMaps &tm, const TreeArgs &a, Smem &sm, int warp, int lane)
 {
+    constexpr int kStages = Smem::kStages;
     uint32_t *err = &a.hdr->error;
-    uint32_t tile = 0;
+    uint32_t tile = 0, it = 0;
     TreeSeg s;
-    for (uint32_t it = 0; tree_take(a, sm, it, s); ++it)
+    for (; tree_take(a, sm, it, s); ++it) {
+        if (warp == kTFixWarp) {
+            // the queries
+            if (!mbar_wait_warp(&sm.q_empty, (it & 1) ^ 1, &sm.abort, err))
+                return;
+            if (lane == 0) {
+                const int tiles = sizeof(sm.q) > kTBytes && s.two ? 2 : 1;
+                mbar_arrive_expect_tx(&sm.q_full, static_cast<uint32_t>(tiles * a.g * a.tpt) * 256u);
+                for (int w = 0; w < tiles; ++w)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+                        tma_load_4d(sm.q[w] + hf * kTHalf, &tm.q, 64 * hf, s.h * a.g, s.tok0 + w * a.tpt, s.b, &sm.q_full);
+            }
+            __syncwarp();
+        }
         for (int t = s.t0; t < s.t1; ++t, ++tile) {
             const uint32_t e = 2 * tile;
-            const int ks = e % kTStages, vs = (e + 1) % kTStages;
-            if (!mbar_wait_warp(&sm.full[ks], (e / kTStages) & 1, &sm.abort, err))
-                return;
+            const int ks = e % kStages, vs = (e + 1) % kStages;
+            if (!mbar_wait_warp(&sm.full[ks], (e / kStages) & 1, &sm.abort, err))
+                break;
             const TreeTile ti = sm.tile[tile % kTInfos];
-            if (!mbar_wait_warp(&sm.full[vs], ((e + 1) / kTStages) & 1, &sm.abort, err))
-                return;
+            if (!mbar_wait_warp(&sm.full[vs], ((e + 1) / kStages) & 1, &sm.abort, err))
+                break;
             bool odd = false;
             if (ti.flags & kEdge) {
                 const int nv = (ti.flags & kDraft) ? s.n : min(kTTile, s.L - ti.key0);
                 const int from = (ti.flags & kMixed) ? 0 : nv * 16;
                 // 16 bytes of row i / 16: eight of each half (their order in a row does not matter)
 #pragma unroll 4
-                for (int i = from + (warp - kTFixWarp) * 32 + lane; i < kTTile * 16; i += kTFixWarps * 32) {
+                for (int i = from + (warp - kTFixWarp) * 32 + lane; i < (ti.flags >> kGroups) * 256; i += kTFixWarps * 32) {
                     uint4 *p = reinterpret_cast<uint4 *>(sm.ring[vs] + ((i >> 3) & 1) * kTHalf + (i >> 4) * 128 + (i & 7) * 16);
                     if ((i >> 4) >= nv) {
                         *p = make_uint4(0u, 0u, 0u, 0u);
@@ -545,117 +717,248 @@ __device__ __forceinline__ void tree_fix(const TreeArgs &a, TreeSmem &sm, int wa
             }
             __syncwarp();
         }
+    }
+    // Before leaving on an abort, let the queries already issued land.
+    if (warp == kTFixWarp && it > 0 && __any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
+        volatile int no_abort = 0;
+        mbar_wait_warp(&sm.q_full, (it - 1) & 1, &no_abort, nullptr);
+    }
 }
 
 // ------------------------------------------------------------ 8-bit caches
-// 16 codes of one row, times its scale, as bf16 (exact: at most 8 bits).
+// Four codes times their row's scale as bf16, exact: an e4m3 code has 4 bits, an int8 one 7.
+//   e4m3: a byte's exponent and fraction, moved to bf16's, are its value times 2^-120
+//   int8: c + 128 in the fraction of 2^23, less 2^23 + 128
 template <bool E4M3>
-__device__ __forceinline__ void put16(uint8_t *tile, int row, int chunk, const uint4 &c, float s)
-{
-    uint32_t o[8];
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t h[2];
-        codes_f16<E4M3>(w[i], h[0], h[1]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float2 v = f16_f32(h[k]);
-            o[2 * i + k] = pack_bf16x2(v.x * s, v.y * s);
-        }
+struct Scale {
+    __nv_bfloat162 f;
+    bool two;
+    __device__ __forceinline__ explicit Scale(float s)
+    {
+        // 2^120 s, in two steps where bf16 does not hold it
+        two = s > 128.f;
+        f = __float2bfloat162_rn(two ? s : s * 0x1p120f);
     }
-    // 32 bytes at column 32 (chunk % 4) of the row's half, 16-byte pieces swizzled; the two
-    // halves' lanes store their pieces in opposite order, so that they meet other banks
-    uint8_t *p = tile + (chunk >> 2) * kTHalf + row * 128;
-    const int c0 = (chunk & 3) * 2, flip = chunk >> 2;
-    const uint4 a0 = make_uint4(o[0], o[1], o[2], o[3]), a1 = make_uint4(o[4], o[5], o[6], o[7]);
-    *reinterpret_cast<uint4 *>(p + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? a1 : a0;
-    *reinterpret_cast<uint4 *>(p + (((c0 + 1 - flip) ^ (row & 7)) << 4)) = flip ? a0 : a1;
-}
+    __device__ __forceinline__ uint32_t pair(uint32_t t) const
+    {
+        uint32_t w = ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+        __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&w);
+        if (two)
+            x = __hmul2(x, __float2bfloat162_rn(0x1p120f));
+        x = __hmul2(x, f);
+        return *reinterpret_cast<const uint32_t *>(&x);
+    }
+    __device__ __forceinline__ uint2 four(uint32_t w) const
+    {
+        return make_uint2(pair(__byte_perm(w, 0u, 0x1404)), pair(__byte_perm(w, 0u, 0x3424)));
+    }
+};
 
-template <bool E4M3>
-__device__ __forceinline__ void tree_convert(const TreeArgs &a, TreeSmem &sm, int ct, int lane)
+template <>
+struct Scale<false> {
+    float f;
+    __device__ __forceinline__ explicit Scale(float s) : f(s) {}
+    __device__ __forceinline__ float one(uint32_t u, uint32_t sel) const
+    {
+        return (__uint_as_float(__byte_perm(u, 0x4b000000u, sel)) - 8388736.f) * f;
+    }
+    __device__ __forceinline__ uint2 four(uint32_t w) const
+    {
+        const uint32_t u = w ^ 0x80808080u;
+        return make_uint2(pack_bf16x2(one(u, 0x7440), one(u, 0x7441)), pack_bf16x2(one(u, 0x7442), one(u, 0x7443)));
+    }
+};
+
+// Warps that turn tiles of codes into the ring's bf16 ones, four for K and four for V, so that the
+// latencies of one (its codes, its scales, the fence) lie under the other's work.  A thread has 16
+// codes of eight rows, one of each 16-key group, so lane i holds the scale of group i.  They go to 32
+// bytes at column 32 (chunk % 4) of the row's half, in 16-byte pieces, swizzled as TMA would (the
+// two halves' lanes store their pieces in opposite order, so that they meet other banks).
+template <bool E4M3, class Smem>
+__device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs &a, Smem &sm, int kv, int ct, int lane)
 {
+    constexpr int kStages = Smem::kStages, kCodes = Smem::kCodes;
+    static_assert(kStages % 2 == 0 && kCodes % 2 == 0, "a stage belongs to K or to V");
     uint32_t *err = &a.hdr->error;
-    uint32_t entry = 0;
+    uint32_t entry = kv, codes = kv, tile = 0;
+    const int chunk = ct & 7, r0 = ct >> 3, flip = chunk >> 2, c0 = (chunk & 3) * 2;
+    const uint32_t off0 = (chunk >> 2) * kTHalf + r0 * 128 + (((c0 + flip) ^ (r0 & 7)) << 4);
+    const uint32_t off1 = (chunk >> 2) * kTHalf + r0 * 128 + (((c0 + 1 - flip) ^ (r0 & 7)) << 4);
+    const float *scales = a.c.scale[kv];
     TreeSeg s;
-    const int chunk = ct & 7, r0 = ct >> 3;
-    for (uint32_t it = 0; tree_take(a, sm, it, s); ++it) {
-        const int u = s.b * a.Hkv + s.h;
-        const TreeUnit x = tree_unit(a, u);
-        struct Codes {
-            uint4 c[2][4];
-            float f[2][4];
-        };
-        auto load = [&](int t, Codes &z) {
-            const TreeTile ti = t < s.t1 ? tree_tile(a, x, u, t) : TreeTile{0, kDraft};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = ti.key0 + 32 * i + r0;
-                int outer = 0, row = -1;
-                if (!(ti.flags & kDraft))
-                    tree_place(a, s.b, s.L, key, outer, row);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    z.c[kv][i] = make_uint4(0u, 0u, 0u, 0u);
-                    z.f[kv][i] = 0.f;
-                    if (row >= 0 && outer >= 0) {
-                        z.c[kv][i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.c.code[kv]) +
-                                                                           outer * a.c.s_outer + row * a.c.s_row +
-                                                                           s.h * a.c.s_head + 16 * chunk));
-                        z.f[kv][i] = __ldg(a.c.scale[kv] + (static_cast<int64_t>(outer) * a.c.Hkv + s.h) * a.c.nsb +
-                                           (row >> a.c.log2sb));
-                    }
+    bool ok = true;
+    for (uint32_t it = 0; ok && tree_take(a, sm, it, s); ++it)
+        for (int t = s.t0; t < s.t1; ++t, ++tile, entry += 2) {
+            const int st = entry % kStages, cs = codes % kCodes;
+            if (t == s.nt - 1) {
+                if (!mbar_wait_warp(&sm.empty[st], ((entry / kStages) & 1) ^ 1, &sm.abort, err)) {
+                    ok = false;
+                    break;
                 }
-            }
-        };
-        auto put = [&](int t, const Codes &z) {
-            const bool draft = t == s.nt - 1;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv, ++entry) {
-                const int st = entry % kTStages;
-                if (!mbar_wait_warp(&sm.empty[st], ((entry / kTStages) & 1) ^ 1, &sm.abort, err))
-                    return false;
-                if (!draft) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        put16<E4M3>(sm.ring[st], 32 * i + r0, chunk, z.c[kv][i], z.f[kv][i]);
-                    fence_proxy_async_smem();
+                if (ct == 0) {
+                    if (kv == 0)
+                        sm.tile[tile % kTInfos] = tree_own_tile(s.L, s.n);
+                    tree_load_draft(tm, sm.ring[st], kv, s, &sm.full[st]);
+                } else if (lane == 0) {
+                    mbar_arrive(&sm.full[st]);
                 }
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&sm.full[st]);
+                continue;
             }
-            return true;
-        };
-        Codes z0;
-        for (int t = s.t0; t < s.t1; ++t) {
-            load(t, z0);
-            if (!put(t, z0))
-                return;
+            if (!mbar_wait_warp(&sm.code_full[cs], (codes / kCodes) & 1, &sm.abort, err)) {
+                ok = false;
+                break;
+            }
+            const TreeTile &ti = sm.tile[tile % kTInfos];
+            float f = 0.f;
+            {
+                const int hf = (lane >> 2) & 1, outer = ti.outer[hf], row = ti.row[hf] + 16 * (lane & 3);
+                if (lane < 8 && outer >= 0 && ti.key0 + 16 * lane < s.L)
+                    f = __ldg(scales + (static_cast<int64_t>(outer) * a.c.Hkv + s.h) * a.c.nsb + (row >> a.c.log2sb));
+            }
+            uint4 c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                c[i] = *reinterpret_cast<const uint4 *>(sm.code[cs] + (16 * i + r0) * 128 + 16 * chunk);
+            const int groups = ti.flags >> kGroups;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.code_empty[cs]);
+            codes += 2;
+            if (!mbar_wait_warp(&sm.empty[st], ((entry / kStages) & 1) ^ 1, &sm.abort, err)) {
+                ok = false;
+                break;
+            }
+            uint8_t *dst = sm.ring[st];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                if (i < groups) {
+                    const Scale<E4M3> sc(fi);
+                    const uint2 w0 = sc.four(c[i].x), w1 = sc.four(c[i].y), w2 = sc.four(c[i].z), w3 = sc.four(c[i].w);
+                    const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
+                    *reinterpret_cast<uint4 *>(dst + off0 + 2048 * i) = flip ? hi : lo;
+                    *reinterpret_cast<uint4 *>(dst + off1 + 2048 * i) = flip ? lo : hi;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.full[st]);
         }
+    // Before leaving on an abort, let the copies already issued land.
+    if (ct < 32 && __any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
+        volatile int no_abort = 0;
+        for (uint32_t n = entry > kStages + 1u ? entry - kStages : kv; n < entry; n += 2)
+            mbar_wait_warp(&sm.full[n % kStages], (n / kStages) & 1, &no_abort, nullptr);
     }
 }
 
 // ------------------------------------------------------------ softmax
-__device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem &sm, uint32_t tmem, int warp, int lane)
+// Which of a tile's 128 keys a node at depth d keeps (where not all rows keep all).
+__device__ __forceinline__ void tree_keep(const TreeArgs &a, const TreeSeg &s, const TreeTile &ti, int d, const uint4 &up,
+                                          uint32_t (&keep)[4])
 {
+    if (ti.flags & kDraft) {
+        const uint32_t w[4] = {up.x, up.y, up.z, up.w};
+        // which ancestors the head's mode keeps at this node's position
+        const bool ssa = s.mode == EA_SSA && d >= a.window, blk = s.mode == EA_BLOCK;
+        const int64_t mrow = (static_cast<int64_t>(s.b) * a.Hkv + s.h) * a.nBm + (s.L + d) / EA_TILE;
+        for (int c = 0; c < 4; ++c) {
+            uint32_t k = (c == 0 ? w[0] : c == 1 ? w[1] : c == 2 ? w[2] : w[3]) & cols_below(s.n, c);
+            if (ssa || blk)
+                for (uint32_t left = k; left; left &= left - 1) {
+                    const int j = 32 * c + __ffs(left) - 1;
+                    const int dj = a.depth[static_cast<int64_t>(s.b) * a.T + j], pos = s.L + dj;
+                    const bool in = ssa ? pos < a.sink || d - dj < a.window
+                                        : dj >= 0 && pos / EA_TILE < a.nBm && a.block_mask[mrow * a.nBm + pos / EA_TILE] != 0;
+                    if (!in)
+                        k &= ~(left & (0u - left));
+                }
+            keep[0] = c == 0 ? k : keep[0];
+            keep[1] = c == 1 ? k : keep[1];
+            keep[2] = c == 2 ? k : keep[2];
+            keep[3] = c == 3 ? k : keep[3];
+        }
+    } else {
+        const int lim = s.L - ti.key0;
+        const bool row_in = s.mode != EA_BLOCK || (ti.flags & ((s.L + d) / EA_TILE > s.L / EA_TILE ? kRow1 : kRow0));
+        const int sink = a.sink - ti.key0;                       // columns below are kept,
+        const int win = s.L - ti.key0 + d - a.window + 1;        // and those from here on
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            keep[c] = row_in ? cols_below(lim, c) : 0u;
+            if (s.mode == EA_SSA)
+                keep[c] &= cols_below(sink, c) | ~cols_below(win, c);
+        }
+    }
+}
+
+// -inf where the row does not keep the key.
+__device__ __forceinline__ void mask32(uint32_t (&x)[32], uint32_t keep)
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        x[i] = (keep >> i) & 1u ? x[i] : 0xff800000u;
+}
+
+__device__ __forceinline__ float max32(const uint32_t (&x)[32], float m)
+{
+    float a = m, b = __uint_as_float(x[1]);
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        a = max3f(a, __uint_as_float(x[i]), __uint_as_float(x[i + 2]));
+        b = max3f(b, __uint_as_float(x[i + 1]), __uint_as_float(x[i + 3]));
+    }
+    return fmaxf(a, b);
+}
+
+// p = 2^(c x + d) of 32 columns into TMEM as bf16; the sums of its even and odd ones grow.
+__device__ __forceinline__ void exp32(const uint32_t (&x)[32], uint64_t c, uint64_t d, uint64_t &sum, uint32_t tp)
+{
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float e0, e1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c, d), e0, e1);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
+        sum = f2_add(sum, f2_pack(e0, e1));
+        p[i] = pack_bf16x2(e0, e1);
+    }
+    tmem_st16(tp, p);
+}
+
+// A row's 128 scores go through its thread's registers once (bf16 caches).  Beside the
+// converting warps there is room for half of them: the other half is read from TMEM twice.
+// P takes the place of the first half of either half of S.
+template <class Smem>
+__device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32_t tmem, int warp, int lane)
+{
+    constexpr int kHeld = Smem::Q8 ? 2 : 4;           // chunks of 32 columns held
+    constexpr bool TWO = sizeof(sm.q) > kTBytes;
     const float NEG_INF = -__int_as_float(0x7f800000);
     uint32_t *err = &a.hdr->error;
     const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + 128 * wg, to = tmem + lane_base + kTColO;
+    const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
+    auto place = [&](int c) { return ts + (c < 2 ? 16 * c : 32 + 16 * c); };
     uint32_t own = 0, tile0 = 0, joined = 0;
     TreeSeg s;
     for (uint32_t it = 0; tree_take(a, sm, it, s); ++it) {
-        const int mt = s.two ? wg : 0, tl = r / a.g, hh = r - tl * a.g;
+        const bool two = TWO && s.two;
+        const int mt = two ? wg : 0, tl = r / a.g, hh = r - tl * a.g;
         const int t = s.tok0 + mt * a.tpt + tl;
         const bool valid = tl < a.tpt && t < s.n;
         const bool active = __any_sync(0xffffffffu, valid);
         const int64_t node = static_cast<int64_t>(s.b) * a.T + t;
         int d = 0;
+        uint4 up = make_uint4(0u, 0u, 0u, 0u);
         if (valid) {
             d = a.depth[node];
+            if (s.t1 == s.nt && !s.dead)
+                up = a.mask[node];
             if (d < 0 || d >= s.n) {
                 raise_error(err, EA_DEVERR_CHECK);
                 d = d < 0 ? 0 : s.n - 1;
@@ -663,7 +966,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem &sm, ui
         }
         float m = NEG_INF, l = 0.f;
         int steps = 0;
-        for (int tt = s.t0 + (s.two ? 0 : wg); tt < s.t1; tt += s.two ? 1 : 2, ++own, ++steps) {
+        for (int tt = s.t0 + (two ? 0 : wg); tt < s.t1; tt += two ? 1 : 2, ++own, ++steps) {
             if (!mbar_wait_warp(&sm.s_full[wg], own & 1, &sm.abort, err))
                 return;
             if (active) {
@@ -671,158 +974,174 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem &sm, ui
                     return;
                 tc_fence_after();
                 const uint32_t tile = tile0 + (tt - s.t0);
-                const TreeTile ti = sm.tile[tile % kTInfos];
-                uint32_t keep[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                const int flags = sm.tile[tile % kTInfos].flags;
+                const bool edge = (flags & kEdge) != 0;
+                const int chunks = ((flags >> kGroups) + 1) / 2;     // of 32 columns, that hold keys
+                uint32_t keep[4];
                 bool odd = false;
-                if (ti.flags & kEdge) {
-                    if (ti.flags & kDraft) {
-                        const uint4 up = valid && !s.dead ? a.mask[node] : make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t w[4] = {up.x, up.y, up.z, up.w};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            keep[c] = w[c] & cols_below(s.n, c);
-                        // which ancestors the head's mode keeps at this node's position
-                        const bool ssa = s.mode == EA_SSA && d >= a.window, blk = s.mode == EA_BLOCK;
-                        if (ssa || blk) {
-                            const int64_t mrow = (static_cast<int64_t>(s.b) * a.Hkv + s.h) * a.nBm + (s.L + d) / EA_TILE;
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                for (uint32_t left = keep[c]; left; left &= left - 1) {
-                                    const int j = 32 * c + __ffs(left) - 1;
-                                    const int dj = a.depth[static_cast<int64_t>(s.b) * a.T + j], pos = s.L + dj;
-                                    bool in;
-                                    if (ssa)
-                                        in = pos < a.sink || d - dj < a.window;
-                                    else
-                                        in = dj >= 0 && pos / EA_TILE < a.nBm && a.block_mask[mrow * a.nBm + pos / EA_TILE] != 0;
-                                    if (!in)
-                                        keep[c] &= ~(left & (0u - left));
-                                }
-                        }
-                    } else {
-                        const int lim = s.L - ti.key0;
-                        const bool row_in = s.mode != EA_BLOCK ||
-                                            (ti.flags & ((s.L + d) / EA_TILE > s.L / EA_TILE ? kRow1 : kRow0));
-                        const int sink = a.sink - ti.key0;                       // columns below are kept,
-                        const int win = s.L - ti.key0 + d - a.window + 1;        // and those from here on
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            keep[c] = row_in ? cols_below(lim, c) : 0u;
-                            if (s.mode == EA_SSA)
-                                keep[c] &= cols_below(sink, c) | ~cols_below(win, c);
-                        }
-                    }
-                    if (ti.flags & kMixed) {
+                if (edge) {
+                    tree_keep(a, s, sm.tile[tile % kTInfos], d, up, keep);
+                    if (flags & kMixed) {
                         if (!mbar_wait_warp(&sm.ready[tile % kTReady], (tile / kTReady) & 1, &sm.abort, err))
                             return;
                         odd = (sm.odd[tile % kTReady][0] | sm.odd[tile % kTReady][1]) != 0;
                     }
                 }
-                const bool edge = (ti.flags & kEdge) != 0;
                 __syncwarp();
-                float mx = NEG_INF;
+                auto grow = [&](float mx) {
+                    const bool grew = mx > m + a.grow;
+                    if (__any_sync(0xffffffffu, grew)) {
+                        const float f = grew && m != NEG_INF ? ex2((m - mx) * a.scale_log2) : 1.f;
+                        m = grew ? mx : m;
+                        l *= f;
+                        if (steps > 0) {
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16(to + 128 * wg + 16 * c, o);
+                                tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32];
-                    tmem_ld32(ts + 32 * c, x);
-                    tmem_wait_ld();
-                    if (edge) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            x[i] = (keep[c] >> i) & 1u ? x[i] : 0xff800000u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        mx = max3f(mx, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                }
-                const bool grew = mx > m + a.grow;
-                if (__any_sync(0xffffffffu, grew)) {
-                    const float f = grew && m != NEG_INF ? ex2((m - mx) * a.scale_log2) : 1.f;
-                    m = grew ? mx : m;
-                    l *= f;
-                    if (steps > 0) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t x[32];
-                            tmem_ld32(to + 128 * wg + 32 * c, x);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                            tmem_st32(to + 128 * wg + 32 * c, x);
+                                for (int i = 0; i < 16; ++i) {
+                                    asm volatile("" : "+r"(o[i]));
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                }
+                                tmem_st16(to + 128 * wg + 16 * c, o);
+                            }
+                            tmem_wait_st();
                         }
-                        tmem_wait_st();
                     }
-                }
-                const float mb = m == NEG_INF ? 0.f : m * a.scale_log2;
-                if (!odd) {
-                    float sum[2] = {0.f, 0.f};
+                };
+                if (!edge) {
+                    float mx = NEG_INF;
+                    uint32_t x[kHeld][32];
+                    if constexpr (kHeld == 2) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t x[32], p[16];
+                        for (int c = 0; c < 2; ++c)
+                            tmem_ld32(ts + 32 * c, x[c]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            tie32(x[c]);
+                            mx = max32(x[c], mx);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < kHeld; ++c)
+                        tmem_ld32(ts + 32 * (c + 4 - kHeld), x[c]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < kHeld; ++c) {
+                        tie32(x[c]);
+                        mx = max32(x[c], mx);
+                    }
+                    grow(mx);
+                    const float mb = m == NEG_INF ? 0.f : m * a.scale_log2;
+                    const uint64_t d2 = f2_pack(-mb, -mb);
+                    uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                    for (int c = 0; c < kHeld; ++c)
+                        exp32(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c + 4 - kHeld));
+                    if constexpr (kHeld == 2) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            tmem_ld32(ts + 32 * c, x[c]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            tie32(x[c]);
+                            exp32(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c));
+                        }
+                    }
+                    float u, v;
+                    f2_unpack(f2_add(sum0, sum1), u, v);
+                    l += u + v;
+                } else if (!odd) {
+                    // 32 columns at a time, those that hold keys (P lies behind what is still to be read)
+                    float mx = NEG_INF;
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        uint32_t x[32];
                         tmem_ld32(ts + 32 * c, x);
                         tmem_wait_ld();
-                        if (edge) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                x[i] = (keep[c] >> i) & 1u ? x[i] : 0xff800000u;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float p0 = ex2(fmaf(__uint_as_float(x[2 * i]), a.scale_log2, -mb));
-                            const float p1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), a.scale_log2, -mb));
-                            sum[0] += p0;
-                            sum[1] += p1;
-                            p[i] = pack_bf16x2(p0, p1);
-                        }
-                        tmem_st16(ts + 16 * c, p);
+                        tie32(x);
+                        mask32(x, c == 0 ? keep[0] : c == 1 ? keep[1] : c == 2 ? keep[2] : keep[3]);
+                        mx = max32(x, mx);
                     }
-                    l += sum[0] + sum[1];
+                    grow(mx);
+                    const float mb = m == NEG_INF ? 0.f : m * a.scale_log2;
+                    const uint64_t d2 = f2_pack(-mb, -mb);
+                    uint64_t sum = 0;
+#pragma unroll 1
+                    for (int c = 0; c < chunks; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(ts + 32 * c, x);
+                        tmem_wait_ld();
+                        tie32(x);
+                        mask32(x, c == 0 ? keep[0] : c == 1 ? keep[1] : c == 2 ? keep[2] : keep[3]);
+                        exp32(x, c2, d2, sum, place(c));
+                    }
+                    float u, v;
+                    f2_unpack(sum, u, v);
+                    l += u + v;
                 } else {
                     // V holds infinities or NaN in a tile that rows keep differently: the kept keys
                     // one by one, so that none reaches a row that does not keep it (the first ones of
                     // a range write O, once nobody reads the last range's)
                     if (steps == 0 && it > 0 && !mbar_wait_warp(&sm.o_free, (it - 1) & 1, &sm.abort, err))
                         return;
-                    float sum = 0.f;
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
+                    const uint8_t *v0 = sm.ring[(2 * tile + 1) % Smem::kStages];
+                    float mx = NEG_INF, sum = 0.f;
+#pragma unroll 1
+                    for (int k = 0; k < 16 * (flags >> kGroups); ++k) {
+                        uint32_t sk = tmem_ld1(ts + k);
+                        tmem_wait_ld();
+                        asm volatile("" : "+r"(sk));
+                        const uint32_t kw = k < 32 ? keep[0] : k < 64 ? keep[1] : k < 96 ? keep[2] : keep[3];
+                        mx = (kw >> (k & 31)) & 1u ? fmaxf(mx, __uint_as_float(sk)) : mx;
+                    }
+                    grow(mx);
+                    const float mb = m == NEG_INF ? 0.f : m * a.scale_log2;
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {                 // 16 dims at a time
+                        uint32_t raw[16];
+                        float o[16];
                         if (steps > 0) {
-                            tmem_ld32(to + 128 * wg + 32 * c, o);
+                            tmem_ld16(to + 128 * wg + 16 * c, raw);
                             tmem_wait_ld();
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                o[i] = 0u;
                         }
-                        const uint32_t e = 2 * tile + 1;
-                        const uint8_t *half = sm.ring[e % kTStages] + (c >> 1) * kTHalf;
 #pragma unroll
-                        for (int kc = 0; kc < 4; ++kc)
-                            for (int k = 0; k < 32; ++k) {
-                                __syncwarp();
-                                const uint32_t raw = tmem_ld1(ts + 32 * kc + k);
-                                tmem_wait_ld();
-                                if (!((keep[kc] >> k) & 1u))
-                                    continue;                    // (lanes meet again above)
-                                const float p = ex2(fmaf(__uint_as_float(raw), a.scale_log2, -mb));
+                        for (int i = 0; i < 16; ++i) {
+                            asm volatile("" : "+r"(raw[i]));
+                            o[i] = steps > 0 ? __uint_as_float(raw[i]) : 0.f;
+                        }
+#pragma unroll 1
+                        for (int k = 0; k < 16 * (flags >> kGroups); ++k) {
+                            __syncwarp();
+                            uint32_t sk = tmem_ld1(ts + k);
+                            tmem_wait_ld();
+                            asm volatile("" : "+r"(sk));
+                            const uint32_t kw = k < 32 ? keep[0] : k < 64 ? keep[1] : k < 96 ? keep[2] : keep[3];
+                            if ((kw >> (k & 31)) & 1u) {
+                                const float p = ex2(fmaf(__uint_as_float(sk), a.scale_log2, -mb));
                                 sum += c == 0 ? p : 0.f;
-                                const int row = 32 * kc + k;
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
+                                for (int j = 0; j < 2; ++j) {
                                     const uint4 v = *reinterpret_cast<const uint4 *>(
-                                        half + row * 128 + ((((c & 1) * 4 + j) ^ (row & 7)) << 4));
+                                        v0 + (c >> 2) * kTHalf + k * 128 + ((((c & 3) * 2 + j) ^ (k & 7)) << 4));
                                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                                     for (int q = 0; q < 4; ++q) {
-                                        float *f = reinterpret_cast<float *>(o) + 8 * j + 2 * q;
-                                        f[0] = fmaf(p, __uint_as_float(w[q] << 16), f[0]);
-                                        f[1] = fmaf(p, __uint_as_float(w[q] & 0xffff0000u), f[1]);
+                                        o[8 * j + 2 * q] = fmaf(p, __uint_as_float(w[q] << 16), o[8 * j + 2 * q]);
+                                        o[8 * j + 2 * q + 1] = fmaf(p, __uint_as_float(w[q] & 0xffff0000u), o[8 * j + 2 * q + 1]);
                                     }
                                 }
                             }
+                        }
                         __syncwarp();
-                        tmem_st32(to + 128 * wg + 32 * c, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            raw[i] = __float_as_uint(o[i]);
+                        tmem_st16(to + 128 * wg + 16 * c, raw);
                     }
                     l += sum;
                 }
@@ -842,7 +1161,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem &sm, ui
         float f0 = 1.f, f1 = 0.f;
         bool both = false;
         float M = m == NEG_INF ? NEG_INF : m * a.scale_log2;
-        if (!s.two) {
+        if (!two) {
             sm.ml[wg][r] = make_float2(M, l);
             __syncwarp();
             if (lane == 0)
@@ -859,49 +1178,59 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem &sm, ui
         }
         if (active) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const bool whole = s.t0 == 0 && s.t1 == s.nt;
+            const bool none = l == 0.f, whole = s.t0 == 0 && s.t1 == s.nt;
+            f0 *= inv;
+            f1 *= inv;
             const int64_t prow = static_cast<int64_t>(s.slot) * a.rows_slot + mt * kTTile + r;
-            const int c0 = s.two ? 0 : 2 * wg, c1 = s.two ? 4 : c0 + 2;
+            const int c0 = two ? 0 : 2 * wg, c1 = two ? 4 : c0 + 2;
+            __nv_bfloat16 *o = a.O + s.b * a.o_sb + t * a.o_st + (s.h * a.g + hh) * a.o_sh;
+            float *po = a.part_o + prow * EA_HEAD_DIM;
+            const uint32_t t0 = to + (two ? 128 * wg : 0);
+#pragma unroll 1
             for (int c = c0; c < c1; ++c) {
                 uint32_t x[32];
                 __syncwarp();
-                tmem_ld32(to + (s.two ? 128 * wg : 0) + 32 * c, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    x[i] = __float_as_uint(__uint_as_float(x[i]) * f0);
+                tmem_ld32(t0 + 32 * c, x);
                 if (both) {
                     uint32_t y[32];
                     tmem_ld32(to + 128 + 32 * c, y);
                     tmem_wait_ld();
+                    tie32(x);
+                    tie32(y);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), f1, __uint_as_float(x[i])));
-                }
+                        x[i] = __float_as_uint(fmaf(__uint_as_float(y[i]), f1, __uint_as_float(x[i]) * f0));
+                } else {
+                    tmem_wait_ld();
+                    tie32(x);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    x[i] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(x[i]) * inv);
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = __float_as_uint(__uint_as_float(x[i]) * f0);
+                }
+                if (none) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = 0u;
+                }
                 if (valid) {
                     if (whole) {
-                        __nv_bfloat16 *o = a.O + s.b * a.o_sb + t * a.o_st + (s.h * a.g + hh) * a.o_sh + 32 * c;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             uint32_t w[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 w[k] = pack_bf16x2(__uint_as_float(x[8 * i + 2 * k]), __uint_as_float(x[8 * i + 2 * k + 1]));
-                            reinterpret_cast<uint4 *>(o)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4 *>(o + 32 * c)[i] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     } else if (in_bounds(prow, 2 * static_cast<int64_t>(gridDim.x) * a.rows_slot, err)) {
-                        float *o = a.part_o + prow * EA_HEAD_DIM + 32 * c;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            st_global_v8(o + 8 * i, x + 8 * i);
+                            st_global_v8(po + 32 * c + 8 * i, x + 8 * i);
                     }
                 }
             }
-            if (valid && (s.two || wg == 0)) {
-                const float l2 = l == 0.f ? NEG_INF : (M == NEG_INF ? 0.f : M) + tree_lg2(l);
+            if (valid && (two || wg == 0)) {
+                const float l2 = none ? NEG_INF : (M == NEG_INF ? 0.f : M) + tree_lg2(l);
                 if (!whole) {
                     if (in_bounds(prow, 2 * static_cast<int64_t>(gridDim.x) * a.rows_slot, err))
                         a.part_lse[prow] = l2;
@@ -918,96 +1247,50 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, TreeSmem &sm, ui
 }
 
 // ------------------------------------------------------------ kernels
-// This CTA's range of the line of tiles: [i W / G, (i + 1) W / G) of its W tiles, G CTAs (fewer
-// where a range would be shorter than min_tiles).
-__device__ __forceinline__ void tree_range(const TreeArgs &a, TreeSmem &sm)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, units = a.B * a.Hkv;
-    const int per = (units + blockDim.x - 1) / static_cast<int>(blockDim.x);
-    const int lo = min(tid * per, units), hi = min(lo + per, units);
-    int64_t mine = 0;
-    bool bad = false;
-    for (int u = lo; u < hi; ++u) {
-        const TreeUnit x = tree_unit(a, u);
-        mine += static_cast<int64_t>(x.nt) * x.pairs;
-        bad |= x.bad;
-    }
-    if (bad && blockIdx.x == 0)
-        raise_error(&a.hdr->error, EA_DEVERR_CHECK);
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
-            incl += v;
-    }
-    int64_t *tot = reinterpret_cast<int64_t *>(sm.ml);
-    if (lane == 31)
-        tot[warp] = incl;
-    if (tid == 0)
-        sm.count = 0;
-    __syncthreads();
-    int64_t before = 0, W = 0;
-    for (int w = 0; w < static_cast<int>(blockDim.x) / 32; ++w) {
-        before += w < warp ? tot[w] : 0;
-        W += tot[w];
-    }
-    int64_t base = before + incl - mine;
-    const int64_t G = max(static_cast<int64_t>(1), min(static_cast<int64_t>(gridDim.x), W / a.min_tiles));
-    const int64_t i = blockIdx.x;
-    const int64_t start = i * W / G, end = (i + 1) * W / G;
-    if (i < G && start < end && start >= base && start < base + mine)
-        for (int u = lo; u < hi; ++u) {
-            const TreeUnit x = tree_unit(a, u);
-            const int64_t w = static_cast<int64_t>(x.nt) * x.pairs;
-            if (start < base + w) {
-                sm.unit = u;
-                sm.off = start - base;
-                sm.count = end - start;
-                break;
-            }
-            base += w;
-        }
-    __syncthreads();
-}
-
-template <int FMT>
+template <int FMT, bool TWO>
 __global__ void __launch_bounds__(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8, 1)
     tree_attn_kernel(const __grid_constant__ TreeMaps tm, const TreeArgs a)
 {
     constexpr bool kQ8 = FMT != EA_CACHE_BF16;
+    using Smem = TreeSmem<kQ8, TWO>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
-    TreeSmem &sm = *reinterpret_cast<TreeSmem *>(smem_raw);
+    Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (smem_u32(smem_raw) & 1023u) {                  // the operands' layout needs it
         if (threadIdx.x == 0)
             raise_error(&a.hdr->error, EA_DEVERR_BOUNDS);
         return;
     }
-    if (threadIdx.x == 0) {
-        const int users = 1 + 8 + kTFixWarps + (kQ8 ? kTConvWarps : 0);
-        for (int s = 0; s < kTStages; ++s) {
-            mbar_init(&sm.full[s], 1 + (kQ8 ? kTConvWarps : 0));
-            mbar_init(&sm.empty[s], 1 + kTFixWarps);
+    if (warp == 0) {
+        constexpr int users = 1 + 8 + kTFixWarps + (kQ8 ? kTConvWarps : 0);
+        if (lane < Smem::kStages) {
+            mbar_init(&sm.full[lane], kQ8 ? kTConvWarps / 2 : 1);
+            mbar_init(&sm.empty[lane], 1 + kTFixWarps);
         }
-        for (int s = 0; s < kTReady; ++s)
-            mbar_init(&sm.ready[s], kTFixWarps);
-        for (int s = 0; s < kTSegs; ++s) {
-            mbar_init(&sm.seg_full[s], 1);
-            mbar_init(&sm.seg_empty[s], users);
+        if (lane < Smem::kCodes) {
+            mbar_init(&sm.code_full[lane], 1);
+            mbar_init(&sm.code_empty[lane], kTConvWarps / 2);
         }
-        mbar_init(&sm.q_full, 1);
-        mbar_init(&sm.q_empty, 1);
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(&sm.s_full[w], 1);
-            mbar_init(&sm.p_full[w], 4);
-            mbar_init(&sm.o_done[w], 1);
+        if (lane < kTReady)
+            mbar_init(&sm.ready[lane], kTFixWarps);
+        if (lane < kTSegs) {
+            mbar_init(&sm.seg_full[lane], 1);
+            mbar_init(&sm.seg_empty[lane], users);
         }
-        mbar_init(&sm.seg_done, 1);
-        mbar_init(&sm.ml_full, 8);
-        mbar_init(&sm.o_free, 8);
-        mbar_init(&sm.drain, 1);
-        sm.abort = 0;
+        if (lane < 2) {
+            mbar_init(&sm.s_full[lane], 1);
+            mbar_init(&sm.p_full[lane], 4);
+            mbar_init(&sm.o_done[lane], 1);
+        }
+        if (lane == 0) {
+            mbar_init(&sm.q_full, 1);
+            mbar_init(&sm.q_empty, 1);
+            mbar_init(&sm.seg_done, 1);
+            mbar_init(&sm.ml_full, 8);
+            mbar_init(&sm.o_free, 8);
+            mbar_init(&sm.drain, 1);
+            sm.abort = 0;
+        }
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -1022,23 +1305,39 @@ __global__ void __launch_bounds__(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8
     }
     griddep_wait();
     griddep_launch_dependents();
-    tree_range(a, sm);                                  // (its barriers order the set-up too)
+    if (a.B * a.Hkv > kTWarpUnits)
+        tree_range(a, sm, threadIdx.x, blockDim.x / 32);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
-    if (warp < 8)
+    // Registers go to the softmax: 256 x 208 + 128 x 88 of the launch's 384 x 168, or, with
+    // converting warps, 256 x 144 + 128 x 72 + 256 x 56 of its 640 x 96.
+    if (warp < 8) {
+        if constexpr (kQ8)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         tree_softmax(a, sm, tmem, warp, lane);
-    else if (warp == kTProducerWarp)
-        tree_producer<kQ8>(tm, a, sm, lane);
-    else if (warp == kTMmaWarp) {
-        if (lane == 0)
-            tree_mma(a, sm, tmem);
-    } else if (warp < kTConvWarp)
-        tree_fix(a, sm, warp, lane);
-    else if constexpr (kQ8)
-        tree_convert<FMT == EA_CACHE_E4M3>(a, sm, threadIdx.x - kTConvWarp * 32, lane);
+    } else if (warp < kTConvWarp) {
+        if constexpr (kQ8)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == kTProducerWarp) {
+            tree_producer(tm, a, sm, lane);
+        } else if (warp == kTMmaWarp) {
+            tree_mma(a, sm, tmem, lane);
+        } else {
+            tree_fix(tm, a, sm, warp, lane);
+        }
+    } else {
+        if constexpr (kQ8) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+            tree_convert<FMT == EA_CACHE_E4M3>(tm, a, sm, (warp - kTConvWarp) / 4, threadIdx.x % 128, lane);
+        }
+    }
 
     __syncwarp();
     tc_fence_before();
@@ -1117,29 +1416,40 @@ __global__ void __launch_bounds__(kTMergeWarps * 32) tree_merge_kernel(const Tre
         return;                                          // written by its CTA
     const int64_t in_slot = (mt & 1) * kTTile + (t - mt * a.tpt) * a.g + hh;
     auto part = [&](int c) { return (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * a.rows_slot + in_slot; };
-    float M = NEG_INF;
-    for (int c = c0 + lane; c <= c1; c += 32)
-        M = fmaxf(M, a.part_lse[part(c)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float ref = M == NEG_INF ? 0.f : M;
-    float w = 0.f;
+    // eight parts' weights and data at a time
+    float M = NEG_INF, w = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int cb = c0; cb <= c1; cb += 32) {
-        const float mine = cb + lane <= c1 ? ex2(a.part_lse[part(cb + lane)] - ref) : 0.f;
-        const int k1 = min(32, c1 - cb + 1);
-#pragma unroll 4
-        for (int k = 0; k < k1; ++k) {
-            const float e = __shfl_sync(0xffffffffu, mine, k);
-            const float4 x = *reinterpret_cast<const float4 *>(a.part_o + part(cb + k) * EA_HEAD_DIM + 4 * lane);
-            w += e;
-            acc.x = fmaf(e, x.x, acc.x);
-            acc.y = fmaf(e, x.y, acc.y);
-            acc.z = fmaf(e, x.z, acc.z);
-            acc.w = fmaf(e, x.w, acc.w);
+    for (int cb = c0; cb <= c1; cb += 8) {
+        float l[8];
+        float4 x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int64_t p = part(min(cb + k, c1));
+            l[k] = cb + k <= c1 ? a.part_lse[p] : NEG_INF;
+            x[k] = *reinterpret_cast<const float4 *>(a.part_o + p * EA_HEAD_DIM + 4 * lane);
+        }
+        float mx = M;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            mx = fmaxf(mx, l[k]);
+        const float f = M == NEG_INF ? 1.f : ex2(M - mx);            // (nothing, or NaN, before)
+        M = mx;
+        const float ref = M == NEG_INF ? 0.f : M;
+        w *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float e = cb + k <= c1 ? ex2(l[k] - ref) : 0.f;
+            if (cb + k <= c1) {
+                w += e;
+                acc.x = fmaf(e, x[k].x, acc.x);
+                acc.y = fmaf(e, x[k].y, acc.y);
+                acc.z = fmaf(e, x[k].z, acc.z);
+                acc.w = fmaf(e, x[k].w, acc.w);
+            }
         }
     }
+    const float ref = M == NEG_INF ? 0.f : M;
     const float inv = w == 0.f ? 0.f : 1.f / w;
     const uint2 o = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
     *reinterpret_cast<uint2 *>(a.O + b * a.o_sb + t * a.o_st + qh * a.o_sh + 4 * lane) = o;
@@ -1149,8 +1459,6 @@ __global__ void __launch_bounds__(kTMergeWarps * 32) tree_merge_kernel(const Tre
 }
 
 // ------------------------------------------------------------ host
-constexpr int kTMinTiles = 2;
-
 struct TreeWs {
     size_t first, last, blk_count, blk_list, part_lse, part_o, total;
     int tpt, pairs, rows_slot;
@@ -1188,6 +1496,12 @@ static bool tree_sizes_ok(int B, int T, int Hq, int Hkv, int d)
            static_cast<int64_t>(B) * T * Hq <= (int64_t(1) << 33);
 }
 
+// The tiles of a step at most, which the kernel counts in 32 bits.
+static bool tree_tiles_ok(int B, int Hkv, int pairs, int Lmax)
+{
+    return static_cast<double>(B) * Hkv * pairs * (ceil_div(Lmax, kTTile) + 1) < 2147483648.;
+}
+
 static bool tree_tensor(const void *p, const int64_t *str)
 {
     if (!p || !str || str[3] != 1 || (reinterpret_cast<uintptr_t>(p) & 15u))
@@ -1198,13 +1512,14 @@ static bool tree_tensor(const void *p, const int64_t *str)
     return true;
 }
 
-template <int FMT>
+template <int FMT, bool TWO>
 static cudaError_t launch_tree(const TreeMaps &tm, const TreeArgs &a, int grid, bool after, cudaStream_t st, int dev)
 {
+    constexpr size_t kSmem = sizeof(TreeSmem<FMT != EA_CACHE_BF16, TWO>);
     static bool attr_done[64] = {};   // the attribute is set once per device
     if (dev >= 64 || !attr_done[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(kTSmemBytes));
+        const cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<FMT, TWO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(kSmem));
         if (e != cudaSuccess)
             return e;
         if (dev < 64)
@@ -1216,11 +1531,18 @@ static cudaError_t launch_tree(const TreeMaps &tm, const TreeArgs &a, int grid, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8);
-    cfg.dynamicSmemBytes = kTSmemBytes;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = after ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tree_attn_kernel<FMT>, tm, a);
+    return cudaLaunchKernelEx(&cfg, tree_attn_kernel<FMT, TWO>, tm, a);
+}
+
+template <int FMT>
+static cudaError_t launch_tree_fmt(const TreeMaps &tm, const TreeArgs &a, int grid, bool after, cudaStream_t st, int dev)
+{
+    return a.rows_slot > kTTile ? launch_tree<FMT, true>(tm, a, grid, after, st, dev)
+                                : launch_tree<FMT, false>(tm, a, grid, after, st, dev);
 }
 
 } // namespace ea
@@ -1231,7 +1553,8 @@ extern "C" size_t ea_tree_workspace_size(int B, int T, int Hq, int Hkv, int d, i
 {
     if (!tree_sizes_ok(B, T, Hq, Hkv, d) || Lmax < 1)
         return 0;
-    return tree_ws_layout(B, T, Hq, Hkv, Lmax).total;
+    const TreeWs w = tree_ws_layout(B, T, Hq, Hkv, Lmax);
+    return tree_tiles_ok(B, Hkv, w.pairs, Lmax) ? w.total : 0;
 }
 
 extern "C" ea_status ea_hybrid_attn_tree(const void *Q, const void *K, const void *V, const ea_cache *cache, void *O,
@@ -1255,6 +1578,8 @@ extern "C" ea_status ea_hybrid_attn_tree(const void *Q, const void *K, const voi
     if (!tree_sizes_ok(B, T, Hq, Hkv, EA_HEAD_DIM) || (a.c.table && a.c.rows % 64) || (block_mask && nBm > 65535))
         return EA_ERR_UNSUPPORTED;
     const TreeWs w = tree_ws_layout(B, T, Hq, Hkv, Lmax);
+    if (!tree_tiles_ok(B, Hkv, w.pairs, Lmax))
+        return EA_ERR_UNSUPPORTED;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || ws_bytes < w.total)
         return EA_ERR_WORKSPACE;
 
@@ -1273,8 +1598,10 @@ extern "C" ea_status ea_hybrid_attn_tree(const void *Q, const void *K, const voi
             !encode_tmap_bf16_rows(&tm.v, a.c.code[1], Hkv, a.c.rows, a.c.outer, cache->kv_str, 1, box))
             return EA_ERR_INVALID_ARG;
     } else {
-        tm.k = tm.kd;
-        tm.v = tm.vd;
+        const int box = a.box128 ? kTTile : 64;
+        if (!encode_tmap_u8_plain(&tm.k, a.c.code[0], Hkv, a.c.rows, a.c.outer, cache->kv_str, box) ||
+            !encode_tmap_u8_plain(&tm.v, a.c.code[1], Hkv, a.c.rows, a.c.outer, cache->kv_str, box))
+            return EA_ERR_INVALID_ARG;
     }
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.O = static_cast<__nv_bfloat16 *>(O);
@@ -1305,7 +1632,6 @@ extern "C" ea_status ea_hybrid_attn_tree(const void *Q, const void *K, const voi
     // positions stay below 2^31 - 128: larger limits say the same
     a.sink = sink < (1 << 30) ? sink : 0x7fffffff;
     a.window = window;
-    a.min_tiles = kTMinTiles;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.grow = kTGrow / a.scale_log2;
 
@@ -1321,11 +1647,11 @@ extern "C" ea_status ea_hybrid_attn_tree(const void *Q, const void *K, const voi
         tree_blocks_kernel<<<static_cast<unsigned>(B) * Hkv, kTBlkThreads, 0, st>>>(a);
     cudaError_t e;
     if (wide)
-        e = launch_tree<EA_CACHE_BF16>(tm, a, grid, block_mask != nullptr, st, dev);
+        e = launch_tree_fmt<EA_CACHE_BF16>(tm, a, grid, block_mask != nullptr, st, dev);
     else if (a.c.format == EA_CACHE_E4M3)
-        e = launch_tree<EA_CACHE_E4M3>(tm, a, grid, block_mask != nullptr, st, dev);
+        e = launch_tree_fmt<EA_CACHE_E4M3>(tm, a, grid, block_mask != nullptr, st, dev);
     else
-        e = launch_tree<EA_CACHE_INT8>(tm, a, grid, block_mask != nullptr, st, dev);
+        e = launch_tree_fmt<EA_CACHE_INT8>(tm, a, grid, block_mask != nullptr, st, dev);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg{};
         cudaLaunchAttribute attr[1];
