@@ -22,9 +22,10 @@
 // Roles of a CTA:
 //   warps 0-7    two softmax warpgroups.  With two M tiles each has one; with one they take
 //                key tiles in turn, each with its own O, m and l, joined at the range's end.
-//   warp 8       ranges, Q, and by TMA the K and V tiles into a ring of 32 KB entries
-//   warp 9       the MMAs: S two tiles ahead of the products that use them
-//   warps 10-11  V's rows that no query row keeps are zeroed before the product (0 * NaN is
+//   warp 8       the range, and by TMA the K and V tiles into a ring of 32 KB entries
+//   warp 9       S = Q K^T
+//   warp 10      O += P V
+//   warp 11      Q, and V's rows that no query row keeps are zeroed before the product (0 * NaN is
 //                NaN), and tiles of which some rows keep a key and others do not are searched
 //                for infinities and NaN; such a tile's product is taken by the softmax warps,
 //                key by key
@@ -43,13 +44,15 @@ constexpr int kTBytes = kTTile * EA_HEAD_DIM * 2;     // a tile of K, V or Q: 32
 constexpr int kTHalf = kTBytes / 2;                   // 64 dims of 128 rows
 constexpr int kTInfos = 8;                            // tile descriptions in flight: the rings and S hold six tiles at most
 constexpr int kTReady = 8;
-constexpr int kTSegs = 4;
-constexpr int kTProducerWarp = 8, kTMmaWarp = 9, kTFixWarp = 10, kTFixWarps = 2, kTConvWarp = 12, kTConvWarps = 8;
+constexpr int kTSegs = 3;
+constexpr int kTProducerWarp = 8, kTQkWarp = 9, kTPvWarp = 10, kTConvWarp = 12, kTConvWarps = 8;
 constexpr int kTThreads = kTConvWarp * 32, kTThreadsQ8 = (kTConvWarp + kTConvWarps) * 32;
 constexpr uint32_t kTColO = 256;                      // TMEM: S0, S1, O0, O1
 constexpr uint32_t kTIdescQK = idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t kTIdescPV = idesc_bf16_f32(128, 128, false, true);
+constexpr uint32_t kTIdescBf16 = 1u << 7 | 1u << 10;  // the operands' type: bf16; without these bits f16
 constexpr float kTGrow = 8.f;                         // the maximum is followed once it grew by 2^8: p <= 2^8
+constexpr float kTShift = 7.f;                        // 8-bit caches: p is f16, at most 2^(7 + 8)
 constexpr int kTMinTiles = 2;                         // of a range at least (a power of two)
 constexpr int kTSms = 152;                            // a workspace's size depends on the grid
 
@@ -69,7 +72,7 @@ struct TreeArgs {
     ea_ws_header *hdr;
     CacheDev c;
     int B, T, Hq, Hkv, g, tpt, pairs, nBm, sink, window, box128, rows_slot;
-    float scale_log2, grow;
+    float scale_log2;
 };
 
 struct TreeMaps {
@@ -187,9 +190,12 @@ struct __align__(1024) TreeSmem {
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], o_done[2];
     uint64_t seg_done, ml_full, o_free, drain;
+    uint64_t q_ready, own_full[2], own_max[2];   // 8-bit caches: Q in f16; the tree's K and V
     TreeSeg seg[kTSegs];
     TreeTile tile[kTInfos];
-    int odd[kTReady][kTFixWarps];        // V holds an infinity or a NaN
+    float k_unit[kTInfos], v_log[kTInfos];       // 8-bit caches: a tile's f16 numbers stand for k_unit, 2^v_log times them
+    uint8_t own_exp[2][2][4];
+    uint8_t odd[kTReady];                // V holds an infinity or a NaN
     TreeUnit unit;                       // this CTA's range: its first unit,
     int u, off, count;                   // where it starts in it, and its tiles
     uint32_t tmem_base;
@@ -277,18 +283,23 @@ __device__ __forceinline__ uint32_t cols_below(int n, int c)
     return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u;
 }
 
-// Segment number `it` (slot it % kTSegs), by a whole warp; false: gave up.
+// Part number `it` of the range (in slot it % kTSegs, held until tree_done), by a whole warp; NULL: none
+// left, or gave up.
 template <class Smem>
-__device__ __forceinline__ bool tree_take(const TreeArgs &a, Smem &sm, uint32_t it, TreeSeg &s)
+__device__ __forceinline__ const TreeSeg *tree_take(const TreeArgs &a, Smem &sm, uint32_t it)
 {
     const int slot = it % kTSegs;
     if (!mbar_wait_warp(&sm.seg_full[slot], (it / kTSegs) & 1, &sm.abort, &a.hdr->error))
-        return false;
-    s = sm.seg[slot];
+        return nullptr;
+    return sm.seg[slot].valid ? &sm.seg[slot] : nullptr;
+}
+
+template <class Smem>
+__device__ __forceinline__ void tree_done(Smem &sm, uint32_t it)
+{
     __syncwarp();
     if ((threadIdx.x & 31) == 0)
-        mbar_arrive(&sm.seg_empty[slot]);
-    return s.valid != 0;
+        mbar_arrive(&sm.seg_empty[it % kTSegs]);
 }
 
 // ------------------------------------------------------------ ranges
@@ -374,7 +385,7 @@ __device__ __forceinline__ void tree_place(const TreeArgs &a, int b, int L, int 
 }
 
 // K or V of the tree's own tokens (rows behind the tensor read zeros).
-__device__ __forceinline__ void tree_load_draft(const TreeMaps &tm, uint8_t *dst, int kv, const TreeSeg &s, uint64_t *bar)
+__device__ __forceinline__ void tree_load_own(const TreeMaps &tm, uint8_t *dst, int kv, const TreeSeg &s, uint64_t *bar)
 {
     mbar_arrive_expect_tx(bar, kTBytes);
 #pragma unroll
@@ -511,7 +522,7 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
                     if (kv == 0)
                         sm.tile[tile % kTInfos] = ti;
                     if (ti.flags & kDraft) {
-                        tree_load_draft(tm, dst, kv, s, bar);
+                        tree_load_own(tm, dst, kv, s, bar);
                     } else if (a.box128) {
                         mbar_arrive_expect_tx(bar, kTBytes);
 #pragma unroll
@@ -550,104 +561,58 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
 }
 
 // ------------------------------------------------------------ products
-// One warp, one thread of it for the MMAs: S = Q K^T of a step once O += P V of the step two before
-// (the last user of that S) is issued.  The warp stays whole and its values uniform, so that the
-// operands' descriptors are worked out in uniform registers: by one thread alone, eight MMAs took 750
-// cycles to issue, more than they take.  (Taking whichever product is ready first, by polling, costs
-// the softmax warps beside it their issue slots.)
+// Two warps, one for S = Q K^T and one for O += P V (an issue with its waits and commits takes one warp
+// about 1000 cycles, as long as the products take: one warp for both paced the kernel), one thread of
+// each for the MMAs.  The warps stay whole and their values uniform, so that the operands' descriptors
+// are worked out in uniform registers: in one thread's own branch, eight MMAs took 750 cycles to issue.
 template <class Smem>
-__device__ __forceinline__ void tree_mma(const TreeArgs &a, Smem &sm, uint32_t tmem_base, int lane)
+__device__ __forceinline__ void tree_qk(const TreeArgs &a, Smem &sm, uint32_t tmem_base)
 {
     constexpr int kStages = Smem::kStages;
     constexpr bool TWO = sizeof(sm.q) > kTBytes;
+    constexpr uint32_t kIdQK = (Smem::Q8 ? kTIdescQK & ~kTIdescBf16 : kTIdescQK) & ~(63u << 17);
     volatile int *abort = &sm.abort;
     uint32_t *err = &a.hdr->error;
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
     const uint64_t q0 = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), ring0 = sdesc_sw128(smem_u32(sm.ring[0]), 16, 1024);
-    const uint64_t vring0 = sdesc_sw128(smem_u32(sm.ring[0]), kTHalf, 1024);
     const uint32_t go = elect_one();
-    uint32_t tile0 = 0, p_cnt[2] = {0, 0};
-    bool ok = true;
-    for (uint32_t it = 0; ok; ++it) {
-        const int slot = it % kTSegs;
-        if (!mbar_wait_warp(&sm.seg_full[slot], (it / kTSegs) & 1, abort, err))
-            break;
-        const int valid = __shfl_sync(0xffffffffu, sm.seg[slot].valid, 0);
-        const int two = TWO ? __shfl_sync(0xffffffffu, sm.seg[slot].two, 0) : 0;
-        const int nt = __shfl_sync(0xffffffffu, sm.seg[slot].t1 - sm.seg[slot].t0, 0);
-        __syncwarp();
-        if (lane == 0)
-            mbar_arrive(&sm.seg_empty[slot]);
-        if (!valid)
-            break;
-        if (!mbar_wait_warp(&sm.q_full, it & 1, abort, err))
+    uint32_t tile0 = 0, cnt[2] = {0, 0};
+    const TreeSeg *sp;
+    for (uint32_t it = 0; (sp = tree_take(a, sm, it)) != nullptr; ++it) {
+        const int two = TWO ? __shfl_sync(0xffffffffu, sp->two, 0) : 0;
+        const int nt = __shfl_sync(0xffffffffu, sp->t1 - sp->t0, 0);
+        if (!mbar_wait_warp(Smem::Q8 ? &sm.q_ready : &sm.q_full, it & 1, abort, err))
             break;
         const int N = nt << two;
-        for (int n = 0; n < N + 2; ++n) {
+        for (int n = 0; n < N; ++n) {
             const int w = n & 1;
-            if (n >= 2) {
-                const int pv = n - 2;
-                const uint32_t tile = tile0 + (pv >> two), e = 2 * tile + 1;
-                const int st = e % kStages;
-                // (O is still read for the range's part before)
-                if ((pv == 0 && it > 0 && !mbar_wait_warp(&sm.o_free, (it - 1) & 1, abort, err)) ||
-                    !mbar_wait_warp(&sm.ready[tile % kTReady], (tile / kTReady) & 1, abort, err) ||
-                    !mbar_wait_warp(&sm.p_full[w], p_cnt[w] & 1, abort, err)) {
-                    ok = false;
-                    break;
-                }
-                ++p_cnt[w];
-                tc_fence_after();
-                const int odd = __shfl_sync(0xffffffffu, sm.odd[tile % kTReady][0] | sm.odd[tile % kTReady][1], 0);
-                const int groups = __shfl_sync(0xffffffffu, sm.tile[tile % kTInfos].flags >> kGroups, 0);
-                const uint64_t vd = vring0 + static_cast<uint64_t>(st * (kTBytes >> 4));
-                const uint32_t tp = tmem + 128 * w, to = tmem + kTColO + 128 * w;
-                // (a warpgroup's first product of the range overwrites what its O held)
-                const uint32_t more = pv >= 2;
-                if (!odd) {
-                    if (groups == 8) {
+            const uint32_t tile = tile0 + (n >> two), e = 2 * tile;
+            const int st = e % kStages;
+            const uint64_t qd = q0 + static_cast<uint64_t>((two & w) * (kTBytes >> 4));
+            const uint64_t kd = ring0 + static_cast<uint64_t>(st * (kTBytes >> 4));
+            const uint32_t ts = tmem + 128 * w;
+            // K, and this S's last user, the product two steps before
+            bool in = mbar_wait(&sm.full[st], (e / kStages) & 1, abort, err);
+            in = in && (cnt[w] == 0 || mbar_wait(&sm.o_done[w], (cnt[w] - 1) & 1, abort, err));
+            if (!__all_sync(0xffffffffu, in))
+                break;
+            ++cnt[w];
+            tc_fence_after();
+            // (a tile with fewer keys: the columns behind them are masked)
+            const uint32_t id = kIdQK | static_cast<uint32_t>(__shfl_sync(0xffffffffu, sm.tile[tile % kTInfos].flags >> kGroups, 0)) << 18;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_ts(go, to, tp + (k < 4 ? 8 * k : 32 + 8 * k), vd + k * (2048 >> 4), kTIdescPV, k ? 1u : more);
-                    } else {
-#pragma unroll 1
-                        for (int k = 0; k < groups; ++k)
-                            mma_ts(go, to, tp + (k < 4 ? 8 * k : 32 + 8 * k), vd + k * (2048 >> 4), kTIdescPV, k ? 1u : more);
-                    }
-                }
-                commit_if(go, &sm.o_done[w]);
-                if (!two || w == 1)
-                    commit_if(go, &sm.empty[st]);
-                if (pv == N - 1)
-                    commit_if(go, &sm.seg_done);
+            for (int k = 0; k < 8; ++k) {
+                const uint64_t o = ((k >> 2) * kTHalf + (k & 3) * 32) >> 4;
+                mma_ss(go, ts, qd + o, kd + o, id, k > 0);
             }
-            if (n < N) {
-                const uint32_t tile = tile0 + (n >> two), e = 2 * tile;
-                const int st = e % kStages;
-                if (!mbar_wait_warp(&sm.full[st], (e / kStages) & 1, abort, err)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint64_t qd = q0 + static_cast<uint64_t>((two & w) * (kTBytes >> 4));
-                const uint64_t kd = ring0 + static_cast<uint64_t>(st * (kTBytes >> 4));
-                // (a tile with fewer keys: the columns behind them are masked)
-                const int groups = __shfl_sync(0xffffffffu, sm.tile[tile % kTInfos].flags >> kGroups, 0);
-                const uint32_t id = (kTIdescQK & ~(63u << 17)) | static_cast<uint32_t>(groups) << 18;
-                const uint32_t ts = tmem + 128 * w;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint64_t o = ((k >> 2) * kTHalf + (k & 3) * 32) >> 4;
-                    mma_ss(go, ts, qd + o, kd + o, id, k > 0);
-                }
-                commit_if(go, &sm.s_full[w]);
-                if (!two || w == 1)
-                    commit_if(go, &sm.empty[st]);
-                if (n == N - 1)
-                    commit_if(go, &sm.q_empty);
-            }
+            commit_if(go, &sm.s_full[w]);
+            if (!two || w == 1)
+                commit_if(go, &sm.empty[st]);
+            if (n == N - 1)
+                commit_if(go, &sm.q_empty);
         }
         tile0 += nt;
+        tree_done(sm, it);
     }
     // All of this warp's MMAs must have completed before TMEM is released.
     commit_if(go, &sm.drain);
@@ -655,34 +620,95 @@ __device__ __forceinline__ void tree_mma(const TreeArgs &a, Smem &sm, uint32_t t
     mbar_wait_warp(&sm.drain, 0, &no_abort, err);
 }
 
-// ------------------------------------------------------------ V's rows
-__device__ __forceinline__ uint32_t odd_bf16x2(uint32_t w)
+template <class Smem>
+__device__ __forceinline__ void tree_pv(const TreeArgs &a, Smem &sm, uint32_t tmem_base)
 {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+    constexpr int kStages = Smem::kStages;
+    constexpr bool TWO = sizeof(sm.q) > kTBytes;
+    constexpr uint32_t kIdPV = Smem::Q8 ? kTIdescPV & ~kTIdescBf16 : kTIdescPV;
+    volatile int *abort = &sm.abort;
+    uint32_t *err = &a.hdr->error;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+    const uint64_t ring0 = sdesc_sw128(smem_u32(sm.ring[0]), kTHalf, 1024);
+    const uint32_t go = elect_one();
+    uint32_t tile0 = 0, cnt[2] = {0, 0};
+    const TreeSeg *sp;
+    for (uint32_t it = 0; (sp = tree_take(a, sm, it)) != nullptr; ++it) {
+        const int two = TWO ? __shfl_sync(0xffffffffu, sp->two, 0) : 0;
+        const int nt = __shfl_sync(0xffffffffu, sp->t1 - sp->t0, 0);
+        // (O is still read for the range's part before)
+        if (it > 0 && !mbar_wait_warp(&sm.o_free, (it - 1) & 1, abort, err))
+            break;
+        const int N = nt << two;
+        for (int n = 0; n < N; ++n) {
+            const int w = n & 1;
+            const uint32_t tile = tile0 + (n >> two), e = 2 * tile + 1;
+            const int st = e % kStages;
+            const uint64_t vd = ring0 + static_cast<uint64_t>(st * (kTBytes >> 4));
+            const uint32_t tp = tmem + 128 * w, to = tmem + kTColO + 128 * w;
+            // (a warpgroup's first product of the range overwrites what its O held)
+            const uint32_t more = n >= 2;
+            bool in = mbar_wait(&sm.ready[tile % kTReady], (tile / kTReady) & 1, abort, err);
+            const int flags = __shfl_sync(0xffffffffu, sm.tile[tile % kTInfos].flags, 0);
+            const int odd = __shfl_sync(0xffffffffu, static_cast<int>(sm.odd[tile % kTReady]), 0);
+            in = in && mbar_wait(&sm.p_full[w], cnt[w] & 1, abort, err);
+            if (!__all_sync(0xffffffffu, in))
+                break;
+            ++cnt[w];
+            tc_fence_after();
+            if (!(flags & kEdge)) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    mma_ts(go, to, tp + (k < 4 ? 8 * k : 32 + 8 * k), vd + k * (2048 >> 4), kIdPV, k ? 1u : more);
+            } else if (!odd) {
+                const int groups = flags >> kGroups;
+#pragma unroll 1
+                for (int k = 0; k < groups; ++k)
+                    mma_ts(go, to, tp + (k < 4 ? 8 * k : 32 + 8 * k), vd + k * (2048 >> 4), kIdPV, k ? 1u : more);
+            }
+            commit_if(go, &sm.o_done[w]);
+            if (!two || w == 1)
+                commit_if(go, &sm.empty[st]);
+            if (n == N - 1)
+                commit_if(go, &sm.seg_done);
+        }
+        tile0 += nt;
+        tree_done(sm, it);
+    }
+    commit_if(go, &sm.drain);
+    volatile int no_abort = 0;
+    mbar_wait_warp(&sm.drain, 0, &no_abort, err);
+}
+
+// ------------------------------------------------------------ V's rows
+// An infinity or a NaN among two bf16 (f16) numbers.
+template <bool F16>
+__device__ __forceinline__ bool odd2(uint32_t w)
+{
+    constexpr uint32_t kLo = F16 ? 0x7c00u : 0x7f80u, kHi = kLo << 16;
+    return (w & kLo) == kLo || (w & kHi) == kHi;
 }
 
 template <class Smem>
-__device__ __forceinline__ void tree_fix(const TreeMaps &tm, const TreeArgs &a, Smem &sm, int warp, int lane)
+__device__ __forceinline__ void tree_fix(const TreeMaps &tm, const TreeArgs &a, Smem &sm, int lane)
 {
     constexpr int kStages = Smem::kStages;
     uint32_t *err = &a.hdr->error;
     uint32_t tile = 0, it = 0;
-    TreeSeg s;
-    for (; tree_take(a, sm, it, s); ++it) {
-        if (warp == kTFixWarp) {
-            // the queries
-            if (!mbar_wait_warp(&sm.q_empty, (it & 1) ^ 1, &sm.abort, err))
-                return;
-            if (lane == 0) {
-                const int tiles = sizeof(sm.q) > kTBytes && s.two ? 2 : 1;
-                mbar_arrive_expect_tx(&sm.q_full, static_cast<uint32_t>(tiles * a.g * a.tpt) * 256u);
-                for (int w = 0; w < tiles; ++w)
+    for (const TreeSeg *sp; (sp = tree_take(a, sm, it)) != nullptr; ++it) {
+        const TreeSeg &s = *sp;
+        // the queries
+        if (!mbar_wait_warp(&sm.q_empty, (it & 1) ^ 1, &sm.abort, err))
+            return;
+        if (lane == 0) {
+            const int tiles = sizeof(sm.q) > kTBytes && s.two ? 2 : 1;
+            mbar_arrive_expect_tx(&sm.q_full, static_cast<uint32_t>(tiles * a.g * a.tpt) * 256u);
+            for (int w = 0; w < tiles; ++w)
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-                        tma_load_4d(sm.q[w] + hf * kTHalf, &tm.q, 64 * hf, s.h * a.g, s.tok0 + w * a.tpt, s.b, &sm.q_full);
-            }
-            __syncwarp();
+                for (int hf = 0; hf < 2; ++hf)
+                    tma_load_4d(sm.q[w] + hf * kTHalf, &tm.q, 64 * hf, s.h * a.g, s.tok0 + w * a.tpt, s.b, &sm.q_full);
         }
+        __syncwarp();
         for (int t = s.t0; t < s.t1; ++t, ++tile) {
             const uint32_t e = 2 * tile;
             const int ks = e % kStages, vs = (e + 1) % kStages;
@@ -697,112 +723,169 @@ __device__ __forceinline__ void tree_fix(const TreeMaps &tm, const TreeArgs &a, 
                 const int from = (ti.flags & kMixed) ? 0 : nv * 16;
                 // 16 bytes of row i / 16: eight of each half (their order in a row does not matter)
 #pragma unroll 4
-                for (int i = from + (warp - kTFixWarp) * 32 + lane; i < (ti.flags >> kGroups) * 256; i += kTFixWarps * 32) {
+                for (int i = from + lane; i < (ti.flags >> kGroups) * 256; i += 32) {
                     uint4 *p = reinterpret_cast<uint4 *>(sm.ring[vs] + ((i >> 3) & 1) * kTHalf + (i >> 4) * 128 + (i & 7) * 16);
                     if ((i >> 4) >= nv) {
                         *p = make_uint4(0u, 0u, 0u, 0u);
                     } else {
                         const uint4 v = *p;
-                        odd |= odd_bf16x2(v.x) | odd_bf16x2(v.y) | odd_bf16x2(v.z) | odd_bf16x2(v.w);
+                        odd |= odd2<Smem::Q8>(v.x) | odd2<Smem::Q8>(v.y) | odd2<Smem::Q8>(v.z) | odd2<Smem::Q8>(v.w);
                     }
                 }
                 fence_proxy_async_smem();
             }
             odd = __any_sync(0xffffffffu, odd);
             if (lane == 0) {
-                sm.odd[tile % kTReady][warp - kTFixWarp] = odd;
+                sm.odd[tile % kTReady] = odd;
                 mbar_arrive(&sm.ready[tile % kTReady]);
                 mbar_arrive(&sm.empty[ks]);
                 mbar_arrive(&sm.empty[vs]);
             }
             __syncwarp();
         }
+        tree_done(sm, it);
     }
     // Before leaving on an abort, let the queries already issued land.
-    if (warp == kTFixWarp && it > 0 && __any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
+    if (it > 0 && __any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
         volatile int no_abort = 0;
         mbar_wait_warp(&sm.q_full, (it - 1) & 1, &no_abort, nullptr);
     }
 }
 
 // ------------------------------------------------------------ 8-bit caches
-// Four codes times their row's scale as bf16, exact: an e4m3 code has 4 bits, an int8 one 7.
-//   e4m3: a byte's exponent and fraction, moved to bf16's, are its value times 2^-120
-//   int8: c + 128 in the fraction of 2^23, less 2^23 + 128
+// A tile of codes becomes f16: a code times 2^(e - E + kTHead), e its block's exponent and E the
+// largest of the tile's, exact while a block's numbers are within 2^24 or so of the tile's largest
+// (smaller ones lose bits that the sums do not see).  The tile's numbers so stand for 2^(E - kTHead)
+// times them, one factor for all of it.  (As bf16, each block with its own scale, a code took four
+// integer operations, and the conversion was what bounded the kernel: 1170 us for 16 sequences of 64K.)
+//   e4m3: two codes a conversion, then a multiplication
+//   int8: c + 128 in the fraction of 1024, then (1024 + c + 128) f - 1152 f
 template <bool E4M3>
-struct Scale {
-    __nv_bfloat162 f;
-    bool two;
-    __device__ __forceinline__ explicit Scale(float s)
-    {
-        // 2^120 s, in two steps where bf16 does not hold it
-        two = s > 128.f;
-        f = __float2bfloat162_rn(two ? s : s * 0x1p120f);
-    }
-    __device__ __forceinline__ uint32_t pair(uint32_t t) const
-    {
-        uint32_t w = ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
-        __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&w);
-        if (two)
-            x = __hmul2(x, __float2bfloat162_rn(0x1p120f));
-        x = __hmul2(x, f);
-        return *reinterpret_cast<const uint32_t *>(&x);
-    }
-    __device__ __forceinline__ uint2 four(uint32_t w) const
-    {
-        return make_uint2(pair(__byte_perm(w, 0u, 0x1404)), pair(__byte_perm(w, 0u, 0x3424)));
-    }
-};
+constexpr int kTHead = E4M3 ? 6 : 5;
 
-template <>
-struct Scale<false> {
-    float f;
-    __device__ __forceinline__ explicit Scale(float s) : f(s) {}
-    __device__ __forceinline__ float one(uint32_t u, uint32_t sel) const
-    {
-        return (__uint_as_float(__byte_perm(u, 0x4b000000u, sel)) - 8388736.f) * f;
-    }
-    __device__ __forceinline__ uint2 four(uint32_t w) const
-    {
+template <bool E4M3>
+__device__ __forceinline__ uint2 codes_scaled(uint32_t w, __half2 f, __half2 g)
+{
+    __half2 x, y;
+    if constexpr (E4M3) {
+        uint32_t lo, hi;
+        codes_f16<true>(w, lo, hi);
+        x = __hmul2(*reinterpret_cast<const __half2 *>(&lo), f);
+        y = __hmul2(*reinterpret_cast<const __half2 *>(&hi), f);
+    } else {
         const uint32_t u = w ^ 0x80808080u;
-        return make_uint2(pack_bf16x2(one(u, 0x7440), one(u, 0x7441)), pack_bf16x2(one(u, 0x7442), one(u, 0x7443)));
+        const uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+        x = __hfma2(*reinterpret_cast<const __half2 *>(&lo), f, g);
+        y = __hfma2(*reinterpret_cast<const __half2 *>(&hi), f, g);
     }
-};
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+}
 
-// Warps that turn tiles of codes into the ring's bf16 ones, four for K and four for V, so that the
-// latencies of one (its codes, its scales, the fence) lie under the other's work.  A thread has 16
-// codes of eight rows, one of each 16-key group, so lane i holds the scale of group i.  They go to 32
-// bytes at column 32 (chunk % 4) of the row's half, in 16-byte pieces, swizzled as TMA would (the
-// two halves' lanes store their pieces in opposite order, so that they meet other banks).
+__device__ __forceinline__ float pow2f(int e)          // -126 .. 127
+{
+    return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// The largest finite magnitude among eight bf16 numbers and `m` (bits).
+__device__ __forceinline__ uint32_t max_finite(const uint4 &v, uint32_t m)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+        m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+    }
+    return m;
+}
+
+// Eight bf16 numbers times f as f16.
+__device__ __forceinline__ uint4 bf16_to_f16(const uint4 &v, float f)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * f, __uint_as_float(w[i] & 0xffff0000u) * f);
+        o[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Warps that turn tiles of codes into the ring's f16 ones, four for K and four for V, so that the
+// latencies of one (its codes, its scales, the fence) lie under the other's work.  A thread has 8
+// codes of either half of eight rows, one row of each 16-key group, so lane i holds the scale of group
+// i.  They become 16 bytes of the row in either half of the tile, swizzled as TMA would (odd rows'
+// lanes take the second half first: two rows' codes then lie in different banks).
 template <bool E4M3, class Smem>
 __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs &a, Smem &sm, int kv, int ct, int lane)
 {
     constexpr int kStages = Smem::kStages, kCodes = Smem::kCodes;
     static_assert(kStages % 2 == 0 && kCodes % 2 == 0, "a stage belongs to K or to V");
     uint32_t *err = &a.hdr->error;
-    uint32_t entry = kv, codes = kv, tile = 0;
-    const int chunk = ct & 7, r0 = ct >> 3, flip = chunk >> 2, c0 = (chunk & 3) * 2;
-    const uint32_t off0 = (chunk >> 2) * kTHalf + r0 * 128 + (((c0 + flip) ^ (r0 & 7)) << 4);
-    const uint32_t off1 = (chunk >> 2) * kTHalf + r0 * 128 + (((c0 + 1 - flip) ^ (r0 & 7)) << 4);
-    const float *scales = a.c.scale[kv];
-    TreeSeg s;
+    uint32_t entry = kv, codes = kv, tile = 0, own = 0;
+    const int piece = ct & 7, r0 = ct >> 3, flip = r0 & 1;
+    const uint32_t in0 = r0 * 128 + 64 * flip + 8 * piece, in1 = in0 ^ 64u;
+    const uint32_t at0 = flip * kTHalf + r0 * 128 + ((piece ^ (r0 & 7)) << 4), at1 = at0 ^ static_cast<uint32_t>(kTHalf);
+    // lanes 0 - 7 look up this warp's scales; K's warps look up V's too (8 - 15), for the tile's factors
+    const float *scales = a.c.scale[kv ^ (lane >> 3 & 1)];
     bool ok = true;
-    for (uint32_t it = 0; ok && tree_take(a, sm, it, s); ++it)
+    for (uint32_t it = 0; ok; ++it) {
+        const TreeSeg *sp = tree_take(a, sm, it);
+        if (!sp)
+            break;
+        const TreeSeg &s = *sp;
         for (int t = s.t0; t < s.t1; ++t, ++tile, entry += 2) {
             const int st = entry % kStages, cs = codes % kCodes;
+            uint8_t *dst = sm.ring[st];
             if (t == s.nt - 1) {
+                // the tree's own: from bf16, times one power of two that puts the largest below 2^15
                 if (!mbar_wait_warp(&sm.empty[st], ((entry / kStages) & 1) ^ 1, &sm.abort, err)) {
                     ok = false;
                     break;
                 }
-                if (ct == 0) {
-                    if (kv == 0)
-                        sm.tile[tile % kTInfos] = tree_own_tile(s.L, s.n);
-                    tree_load_draft(tm, sm.ring[st], kv, s, &sm.full[st]);
-                } else if (lane == 0) {
-                    mbar_arrive(&sm.full[st]);
+                if (ct == 0)
+                    tree_load_own(tm, dst, kv, s, &sm.own_full[kv]);
+                __syncwarp();
+                const bool got = mbar_wait_warp(&sm.own_full[kv], own & 1, &sm.abort, err);
+                const int rows = (s.n + 15) & ~15;
+                uint32_t mx = 0;
+                if (got && ct < s.n)
+                    for (int c = 0; c < 16; ++c)
+                        mx = max_finite(*reinterpret_cast<const uint4 *>(dst + (c >> 3) * kTHalf + ct * 128 + (((c & 7) ^ (ct & 7)) << 4)), mx);
+                mx = __reduce_max_sync(0xffffffffu, mx);
+                if (lane == 0) {
+                    sm.own_exp[own & 1][kv][ct / 32] = static_cast<uint8_t>(mx >> 7);
+                    mbar_arrive(&sm.own_max[kv]);
                 }
                 __syncwarp();
+                if (!got || !mbar_wait_warp(&sm.own_max[kv], own & 1, &sm.abort, err)) {
+                    ok = false;
+                    break;
+                }
+                int top = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top = max(top, static_cast<int>(sm.own_exp[own & 1][kv][i]));
+                const int e = min(14 + 127 - top, 120);
+                const float f = pow2f(e);
+                if (ct < rows)
+                    for (int c = 0; c < 16; ++c) {
+                        uint4 *p = reinterpret_cast<uint4 *>(dst + (c >> 3) * kTHalf + ct * 128 + (((c & 7) ^ (ct & 7)) << 4));
+                        *p = bf16_to_f16(*p, f);
+                    }
+                if (ct == 0) {
+                    if (kv == 0) {
+                        sm.tile[tile % kTInfos] = tree_own_tile(s.L, s.n);
+                        sm.k_unit[tile % kTInfos] = pow2f(-e);
+                    } else {
+                        sm.v_log[tile % kTInfos] = static_cast<float>(-e);
+                    }
+                }
+                ++own;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.full[st]);
                 continue;
             }
             if (!mbar_wait_warp(&sm.code_full[cs], (codes / kCodes) & 1, &sm.abort, err)) {
@@ -810,35 +893,57 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                 break;
             }
             const TreeTile &ti = sm.tile[tile % kTInfos];
-            float f = 0.f;
+            uint32_t f = 0x7fc00000u;                  // a group's scale; NaN as well where there is none
             {
-                const int hf = (lane >> 2) & 1, outer = ti.outer[hf], row = ti.row[hf] + 16 * (lane & 3);
-                if (lane < 8 && outer >= 0 && ti.key0 + 16 * lane < s.L)
-                    f = __ldg(scales + (static_cast<int64_t>(outer) * a.c.Hkv + s.h) * a.c.nsb + (row >> a.c.log2sb));
+                const int i = lane & 7, hf = i >> 2, outer = ti.outer[hf], row = ti.row[hf] + 16 * (i & 3);
+                if (lane < (kv ? 8 : 16) && outer >= 0 && ti.key0 + 16 * i < s.L)
+                    f = __ldg(reinterpret_cast<const uint32_t *>(scales) +
+                              (static_cast<int64_t>(outer) * a.c.Hkv + s.h) * a.c.nsb + (row >> a.c.log2sb));
             }
-            uint4 c[8];
+            uint2 c[8][2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                c[i] = *reinterpret_cast<const uint4 *>(sm.code[cs] + (16 * i + r0) * 128 + 16 * chunk);
+            for (int i = 0; i < 8; ++i) {
+                c[i][0] = *reinterpret_cast<const uint2 *>(sm.code[cs] + 2048 * i + in0);
+                c[i][1] = *reinterpret_cast<const uint2 *>(sm.code[cs] + 2048 * i + in1);
+            }
             const int groups = ti.flags >> kGroups;
+            const bool absent = ti.outer[lane >> 2 & 1] < 0;
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&sm.code_empty[cs]);
             codes += 2;
+            // the exponents, and the largest of them (0: no scale but NaN)
+            const uint32_t e = (f & 0x7fffffffu) < 0x7f800000u ? f >> 23 : 0u;
+            const uint32_t E = __reduce_max_sync(0xffffffffu, lane < 8 ? e : 0u);
+            if (kv == 0) {
+                const uint32_t EV = __reduce_max_sync(0xffffffffu, lane >= 8 && lane < 16 ? e : 0u);
+                if (ct == 0) {
+                    sm.k_unit[tile % kTInfos] = pow2f((E ? static_cast<int>(E) - 127 : 0) - kTHead<E4M3>);
+                    sm.v_log[tile % kTInfos] = static_cast<float>((EV ? static_cast<int>(EV) - 127 : 0) - kTHead<E4M3>);
+                }
+            }
+            // (a page outside the cache reads zeros, a block of a NaN scale NaN)
+            uint32_t fg;
+            {
+                const __half x = e ? __float2half_rn(pow2f(max(static_cast<int>(e) - static_cast<int>(E) + kTHead<E4M3>, -126)))
+                                   : absent ? __ushort_as_half(0) : __ushort_as_half(0x7e00);
+                fg = static_cast<uint32_t>(__half_as_ushort(x)) |
+                     static_cast<uint32_t>(__half_as_ushort(__hmul(x, __float2half_rn(-1152.f)))) << 16;
+            }
             if (!mbar_wait_warp(&sm.empty[st], ((entry / kStages) & 1) ^ 1, &sm.abort, err)) {
                 ok = false;
                 break;
             }
-            uint8_t *dst = sm.ring[st];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float fi = __shfl_sync(0xffffffffu, f, i);
+                const uint32_t w = __shfl_sync(0xffffffffu, fg, i);
                 if (i < groups) {
-                    const Scale<E4M3> sc(fi);
-                    const uint2 w0 = sc.four(c[i].x), w1 = sc.four(c[i].y), w2 = sc.four(c[i].z), w3 = sc.four(c[i].w);
-                    const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
-                    *reinterpret_cast<uint4 *>(dst + off0 + 2048 * i) = flip ? hi : lo;
-                    *reinterpret_cast<uint4 *>(dst + off1 + 2048 * i) = flip ? lo : hi;
+                    const __half2 x = *reinterpret_cast<const __half2 *>(&w);
+                    const __half2 fx = __low2half2(x), gx = __high2half2(x);
+                    const uint2 w0 = codes_scaled<E4M3>(c[i][0].x, fx, gx), w1 = codes_scaled<E4M3>(c[i][0].y, fx, gx);
+                    *reinterpret_cast<uint4 *>(dst + 2048 * i + at0) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                    const uint2 w2 = codes_scaled<E4M3>(c[i][1].x, fx, gx), w3 = codes_scaled<E4M3>(c[i][1].y, fx, gx);
+                    *reinterpret_cast<uint4 *>(dst + 2048 * i + at1) = make_uint4(w2.x, w2.y, w3.x, w3.y);
                 }
             }
             fence_proxy_async_smem();
@@ -846,11 +951,13 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
             if (lane == 0)
                 mbar_arrive(&sm.full[st]);
         }
+        if (ok)
+            tree_done(sm, it);
+    }
     // Before leaving on an abort, let the copies already issued land.
-    if (ct < 32 && __any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
+    if (ct < 32 && own > 0 && __any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
         volatile int no_abort = 0;
-        for (uint32_t n = entry > kStages + 1u ? entry - kStages : kv; n < entry; n += 2)
-            mbar_wait_warp(&sm.full[n % kStages], (n / kStages) & 1, &no_abort, nullptr);
+        mbar_wait_warp(&sm.own_full[kv], (own - 1) & 1, &no_abort, nullptr);
     }
 }
 
@@ -913,7 +1020,8 @@ __device__ __forceinline__ float max32(const uint32_t (&x)[32], float m)
     return fmaxf(a, b);
 }
 
-// p = 2^(c x + d) of 32 columns into TMEM as bf16; the sums of its even and odd ones grow.
+// p = 2^(c x + d) of 32 columns into TMEM as bf16 (f16); the sums of its even and odd ones grow.
+template <bool F16>
 __device__ __forceinline__ void exp32(const uint32_t (&x)[32], uint64_t c, uint64_t d, uint64_t &sum, uint32_t tp)
 {
     uint32_t p[16];
@@ -924,7 +1032,12 @@ __device__ __forceinline__ void exp32(const uint32_t (&x)[32], uint64_t c, uint6
         e0 = ex2(e0);
         e1 = ex2(e1);
         sum = f2_add(sum, f2_pack(e0, e1));
-        p[i] = pack_bf16x2(e0, e1);
+        if constexpr (F16) {
+            const __half2 h = __floats2half2_rn(e0, e1);
+            p[i] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            p[i] = pack_bf16x2(e0, e1);
+        }
     }
     tmem_st16(tp, p);
 }
@@ -942,11 +1055,11 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
     const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + 128 * wg, to = tmem + lane_base + kTColO;
-    const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2);
     auto place = [&](int c) { return ts + (c < 2 ? 16 * c : 32 + 16 * c); };
     uint32_t own = 0, tile0 = 0, joined = 0;
-    TreeSeg s;
-    for (uint32_t it = 0; tree_take(a, sm, it, s); ++it) {
+    const TreeSeg *sp;
+    for (uint32_t it = 0; (sp = tree_take(a, sm, it)) != nullptr; ++it) {
+        const TreeSeg &s = *sp;
         const bool two = TWO && s.two;
         const int mt = two ? wg : 0, tl = r / a.g, hh = r - tl * a.g;
         const int t = s.tok0 + mt * a.tpt + tl;
@@ -964,14 +1077,46 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                 d = d < 0 ? 0 : s.n - 1;
             }
         }
-        float m = NEG_INF, l = 0.f;
+        // 8-bit caches: the queries as f16, each row times a power of two that puts its largest below
+        // 2^11 (exact but for what is 2^-35 of it); `cs` undoes it.  With one M tile the first
+        // warpgroup does it and hands cs on.
+        float cs = a.scale_log2;
+        bool have = true;
+        if constexpr (Smem::Q8) {
+            if (!mbar_wait_warp(&sm.q_full, it & 1, &sm.abort, err))
+                return;
+            have = two || wg == 0;
+            if (have) {
+                if (it > 0 && !mbar_wait_warp(&sm.o_free, (it - 1) & 1, &sm.abort, err))
+                    return;                            // (the last range's maxima have been read)
+                if (active) {
+                    uint8_t *row = sm.q[mt] + r * 128;
+                    uint32_t mx = 0;
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c)
+                        mx = max_finite(*reinterpret_cast<const uint4 *>(row + (c >> 3) * kTHalf + (((c & 7) ^ (r & 7)) << 4)), mx);
+                    const int e = min(10 + 127 - static_cast<int>(mx >> 7), 120);
+#pragma unroll 4
+                    for (int c = 0; c < 16; ++c) {
+                        uint4 *p = reinterpret_cast<uint4 *>(row + (c >> 3) * kTHalf + (((c & 7) ^ (r & 7)) << 4));
+                        *p = bf16_to_f16(*p, pow2f(e));
+                    }
+                    cs = a.scale_log2 * pow2f(-e);
+                }
+                if (!two)
+                    sm.ml[0][r].x = cs;
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&sm.q_ready);
+        }
+        float m = NEG_INF, l = 0.f;                    // of the exponents' unit: log2
         int steps = 0;
         for (int tt = s.t0 + (two ? 0 : wg); tt < s.t1; tt += two ? 1 : 2, ++own, ++steps) {
             if (!mbar_wait_warp(&sm.s_full[wg], own & 1, &sm.abort, err))
                 return;
             if (active) {
-                if (own > 0 && !mbar_wait_warp(&sm.o_done[wg], (own - 1) & 1, &sm.abort, err))
-                    return;
                 tc_fence_after();
                 const uint32_t tile = tile0 + (tt - s.t0);
                 const int flags = sm.tile[tile % kTInfos].flags;
@@ -984,14 +1129,28 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                     if (flags & kMixed) {
                         if (!mbar_wait_warp(&sm.ready[tile % kTReady], (tile / kTReady) & 1, &sm.abort, err))
                             return;
-                        odd = (sm.odd[tile % kTReady][0] | sm.odd[tile % kTReady][1]) != 0;
+                        odd = sm.odd[tile % kTReady] != 0;
                     }
                 }
                 __syncwarp();
-                auto grow = [&](float mx) {
-                    const bool grew = mx > m + a.grow;
+                // p = 2^(unit x + dv - m): unit and dv hold what the tile's numbers of K and V stand for
+                float unit = a.scale_log2, dv = 0.f, iv = 1.f;
+                if constexpr (Smem::Q8) {
+                    if (!have)
+                        cs = sm.ml[0][r].x;
+                    have = true;
+                    unit = fmaxf(cs * sm.k_unit[tile % kTInfos], 1e-37f);
+                    dv = sm.v_log[tile % kTInfos];
+                    iv = pow2f(-static_cast<int>(dv));
+                    dv += kTShift;
+                }
+                const uint64_t c2 = f2_pack(unit, unit);
+                // (O's product of this warpgroup's step before is over: its S is issued behind that.)
+                auto grow = [&](float x) {
+                    const float mx = x == NEG_INF ? NEG_INF : fmaf(x, unit, Smem::Q8 ? dv - kTShift : 0.f);
+                    const bool grew = mx > m + kTGrow;
                     if (__any_sync(0xffffffffu, grew)) {
-                        const float f = grew && m != NEG_INF ? ex2((m - mx) * a.scale_log2) : 1.f;
+                        const float f = grew && m != NEG_INF ? ex2(m - mx) : 1.f;
                         m = grew ? mx : m;
                         l *= f;
                         if (steps > 0) {
@@ -1035,12 +1194,12 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         mx = max32(x[c], mx);
                     }
                     grow(mx);
-                    const float mb = m == NEG_INF ? 0.f : m * a.scale_log2;
-                    const uint64_t d2 = f2_pack(-mb, -mb);
+                    const float db = dv - (m == NEG_INF ? 0.f : m);
+                    const uint64_t d2 = f2_pack(db, db);
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
                     for (int c = 0; c < kHeld; ++c)
-                        exp32(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c + 4 - kHeld));
+                        exp32<Smem::Q8>(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c + 4 - kHeld));
                     if constexpr (kHeld == 2) {
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
@@ -1049,12 +1208,12 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             tie32(x[c]);
-                            exp32(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c));
+                            exp32<Smem::Q8>(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c));
                         }
                     }
                     float u, v;
                     f2_unpack(f2_add(sum0, sum1), u, v);
-                    l += u + v;
+                    l = fmaf(u + v, iv, l);
                 } else if (!odd) {
                     // 32 columns at a time, those that hold keys (P lies behind what is still to be read)
                     float mx = NEG_INF;
@@ -1068,8 +1227,8 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         mx = max32(x, mx);
                     }
                     grow(mx);
-                    const float mb = m == NEG_INF ? 0.f : m * a.scale_log2;
-                    const uint64_t d2 = f2_pack(-mb, -mb);
+                    const float db = dv - (m == NEG_INF ? 0.f : m);
+                    const uint64_t d2 = f2_pack(db, db);
                     uint64_t sum = 0;
 #pragma unroll 1
                     for (int c = 0; c < chunks; ++c) {
@@ -1078,11 +1237,11 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         tmem_wait_ld();
                         tie32(x);
                         mask32(x, c == 0 ? keep[0] : c == 1 ? keep[1] : c == 2 ? keep[2] : keep[3]);
-                        exp32(x, c2, d2, sum, place(c));
+                        exp32<Smem::Q8>(x, c2, d2, sum, place(c));
                     }
                     float u, v;
                     f2_unpack(sum, u, v);
-                    l += u + v;
+                    l = fmaf(u + v, iv, l);
                 } else {
                     // V holds infinities or NaN in a tile that rows keep differently: the kept keys
                     // one by one, so that none reaches a row that does not keep it (the first ones of
@@ -1100,13 +1259,13 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         mx = (kw >> (k & 31)) & 1u ? fmaxf(mx, __uint_as_float(sk)) : mx;
                     }
                     grow(mx);
-                    const float mb = m == NEG_INF ? 0.f : m * a.scale_log2;
+                    const float db = dv - (m == NEG_INF ? 0.f : m);
 #pragma unroll 1
-                    for (int c = 0; c < 8; ++c) {                 // 16 dims at a time
+                    for (int dc = 0; dc < 8; ++dc) {              // 16 dims at a time
                         uint32_t raw[16];
                         float o[16];
                         if (steps > 0) {
-                            tmem_ld16(to + 128 * wg + 16 * c, raw);
+                            tmem_ld16(to + 128 * wg + 16 * dc, raw);
                             tmem_wait_ld();
                         }
 #pragma unroll
@@ -1122,17 +1281,20 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                             asm volatile("" : "+r"(sk));
                             const uint32_t kw = k < 32 ? keep[0] : k < 64 ? keep[1] : k < 96 ? keep[2] : keep[3];
                             if ((kw >> (k & 31)) & 1u) {
-                                const float p = ex2(fmaf(__uint_as_float(sk), a.scale_log2, -mb));
-                                sum += c == 0 ? p : 0.f;
+                                const float p = ex2(fmaf(__uint_as_float(sk), unit, db));
+                                sum += dc == 0 ? p : 0.f;
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
                                     const uint4 v = *reinterpret_cast<const uint4 *>(
-                                        v0 + (c >> 2) * kTHalf + k * 128 + ((((c & 3) * 2 + j) ^ (k & 7)) << 4));
+                                        v0 + (dc >> 2) * kTHalf + k * 128 + ((((dc & 3) * 2 + j) ^ (k & 7)) << 4));
                                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                                     for (int q = 0; q < 4; ++q) {
-                                        o[8 * j + 2 * q] = fmaf(p, __uint_as_float(w[q] << 16), o[8 * j + 2 * q]);
-                                        o[8 * j + 2 * q + 1] = fmaf(p, __uint_as_float(w[q] & 0xffff0000u), o[8 * j + 2 * q + 1]);
+                                        const float2 x = Smem::Q8 ? f16_f32(w[q])
+                                                                  : make_float2(__uint_as_float(w[q] << 16),
+                                                                                __uint_as_float(w[q] & 0xffff0000u));
+                                        o[8 * j + 2 * q] = fmaf(p, x.x, o[8 * j + 2 * q]);
+                                        o[8 * j + 2 * q + 1] = fmaf(p, x.y, o[8 * j + 2 * q + 1]);
                                     }
                                 }
                             }
@@ -1141,9 +1303,9 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             raw[i] = __float_as_uint(o[i]);
-                        tmem_st16(to + 128 * wg + 16 * c, raw);
+                        tmem_st16(to + 128 * wg + 16 * dc, raw);
                     }
-                    l += sum;
+                    l = fmaf(sum, iv, l);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1160,7 +1322,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
         tc_fence_after();
         float f0 = 1.f, f1 = 0.f;
         bool both = false;
-        float M = m == NEG_INF ? NEG_INF : m * a.scale_log2;
+        float M = m;
         if (!two) {
             sm.ml[wg][r] = make_float2(M, l);
             __syncwarp();
@@ -1230,7 +1392,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                 }
             }
             if (valid && (two || wg == 0)) {
-                const float l2 = none ? NEG_INF : (M == NEG_INF ? 0.f : M) + tree_lg2(l);
+                const float l2 = none ? NEG_INF : (M == NEG_INF ? 0.f : M) - (Smem::Q8 ? kTShift : 0.f) + tree_lg2(l);
                 if (!whole) {
                     if (in_bounds(prow, 2 * static_cast<int64_t>(gridDim.x) * a.rows_slot, err))
                         a.part_lse[prow] = l2;
@@ -1243,6 +1405,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&sm.o_free);
+        tree_done(sm, it);
     }
 }
 
@@ -1262,17 +1425,17 @@ __global__ void __launch_bounds__(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8
         return;
     }
     if (warp == 0) {
-        constexpr int users = 1 + 8 + kTFixWarps + (kQ8 ? kTConvWarps : 0);
+        constexpr int users = 8 + 3 + (kQ8 ? kTConvWarps : 0);
         if (lane < Smem::kStages) {
             mbar_init(&sm.full[lane], kQ8 ? kTConvWarps / 2 : 1);
-            mbar_init(&sm.empty[lane], 1 + kTFixWarps);
+            mbar_init(&sm.empty[lane], 2);
         }
         if (lane < Smem::kCodes) {
             mbar_init(&sm.code_full[lane], 1);
             mbar_init(&sm.code_empty[lane], kTConvWarps / 2);
         }
         if (lane < kTReady)
-            mbar_init(&sm.ready[lane], kTFixWarps);
+            mbar_init(&sm.ready[lane], 1);
         if (lane < kTSegs) {
             mbar_init(&sm.seg_full[lane], 1);
             mbar_init(&sm.seg_empty[lane], users);
@@ -1288,13 +1451,18 @@ __global__ void __launch_bounds__(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8
             mbar_init(&sm.seg_done, 1);
             mbar_init(&sm.ml_full, 8);
             mbar_init(&sm.o_free, 8);
-            mbar_init(&sm.drain, 1);
+            mbar_init(&sm.drain, 2);
+            mbar_init(&sm.q_ready, 8);
+            for (int k = 0; k < 2; ++k) {
+                mbar_init(&sm.own_full[k], 1);
+                mbar_init(&sm.own_max[k], 4);
+            }
             sm.abort = 0;
         }
         fence_barrier_init();
         fence_proxy_async_smem();
     }
-    if (warp == kTMmaWarp) {
+    if (warp == kTQkWarp) {
         tmem_alloc(&sm.tmem_base, 512);
         tmem_relinquish();
     }
@@ -1313,10 +1481,10 @@ __global__ void __launch_bounds__(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8
     const uint32_t tmem = sm.tmem_base;
 
     // Registers go to the softmax: 256 x 208 + 128 x 88 of the launch's 384 x 168, or, with
-    // converting warps, 256 x 144 + 128 x 72 + 256 x 56 of its 640 x 96.
+    // converting warps, 256 x 128 + 128 x 72 + 256 x 72 of its 640 x 96.
     if (warp < 8) {
         if constexpr (kQ8)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         tree_softmax(a, sm, tmem, warp, lane);
@@ -1327,14 +1495,16 @@ __global__ void __launch_bounds__(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8
             asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == kTProducerWarp) {
             tree_producer(tm, a, sm, lane);
-        } else if (warp == kTMmaWarp) {
-            tree_mma(a, sm, tmem, lane);
+        } else if (warp == kTQkWarp) {
+            tree_qk(a, sm, tmem);
+        } else if (warp == kTPvWarp) {
+            tree_pv(a, sm, tmem);
         } else {
-            tree_fix(tm, a, sm, warp, lane);
+            tree_fix(tm, a, sm, lane);
         }
     } else {
         if constexpr (kQ8) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
             tree_convert<FMT == EA_CACHE_E4M3>(tm, a, sm, (warp - kTConvWarp) / 4, threadIdx.x % 128, lane);
         }
     }
@@ -1342,7 +1512,7 @@ __global__ void __launch_bounds__(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == kTMmaWarp) {
+    if (warp == kTQkWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -1633,7 +1803,6 @@ extern "C" ea_status ea_hybrid_attn_tree(const void *Q, const void *K, const voi
     a.sink = sink < (1 << 30) ? sink : 0x7fffffff;
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.grow = kTGrow / a.scale_log2;
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int dev = 0;

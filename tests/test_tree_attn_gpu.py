@@ -8,9 +8,9 @@ import pytest
 import torch
 
 import sparse_head_attention_gb300 as ea
-from cache_reference import capacity, logical, make_cache, rows_of, tokens
+from cache_reference import capacity, logical, make_cache, rows_of, tokens, value_scales
 from gpu_helpers import check_no_device_error, gpu_device
-from tree_reference import accept, attend, inv_freq, plan, random_tree, rotate
+from tree_reference import accept, attend, inv_freq, plan, random_tree, rotate, units
 
 pytestmark = pytest.mark.gpu
 E4M3, INT8, BF16 = torch.float8_e4m3fn, torch.int8, torch.bfloat16
@@ -77,7 +77,8 @@ def check(dev, c, Hq, Hkv, T, lens, n, modes, sink=16, window=100, kind="tree", 
     p = random_tree(B, T, seed, kind)
     depth, mask = plan(p, n)
     Kc, Vc = logical(c)
-    ref = attend(*(x.double().numpy() for x in (Q, K, V)), Kc, Vc, lens, n, depth, mask, modes, sink, window, scale or SCALE, bm)
+    ref = attend(*(x.double().numpy() for x in (Q, K, V)), Kc, Vc, lens, n, depth, mask, modes, sink, window, scale or SCALE, bm,
+                 None if c["ks"] is None else units(value_scales(c), lens))
     spoil(c, lens)
     for b in range(B):
         K[b, n[b] :], V[b, n[b] :] = math.nan, math.inf
@@ -177,7 +178,8 @@ def test_non_finite_in_masked_places(dev):
         if dtype == BF16:
             c["V"][0, first, 0, 77] = -math.inf
         ref = attend(*(np.nan_to_num(x.double().numpy(), nan=0.0, posinf=0.0) for x in (Q, K, V)),
-                     *(np.nan_to_num(x, neginf=0.0) for x in logical(c)), lens, n, depth, mask, modes, sink, window, SCALE)
+                     *(np.nan_to_num(x, neginf=0.0) for x in logical(c)), lens, n, depth, mask, modes, sink, window, SCALE,
+                     vunit=None if dtype == BF16 else units(value_scales(c), lens))
         h = handle(c, dev)
         ws = ea.tree_workspace(B, T, Hq, 1, 512, device=dev)
         O, LSE = out(B, T, Hq, dev)

@@ -97,13 +97,27 @@ def random_tree(B, T, seed, kind="tree"):
     return p
 
 
-def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, scale, bm=None):
+def units(scales, lens):
+    """What the f16 numbers of a key's tile of an 8-bit cache stand for: the largest scale of the 128 aligned rows (below the
+    sequence's length), over 2^6 (e4m3) or 2^5 (int8; 2^6 here, the smaller).  scales float64 [B, cap, Hkv]."""
+    u = np.ones_like(scales)
+    for b, L in enumerate(lens):
+        for j in range(0, L, 128):
+            u[b, j : j + 128] = scales[b, j : min(j + 128, L)].max(0) / 64
+    return u
+
+
+def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, scale, bm=None, vunit=None):
     """ea_hybrid_attn_tree in 64 bits.  Q [B, T, Hq, 128], K, V [B, T, Hkv, 128], Kc, Vc [B, cap, Hkv, 128] float64.
     Returns O [B, T, Hq, 128], LSE [B, Hq, T] and how far an fp32 kernel with bf16 probabilities may be off:
       a product q . k sums 128 fp32 terms: 2^-17 of sum |q k|, times scale: a logit's error; its exponent is one fused
       multiply-add of up to 2^6 (2^-18 relative to p) and the exponential 2^-22;
       a probability is rounded to bf16 (2^-8), the output too; sums over keys are fp32 in tiles of 128 (2^-17) that are
-      joined by weights of 2^-20."""
+      joined by weights of 2^-20.
+    8-bit caches (vunit: units() of V's scales): probabilities are f16 instead, w_j = p_j u_j in units of 2^-7 of the largest
+    weight M; one that is below 2^-14 is subnormal, off by 2^-25.  The sum of w / u is 2^7 / max u at least, and the f16
+    numbers of V are v_j / u_j, so that adds at most 2^-32 max(u) sum |v_j| / u_j to an output.  The tree's own values are f16
+    too, times a power of two that puts the largest in [2^14, 2^15), so off by 2^-39 of it at most where subnormal."""
     B, T, Hq, D = Q.shape
     Hkv = K.shape[2]
     g = Hq // Hkv
@@ -117,6 +131,9 @@ def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, scale, bm
         for h in range(Hkv):
             k = np.concatenate([Kc[b, :L, h], K[b, :nb, h]])
             v = np.concatenate([Vc[b, :L, h], V[b, :nb, h]])
+            if vunit is not None and nb:
+                own = 2.0 ** (np.floor(np.log2(max(np.abs(V[b, :nb, h]).max(), 2.0 ** -126))) - 14)
+                u = np.concatenate([vunit[b, :L, h], np.full(nb, own)])
             keep = np.concatenate([np.ones((nb, L), bool), up], 1)
             if modes[b][h] == SSA:
                 keep &= (at[None] < sink) | (pos[:, None] - at[None] < window)
@@ -137,5 +154,7 @@ def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, scale, bm
                 O[b, t, hs] = p @ v[j]
                 LSE[b, hs, t] = (top + np.log(s))[:, 0]
                 tO[b, t, hs] = (p @ np.abs(v[j])) * (2.0 ** -8 + 2 * e[:, None]) + np.abs(O[b, t, hs]) * 2.0 ** -8
+                if vunit is not None:
+                    tO[b, t, hs] += 2.0 ** -32 * u[j].max() * (np.abs(v[j]) / u[j][:, None]).sum(0) + 2.0 ** -39 * np.abs(V[b, :nb, h]).max()
                 tL[b, hs, t] = e + np.abs(LSE[b, hs, t]) * 2.0 ** -20
     return O, LSE, tO, tL
