@@ -54,6 +54,7 @@ constexpr uint32_t kTIdescBf16 = 1u << 7 | 1u << 10;  // the operands' type: bf1
 constexpr float kTGrow = 8.f;                         // the maximum is followed once it grew by 2^8: p <= 2^8
 constexpr float kTShift = 7.f;                        // 8-bit caches: p is f16, at most 2^(7 + 8)
 constexpr int kTMinTiles = 2;                         // of a range at least (a power of two)
+constexpr int kTPartTiles = 4;                        // see tree_range
 constexpr int kTSms = 152;                            // a workspace's size depends on the grid
 
 enum { kEdge = 1, kDraft = 2, kRow0 = 4, kRow1 = 8, kMixed = 16, kGroups = 8 };   // (from bit 8 on: 16-key groups)
@@ -72,12 +73,21 @@ struct TreeArgs {
     ea_ws_header *hdr;
     CacheDev c;
     int B, T, Hq, Hkv, g, tpt, pairs, nBm, sink, window, box128, rows_slot;
+    int page_log2;                       // of a page size that is a power of two, else -1
+    float inv_Hkv, inv_g, inv_tpt;       // for quot()
     float scale_log2;
 };
 
 struct TreeMaps {
     CUtensorMap q, kd, vd, k, v;
 };
+
+// x / d for 0 <= x < 2^24, inv = 1 / d (a division takes the start of a CTA ten times as long).
+__device__ __forceinline__ int quot(int x, int d, float inv)
+{
+    const int q = __float2int_rz(static_cast<float>(x) * inv), r = x - q * d;
+    return q + (r >= d ? 1 : 0) - (r < 0 ? 1 : 0);
+}
 
 // One (sequence, KV head).
 struct TreeUnit {
@@ -90,10 +100,10 @@ struct TreeUnit {
 __device__ __forceinline__ TreeUnit tree_unit(const TreeArgs &a, int u)
 {
     TreeUnit x;
-    const int b = u / a.Hkv;
-    x.n = a.n_nodes ? a.n_nodes[b] : a.T;
-    x.L = a.seqlens[b];
-    x.mode = a.m[u];
+    const int b = quot(u, a.Hkv, a.inv_Hkv);
+    x.n = a.n_nodes ? __ldg(a.n_nodes + b) : a.T;
+    x.L = __ldg(a.seqlens + b);
+    x.mode = __ldg(a.m + u);
     x.bad = x.dead = false;
     if (x.n < 0 || x.n > a.T) {
         x.bad = true;
@@ -122,7 +132,7 @@ __device__ __forceinline__ TreeUnit tree_unit(const TreeArgs &a, int u)
         x.need = (x.L + x.n - 1) / EA_TILE > x.L / EA_TILE ? kRow0 | kRow1 : kRow0;
     }
     x.nt = tiles + 1;
-    x.pairs = x.n <= 0 ? 0 : a.pairs == 1 ? 1 : ((x.n + a.tpt - 1) / a.tpt + 1) / 2;
+    x.pairs = x.n <= 0 ? 0 : a.pairs == 1 ? 1 : (quot(x.n + a.tpt - 1, a.tpt, a.inv_tpt) + 1) / 2;
     return x;
 }
 
@@ -303,9 +313,11 @@ __device__ __forceinline__ void tree_done(Smem &sm, uint32_t it)
 }
 
 // ------------------------------------------------------------ ranges
-// This CTA's range of the line of tiles: an equal share of its W tiles among G CTAs (fewer than
-// the grid where a share would be shorter than min_tiles).  Found by one warp where there are few
-// units, so that the others' set-up runs beside it; by all of them (ahead of their roles) else.
+// This CTA's range: an equal share of the line of tiles among G CTAs (fewer than the grid where a share
+// would be shorter than kTMinTiles).  A unit's queries, its own keys and its results cost about as much
+// as kTPartTiles of its tiles, which lie ahead of them in the line (eight int8 sequences, of 30000 keys
+// and of none: 101 -> 55 us).  Found by one warp where there are few units, so that the others'
+// set-up runs beside it; by all of them (ahead of their roles) else.
 constexpr int kTWarpUnits = 256;
 
 template <class Smem>
@@ -319,7 +331,7 @@ __device__ __forceinline__ void tree_range(const TreeArgs &a, Smem &sm, int tid,
     TreeUnit x{};
     for (int u = lo; u < hi; ++u) {
         x = tree_unit(a, u);
-        mine += x.nt * x.pairs;
+        mine += (x.nt + kTPartTiles) * x.pairs;
         bad |= x.bad;
     }
     if (bad && blockIdx.x == 0)
@@ -355,7 +367,7 @@ __device__ __forceinline__ void tree_range(const TreeArgs &a, Smem &sm, int tid,
         for (int u = lo; u < hi; ++u) {
             if (per > 1)
                 x = tree_unit(a, u);
-            const int w = x.nt * x.pairs;
+            const int w = (x.nt + kTPartTiles) * x.pairs;
             if (start < base + w) {
                 sm.unit = x;
                 sm.u = u;
@@ -374,7 +386,7 @@ __device__ __forceinline__ void tree_place(const TreeArgs &a, int b, int L, int 
     outer = b;
     row = key < L ? key : -1;
     if (row >= 0 && a.c.table) {
-        const int pg = key / a.c.rows;
+        const int pg = a.page_log2 >= 0 ? key >> a.page_log2 : key / a.c.rows;
         row = key - pg * a.c.rows;
         outer = a.c.table[b * a.c.bt_stride + pg];
         if (outer < 0 || outer >= a.c.outer) {         // reported; reads zeros
@@ -399,10 +411,6 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
     constexpr bool Q8 = Smem::Q8;
     constexpr int kStages = Smem::kStages, kCodes = Smem::kCodes;
     uint32_t *err = &a.hdr->error;
-    if (a.B * a.Hkv <= kTWarpUnits) {
-        tree_range(a, sm, lane, 1);
-        __syncwarp();
-    }
     int u = sm.u, off = sm.off, left = sm.count;
     TreeUnit &x = sm.unit;               // the unit at hand
     uint32_t it = 0, entry = 0, codes = 0, tile = 0;
@@ -419,7 +427,8 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
         return true;
     };
     while (ok && left > 0) {
-        if (off >= x.nt * x.pairs) {
+        const int len = x.nt + kTPartTiles;
+        if (off >= len * x.pairs) {
             const TreeUnit next = tree_unit(a, ++u);
             __syncwarp();
             if (lane == 0)
@@ -429,9 +438,14 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
             continue;
         }
         TreeSeg s;
-        const int pair = x.pairs == 1 ? 0 : off / x.nt;
+        // the rest of one pair of M tiles, as far as the range goes
+        const int pair = x.pairs == 1 ? 0 : off / len, from = off - pair * len, to = left < len - from ? from + left : len;
+        off += to - from;
+        left -= to - from;
+        if (to <= kTPartTiles)
+            continue;
         s.valid = 1;
-        s.b = u / a.Hkv;
+        s.b = quot(u, a.Hkv, a.inv_Hkv);
         s.h = u - s.b * a.Hkv;
         s.v = u * a.pairs + pair;
         s.mode = x.mode;
@@ -440,13 +454,11 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
         s.dead = x.dead;
         s.tok0 = 2 * pair * a.tpt;
         s.two = s.tok0 + a.tpt < x.n;
-        s.t0 = off - pair * x.nt;
-        s.t1 = left < x.nt - s.t0 ? s.t0 + left : x.nt;
+        s.t0 = max(from - kTPartTiles, 0);
+        s.t1 = to - kTPartTiles;
         s.nt = x.nt;
         // a range holds one part that continues a unit (its first) and one that is continued at most
         s.slot = 2 * blockIdx.x + (s.t0 == 0 ? 1 : 0);
-        off += s.t1 - s.t0;
-        left -= s.t1 - s.t0;
         if (!publish(s))
             break;
         if (lane == 0) {
@@ -786,14 +798,17 @@ __device__ __forceinline__ float pow2f(int e)          // -126 .. 127
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// The largest finite magnitude among eight bf16 numbers and `m` (bits).
+// The largest finite magnitude among eight bf16 numbers and `m` (two 16-bit halves of bits).
 __device__ __forceinline__ uint32_t max_finite(const uint4 &v, uint32_t m)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
+    const uint32_t all = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+    if ((all & 0xffffu) < 0x7f80u && all < 0x7f800000u)
+        return __vmaxu2(m, all);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-        m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        const uint32_t lo = w[i] & 0xffffu, hi = w[i] & 0xffff0000u;
+        m = __vmaxu2(m, (lo < 0x7f80u ? lo : 0u) | (hi < 0x7f800000u ? hi : 0u));
     }
     return m;
 }
@@ -852,7 +867,7 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                 if (got && ct < s.n)
                     for (int c = 0; c < 16; ++c)
                         mx = max_finite(*reinterpret_cast<const uint4 *>(dst + (c >> 3) * kTHalf + ct * 128 + (((c & 7) ^ (ct & 7)) << 4)), mx);
-                mx = __reduce_max_sync(0xffffffffu, mx);
+                mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
                 if (lane == 0) {
                     sm.own_exp[own & 1][kv][ct / 32] = static_cast<uint8_t>(mx >> 7);
                     mbar_arrive(&sm.own_max[kv]);
@@ -1061,7 +1076,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
     for (uint32_t it = 0; (sp = tree_take(a, sm, it)) != nullptr; ++it) {
         const TreeSeg &s = *sp;
         const bool two = TWO && s.two;
-        const int mt = two ? wg : 0, tl = r / a.g, hh = r - tl * a.g;
+        const int mt = two ? wg : 0, tl = quot(r, a.g, a.inv_g), hh = r - tl * a.g;
         const int t = s.tok0 + mt * a.tpt + tl;
         const bool valid = tl < a.tpt && t < s.n;
         const bool active = __any_sync(0xffffffffu, valid);
@@ -1095,11 +1110,12 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
 #pragma unroll 4
                     for (int c = 0; c < 16; ++c)
                         mx = max_finite(*reinterpret_cast<const uint4 *>(row + (c >> 3) * kTHalf + (((c & 7) ^ (r & 7)) << 4)), mx);
-                    const int e = min(10 + 127 - static_cast<int>(mx >> 7), 120);
+                    const int e = min(10 + 127 - static_cast<int>(max(mx & 0xffffu, mx >> 16) >> 7), 120);
+                    const float f = pow2f(e);
 #pragma unroll 4
                     for (int c = 0; c < 16; ++c) {
                         uint4 *p = reinterpret_cast<uint4 *>(row + (c >> 3) * kTHalf + (((c & 7) ^ (r & 7)) << 4));
-                        *p = bf16_to_f16(*p, pow2f(e));
+                        *p = bf16_to_f16(*p, f);
                     }
                     cs = a.scale_log2 * pow2f(-e);
                 }
@@ -1475,6 +1491,8 @@ __global__ void __launch_bounds__(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8
     griddep_launch_dependents();
     if (a.B * a.Hkv > kTWarpUnits)
         tree_range(a, sm, threadIdx.x, blockDim.x / 32);
+    else if (warp == kTProducerWarp)
+        tree_range(a, sm, lane, 1);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1669,7 +1687,7 @@ static bool tree_sizes_ok(int B, int T, int Hq, int Hkv, int d)
 // The tiles of a step at most, which the kernel counts in 32 bits.
 static bool tree_tiles_ok(int B, int Hkv, int pairs, int Lmax)
 {
-    return static_cast<double>(B) * Hkv * pairs * (ceil_div(Lmax, kTTile) + 1) < 2147483648.;
+    return static_cast<double>(B) * Hkv * pairs * (ceil_div(Lmax, kTTile) + 1 + kTPartTiles) < 2147483648.;
 }
 
 static bool tree_tensor(const void *p, const int64_t *str)
@@ -1803,6 +1821,13 @@ extern "C" ea_status ea_hybrid_attn_tree(const void *Q, const void *K, const voi
     a.sink = sink < (1 << 30) ? sink : 0x7fffffff;
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
+    a.inv_Hkv = 1.f / static_cast<float>(Hkv);
+    a.inv_g = 1.f / static_cast<float>(a.g);
+    a.inv_tpt = 1.f / static_cast<float>(a.tpt);
+    a.page_log2 = -1;
+    for (int k = 6; k < 31; ++k)
+        if (a.c.rows == 1 << k)
+            a.page_log2 = k;
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     int dev = 0;
