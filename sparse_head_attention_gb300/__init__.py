@@ -27,6 +27,7 @@ present, the device entry points raise instead of computing anything else.
     ea_check_errors          read back the device error word of a workspace
 """
 import ctypes
+import functools
 import math
 import os
 
@@ -1017,19 +1018,48 @@ def ea_cache_compact(src, dst, index, counts, *, weights=None, weights_out=None,
             _ptr(weights_out), workspace.data_ptr(), workspace.numel(), st))
 
 
-def _rows4(t, name, shape):
-    _dev(t, name, torch.bfloat16)
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must be a %s tensor, got %s" % (name, list(shape), list(t.shape)))
-    return t
+_BF16, _I32 = torch.bfloat16, torch.int32
 
 
-def _i32_rows(t, name, B, T):
-    return t if t is None else _like(t, name, (B, T), torch.int32)
+def _fit(t, name, dtype, shape, dev):
+    """t is a contiguous CUDA tensor of this kind on device `dev`, or None (these calls
+    are short: their checks are made in one place, and told apart when one fails)."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+        return
+    _like(t, name, shape, dtype)
+    raise ValueError("tensors on several devices: %s on %s" % (name, t.device))
 
 
-def _strides4(t):
-    return None if t is None else _I64[4](*t.stride())
+def _fit4(t, name, shape, dev):
+    """The same for bfloat16 tensors of any strides; returns their strides."""
+    if not (t.dtype is _BF16 and t.shape == shape and t.get_device() == dev):
+        _dev(t, name, _BF16)
+        if tuple(t.shape) != shape:
+            raise ValueError("%s must be a %s tensor, got %s" % (name, list(shape), list(t.shape)))
+        raise ValueError("tensors on several devices: %s on %s" % (name, t.device))
+    return _strides4(t.stride())
+
+
+@functools.lru_cache(maxsize=256)
+def _strides4(strides):
+    return _I64[4](*strides)
+
+
+def _shape4(t, name):
+    _dev(t, name, _BF16)
+    if t.dim() != 4 or t.shape[3] != 128:
+        raise ValueError("%s must be [B, T, heads, 128]" % name)
+    return t.shape
+
+
+def _needed(t, name):
+    if t is None:
+        raise ValueError("%s is needed" % name)
+
+
+def _workspace_fits(workspace, dev):
+    if workspace is not None and workspace.get_device() != dev:
+        raise ValueError("tensors on several devices: workspace on %s" % workspace.device)
 
 
 MAX_TREE = 128
@@ -1046,41 +1076,45 @@ def ea_rope(Q, K, positions, inv_freq, *, n_new=None, interleaved=False, rope_sc
     if Q is None and K is None:
         raise ValueError("Q or K is needed")
     x = Q if Q is not None else K
-    _dev(x, "Q" if Q is not None else "K", torch.bfloat16)
-    if x.dim() != 4 or x.shape[3] != 128:
-        raise ValueError("Q and K must be [B, T, heads, 128]")
-    B, T = x.shape[:2]
-    if positions is None:
-        raise ValueError("positions is needed")
-    _i32_rows(positions, "positions", B, T)
-    rot = 2 * _like(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32).numel()
-    _i32_vec(n_new, "n_new", B)
-    heads = [0, 0]
-    for k, (t, o, nm) in enumerate(((Q, Q_out, "Q"), (K, K_out, "K"))):
-        if t is None:
-            if o is not None:
-                raise ValueError("%s_out without %s" % (nm, nm))
-            continue
-        if t.dim() != 4:
-            raise ValueError("%s must be [B, T, heads, 128]" % nm)
-        heads[k] = t.shape[2]
-        _rows4(t, nm, (B, T, heads[k], 128))
-        if o is not None:
-            _rows4(o, nm + "_out", (B, T, heads[k], 128))
-    _one_device(x, Q, K, positions, inv_freq, n_new, Q_out, K_out, workspace)
+    B, T = _shape4(x, "Q" if Q is not None else "K")[:2]
+    dev = x.get_device()
+    _needed(positions, "positions")
+    _needed(inv_freq, "inv_freq")
+    _fit(positions, "positions", _I32, (B, T), dev)
+    half = inv_freq.numel()
+    _fit(inv_freq, "inv_freq", torch.float32, (half,), dev)
+    _fit(n_new, "n_new", _I32, (B,), dev)
+    _workspace_fits(workspace, dev)
+    Hq = Hkv = 0
+    qs = qos = ks = kos = None
     with _at(x.device, stream) as st:
-        if Q is not None and Q_out is None:
-            Q_out = Q.new_empty(Q.shape)
-        if K is not None and K_out is None:
-            K_out = K.new_empty(K.shape)
+        if Q is not None:
+            Hq = Q.shape[2]
+            qs = _fit4(Q, "Q", (B, T, Hq, 128), dev)
+            if Q_out is None:
+                Q_out = torch.empty_like(Q)
+            qos = _fit4(Q_out, "Q_out", (B, T, Hq, 128), dev)
+        elif Q_out is not None:
+            raise ValueError("Q_out without Q")
+        if K is not None:
+            Hkv = _shape4(K, "K")[2]
+            ks = _fit4(K, "K", (B, T, Hkv, 128), dev)
+            if K_out is None:
+                K_out = torch.empty_like(K)
+            kos = _fit4(K_out, "K_out", (B, T, Hkv, 128), dev)
+        elif K_out is not None:
+            raise ValueError("K_out without K")
         if workspace is None:
             workspace = cache_workspace(x.device)
         _check("ea_rope", lib().ea_rope(
-            _ptr(Q), _ptr(Q_out), _strides4(Q), _strides4(Q_out), heads[0], _ptr(K), _ptr(K_out),
-            _strides4(K), _strides4(K_out), heads[1], B, T, 128, inv_freq.data_ptr(), rot,
-            1 if interleaved else 0, float(rope_scale), positions.data_ptr(), _ptr(n_new),
+            _adr(Q), _adr(Q_out), qs, qos, Hq, _adr(K), _adr(K_out), ks, kos, Hkv, B, T, 128, inv_freq.data_ptr(),
+            2 * half, 1 if interleaved else 0, rope_scale, positions.data_ptr(), _adr(n_new),
             workspace.data_ptr(), workspace.numel(), st))
     return Q_out, K_out
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
 
 
 def ea_cache_write_rope(cache, K, V, inv_freq, *, Q=None, Q_out=None, start=None, n_new=None, rows=None,
@@ -1091,46 +1125,46 @@ def ea_cache_write_rope(cache, K, V, inv_freq, *, Q=None, Q_out=None, start=None
     and V (an accepted path).  positions (int32 [B, T]) of the rows of K (and
     Q); None: start[b] + i.  Q [B, T, Hq, 128] (not with rows) is rotated into
     Q_out (may be Q; allocated if None), which is returned."""
-    _dev(K, "K", torch.bfloat16)
-    _dev(V, "V", torch.bfloat16)
-    if K.dim() != 4 or V.shape != K.shape or V.stride() != K.stride():
-        raise ValueError("K and V must share 4-dimensional shapes and strides")
-    B, T, Hkv, d = K.shape
-    if (B, Hkv, d) != (cache.B, cache.Hkv, 128):
-        raise ValueError("K and V must be [%d, T, %d, 128]" % (cache.B, cache.Hkv))
-    rot = 2 * _like(inv_freq, "inv_freq", (inv_freq.numel(),), torch.float32).numel()
-    _i32_vec(start, "start", B)
-    _i32_vec(n_new, "n_new", B)
-    _i32_rows(rows, "rows", B, T)
-    _i32_rows(positions, "positions", B, T)
-    Hq = 0
-    if Q is not None:
-        if rows is not None:
-            raise ValueError("Q and rows do not go together")
-        if Q.dim() != 4:
-            raise ValueError("Q must be [B, T, Hq, 128]")
-        Hq = Q.shape[2]
-        _rows4(Q, "Q", (B, T, Hq, 128))
-        if Q_out is not None:
-            _rows4(Q_out, "Q_out", (B, T, Hq, 128))
-    elif Q_out is not None:
-        raise ValueError("Q_out without Q")
-    _one_device(cache.K, K, V, inv_freq, Q, Q_out, start, n_new, rows, positions, workspace)
+    B, T, Hkv = _shape4(K, "K")[:3]
+    _dev(V, "V", _BF16)
+    if V.shape != K.shape or V.stride() != K.stride():
+        raise ValueError("K and V must share shapes and strides")
+    if not isinstance(cache, KVCache) or (B, Hkv) != (cache.B, cache.Hkv):
+        raise ValueError("K and V must have the sequences and heads of the KVCache")
+    dev = cache.device.index
+    ns = _fit4(K, "K", (B, T, Hkv, 128), dev)
+    _fit4(V, "V", (B, T, Hkv, 128), dev)
+    _needed(inv_freq, "inv_freq")
+    half = inv_freq.numel()
+    _fit(inv_freq, "inv_freq", torch.float32, (half,), dev)
+    _fit(start, "start", _I32, (B,), dev)
+    _fit(n_new, "n_new", _I32, (B,), dev)
+    _fit(rows, "rows", _I32, (B, T), dev)
+    _fit(positions, "positions", _I32, (B, T), dev)
+    _workspace_fits(workspace, dev)
+    Hq, qs, qos = 0, None, None
     with _at(cache.device, stream) as st:
-        if Q is not None and Q_out is None:
-            Q_out = Q.new_empty(Q.shape)
+        if Q is not None:
+            if rows is not None:
+                raise ValueError("Q and rows do not go together")
+            Hq = _shape4(Q, "Q")[2]
+            qs = _fit4(Q, "Q", (B, T, Hq, 128), dev)
+            if Q_out is None:
+                Q_out = torch.empty_like(Q)
+            qos = _fit4(Q_out, "Q_out", (B, T, Hq, 128), dev)
+        elif Q_out is not None:
+            raise ValueError("Q_out without Q")
         if workspace is None:
             workspace = cache_workspace(cache.device)
         _check("ea_cache_write_rope", lib().ea_cache_write_rope(
-            cache._ref, K.data_ptr(), V.data_ptr(), _I64[4](*K.stride()), _ptr(Q), _ptr(Q_out), _strides4(Q),
-            _strides4(Q_out), Hq, inv_freq.data_ptr(), rot, 1 if interleaved else 0, float(rope_scale),
-            _ptr(positions), _ptr(start), _ptr(n_new), _ptr(rows), B, T, workspace.data_ptr(),
-            workspace.numel(), st))
+            cache._ref, K.data_ptr(), V.data_ptr(), ns, _adr(Q), _adr(Q_out), qs, qos, Hq, inv_freq.data_ptr(),
+            2 * half, 1 if interleaved else 0, rope_scale, _adr(positions), _adr(start), _adr(n_new), _adr(rows), B,
+            T, workspace.data_ptr(), workspace.numel(), st))
     return Q_out
 
 
 def _tree_shape(t, name):
-    _dev(t, name, torch.int32)
+    _dev(t, name, _I32)
     if t.dim() != 2 or not t.is_contiguous():
         raise ValueError("%s must be a contiguous [B, T] tensor" % name)
     return t.shape
@@ -1143,20 +1177,20 @@ def ea_tree_plan(parents, n_nodes=None, *, depth=None, mask=None, workspace=None
     u // 32 for the node itself and every ancestor u); zeros behind a
     sequence's last node."""
     B, T = _tree_shape(parents, "parents")
-    _i32_vec(n_nodes, "n_nodes", B)
-    _i32_rows(depth, "depth", B, T)
-    if mask is not None:
-        _like(mask, "mask", (B, T, 4), torch.int32)
-    _one_device(parents, n_nodes, depth, mask, workspace)
+    dev = parents.get_device()
+    _fit(n_nodes, "n_nodes", _I32, (B,), dev)
+    _fit(depth, "depth", _I32, (B, T), dev)
+    _fit(mask, "mask", _I32, (B, T, 4), dev)
+    _workspace_fits(workspace, dev)
     with _at(parents.device, stream) as st:
         if depth is None:
-            depth = parents.new_empty((B, T))
+            depth = torch.empty_like(parents)
         if mask is None:
-            mask = parents.new_empty((B, T, 4))
+            mask = torch.empty((B, T, 4), dtype=_I32, device=parents.device)
         if workspace is None:
             workspace = cache_workspace(parents.device)
         _check("ea_tree_plan", lib().ea_tree_plan(
-            parents.data_ptr(), _ptr(n_nodes), B, T, depth.data_ptr(), mask.data_ptr(), workspace.data_ptr(),
+            parents.data_ptr(), _adr(n_nodes), B, T, depth.data_ptr(), mask.data_ptr(), workspace.data_ptr(),
             workspace.numel(), st))
     return depth, mask
 
@@ -1183,40 +1217,45 @@ def ea_hybrid_attn_tree(Q, K, V, cache, seqlens, depth, mask, m, *, sink, window
     [B] (None: T; rows at or behind it are not written), block_mask uint8 [B,
     Hkv, nB, nB] (nB = ceil(capacity / 128)) when a head is BLOCK; all CUDA.
     Returns (O [B, T, Hq, 128], LSE float32 [B, Hq, T])."""
-    for t, nm in ((Q, "Q"), (K, "K"), (V, "V")):
-        _dev(t, nm, torch.bfloat16)
-    if Q.dim() != 4 or Q.shape[0] != cache.B or Q.shape[3] != 128:
-        raise ValueError("Q must be [%d, T, Hq, 128]" % cache.B)
-    B, T, Hq, d = Q.shape
-    if tuple(K.shape) != (B, T, cache.Hkv, 128) or V.shape != K.shape or V.stride() != K.stride():
-        raise ValueError("K and V must be [%d, %d, %d, 128] and share strides" % (B, T, cache.Hkv))
-    for t, nm in ((seqlens, "seqlens"), (depth, "depth"), (mask, "mask")):
+    B, T, Hq = _shape4(Q, "Q")[:3]
+    if not isinstance(cache, KVCache) or B != cache.B:
+        raise ValueError("Q must have the sequences of the KVCache")
+    dev, Hkv = cache.device.index, cache.Hkv
+    qs = _fit4(Q, "Q", (B, T, Hq, 128), dev)
+    ks = _fit4(K, "K", (B, T, Hkv, 128), dev)
+    _fit4(V, "V", (B, T, Hkv, 128), dev)
+    if V.stride() != K.stride():
+        raise ValueError("K and V must share strides")
+    for t, nm in ((seqlens, "seqlens"), (depth, "depth"), (mask, "mask"), (m, "m")):
         if t is None:
             raise ValueError("%s is needed" % nm)
-    _i32_vec(seqlens, "seqlens", B)
-    _i32_vec(n_nodes, "n_nodes", B)
-    _i32_rows(depth, "depth", B, T)
-    _like(mask, "mask", (B, T, 4), torch.int32)
-    _like(m, "m", (B, cache.Hkv), torch.uint8)
-    bm = _block_mask_arg(block_mask, B, cache.Hkv, cache.capacity)
-    if O is not None:
-        _rows4(O, "O", (B, T, Hq, 128))
-    if LSE is not None:
-        _like(LSE, "LSE", (B, Hq, T), torch.float32)
-    _one_device(cache.K, Q, K, V, seqlens, n_nodes, depth, mask, m, bm, O, LSE, workspace)
+    _fit(seqlens, "seqlens", _I32, (B,), dev)
+    _fit(n_nodes, "n_nodes", _I32, (B,), dev)
+    _fit(depth, "depth", _I32, (B, T), dev)
+    _fit(mask, "mask", _I32, (B, T, 4), dev)
+    _fit(m, "m", torch.uint8, (B, Hkv), dev)
+    _fit(LSE, "LSE", torch.float32, (B, Hq, T), dev)
+    bm = _block_mask_arg(block_mask, B, Hkv, cache.capacity)
+    if bm is not None and bm.get_device() != dev:
+        raise ValueError("tensors on several devices: block_mask on %s" % bm.device)
+    _workspace_fits(workspace, dev)
     with _at(cache.device, stream) as st:
         if O is None:
-            O = Q.new_empty(Q.shape)
+            O = torch.empty_like(Q)
+        os = _fit4(O, "O", (B, T, Hq, 128), dev)
         if LSE is None and want_lse:
-            LSE = Q.new_empty((B, Hq, T), dtype=torch.float32)
+            LSE = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device)
         if workspace is None:
-            workspace = tree_workspace(B, T, Hq, cache.Hkv, cache.capacity, d, Q.device)
+            workspace = tree_workspace(B, T, Hq, Hkv, cache.capacity, 128, cache.device)
         _check("ea_hybrid_attn_tree", lib().ea_hybrid_attn_tree(
-            Q.data_ptr(), K.data_ptr(), V.data_ptr(), cache._ref, O.data_ptr(), _ptr(LSE), _I64[4](*Q.stride()),
-            _I64[4](*K.stride()), _I64[4](*O.stride()), seqlens.data_ptr(), _ptr(n_nodes), depth.data_ptr(),
-            mask.data_ptr(), B, T, Hq, 1.0 / math.sqrt(d) if scale is None else float(scale), m.data_ptr(), int(sink),
-            int(window), _ptr(bm), TILE, workspace.data_ptr(), workspace.numel(), st))
+            Q.data_ptr(), K.data_ptr(), V.data_ptr(), cache._ref, O.data_ptr(), _adr(LSE), qs, ks, os,
+            seqlens.data_ptr(), _adr(n_nodes), depth.data_ptr(), mask.data_ptr(), B, T, Hq,
+            _SCALE128 if scale is None else float(scale), m.data_ptr(), int(sink), int(window), _adr(bm),
+            TILE, workspace.data_ptr(), workspace.numel(), st))
     return O, LSE
+
+
+_SCALE128 = 1.0 / math.sqrt(128)
 
 
 def ea_tree_accept(tokens, parents, targets, n_nodes=None, *, path=None, n_accepted=None, next_token=None,
@@ -1227,24 +1266,27 @@ def ea_tree_accept(tokens, parents, targets, n_nodes=None, *, path=None, n_accep
     T], -1 behind the accepted nodes; n_accepted int32 [B]; next_token int32
     [B])."""
     B, T = _tree_shape(tokens, "tokens")
-    for t, nm in ((parents, "parents"), (targets, "targets"), (path, "path")):
-        if t is None and nm != "path":
-            raise ValueError("%s is needed" % nm)
-        _i32_rows(t, nm, B, T)
-    for t, nm in ((n_nodes, "n_nodes"), (n_accepted, "n_accepted"), (next_token, "next_token")):
-        _i32_vec(t, nm, B)
-    _one_device(tokens, parents, targets, n_nodes, path, n_accepted, next_token, workspace)
+    _needed(parents, "parents")
+    _needed(targets, "targets")
+    dev = tokens.get_device()
+    _fit(parents, "parents", _I32, (B, T), dev)
+    _fit(targets, "targets", _I32, (B, T), dev)
+    _fit(path, "path", _I32, (B, T), dev)
+    _fit(n_nodes, "n_nodes", _I32, (B,), dev)
+    _fit(n_accepted, "n_accepted", _I32, (B,), dev)
+    _fit(next_token, "next_token", _I32, (B,), dev)
+    _workspace_fits(workspace, dev)
     with _at(tokens.device, stream) as st:
         if path is None:
-            path = tokens.new_empty((B, T))
+            path = torch.empty_like(tokens)
         if n_accepted is None:
-            n_accepted = tokens.new_empty(B)
+            n_accepted = torch.empty(B, dtype=_I32, device=tokens.device)
         if next_token is None:
-            next_token = tokens.new_empty(B)
+            next_token = torch.empty_like(n_accepted)
         if workspace is None:
             workspace = cache_workspace(tokens.device)
         _check("ea_tree_accept", lib().ea_tree_accept(
-            tokens.data_ptr(), parents.data_ptr(), targets.data_ptr(), _ptr(n_nodes), B, T, path.data_ptr(),
+            tokens.data_ptr(), parents.data_ptr(), targets.data_ptr(), _adr(n_nodes), B, T, path.data_ptr(),
             n_accepted.data_ptr(), next_token.data_ptr(), workspace.data_ptr(), workspace.numel(), st))
     return path, n_accepted, next_token
 

@@ -412,7 +412,7 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
     constexpr int kStages = Smem::kStages, kCodes = Smem::kCodes;
     uint32_t *err = &a.hdr->error;
     int u = sm.u, off = sm.off, left = sm.count;
-    TreeUnit &x = sm.unit;               // the unit at hand
+    TreeUnit x = sm.unit;                // the unit at hand
     uint32_t it = 0, entry = 0, codes = 0, tile = 0;
     bool ok = true;
     auto publish = [&](const TreeSeg &s) {
@@ -429,11 +429,7 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
     while (ok && left > 0) {
         const int len = x.nt + kTPartTiles;
         if (off >= len * x.pairs) {
-            const TreeUnit next = tree_unit(a, ++u);
-            __syncwarp();
-            if (lane == 0)
-                x = next;
-            __syncwarp();
+            x = tree_unit(a, ++u);
             off = 0;
             continue;
         }
@@ -798,19 +794,32 @@ __device__ __forceinline__ float pow2f(int e)          // -126 .. 127
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// The largest finite magnitude among eight bf16 numbers and `m` (two 16-bit halves of bits).
-__device__ __forceinline__ uint32_t max_finite(const uint4 &v, uint32_t m)
+// The largest magnitude among eight bf16 numbers and `m`; NaN do not count.
+__device__ __forceinline__ float max_mag(const uint4 &v, float m)
 {
-    const uint32_t w[4] = {v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu};
-    const uint32_t all = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
-    if ((all & 0xffffu) < 0x7f80u && all < 0x7f800000u)
-        return __vmaxu2(m, all);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0xffffu, hi = w[i] & 0xffff0000u;
-        m = __vmaxu2(m, (lo < 0x7f80u ? lo : 0u) | (hi < 0x7f800000u ? hi : 0u));
+    for (int i = 0; i < 4; ++i)
+        m = max3f(m, __uint_as_float((w[i] << 16) & 0x7fffffffu), __uint_as_float(w[i] & 0x7fff0000u));
+    return m;
+}
+
+// The same without infinities.
+__device__ __forceinline__ float max_finite(const uint4 &v, float m)
+{
+    const uint32_t w[8] = {v.x << 16, v.x, v.y << 16, v.y, v.z << 16, v.z, v.w << 16, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = __uint_as_float(w[i] & 0x7fff0000u);
+        m = x < __uint_as_float(0x7f800000u) ? fmaxf(m, x) : m;
     }
     return m;
+}
+
+// The biased exponent of a non-negative number.
+__device__ __forceinline__ int exponent_of(float x)
+{
+    return static_cast<int>(__float_as_uint(x) >> 23);
 }
 
 // Eight bf16 numbers times f as f16.
@@ -863,13 +872,14 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                 __syncwarp();
                 const bool got = mbar_wait_warp(&sm.own_full[kv], own & 1, &sm.abort, err);
                 const int rows = (s.n + 15) & ~15;
-                uint32_t mx = 0;
+                float mx = 0.f;
                 if (got && ct < s.n)
+#pragma unroll 8
                     for (int c = 0; c < 16; ++c)
                         mx = max_finite(*reinterpret_cast<const uint4 *>(dst + (c >> 3) * kTHalf + ct * 128 + (((c & 7) ^ (ct & 7)) << 4)), mx);
-                mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+                const int ex = __reduce_max_sync(0xffffffffu, exponent_of(mx));
                 if (lane == 0) {
-                    sm.own_exp[own & 1][kv][ct / 32] = static_cast<uint8_t>(mx >> 7);
+                    sm.own_exp[own & 1][kv][ct / 32] = static_cast<uint8_t>(ex);
                     mbar_arrive(&sm.own_max[kv]);
                 }
                 __syncwarp();
@@ -884,6 +894,7 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                 const int e = min(14 + 127 - top, 120);
                 const float f = pow2f(e);
                 if (ct < rows)
+#pragma unroll 8
                     for (int c = 0; c < 16; ++c) {
                         uint4 *p = reinterpret_cast<uint4 *>(dst + (c >> 3) * kTHalf + ct * 128 + (((c & 7) ^ (ct & 7)) << 4));
                         *p = bf16_to_f16(*p, f);
@@ -1106,17 +1117,24 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                     return;                            // (the last range's maxima have been read)
                 if (active) {
                     uint8_t *row = sm.q[mt] + r * 128;
-                    uint32_t mx = 0;
-#pragma unroll 4
+                    auto part = [&](int c) { return reinterpret_cast<uint4 *>(row + (c >> 3) * kTHalf + (((c & 7) ^ (r & 7)) << 4)); };
+                    float mx[2] = {0.f, 0.f};
+#pragma unroll 8
                     for (int c = 0; c < 16; ++c)
-                        mx = max_finite(*reinterpret_cast<const uint4 *>(row + (c >> 3) * kTHalf + (((c & 7) ^ (r & 7)) << 4)), mx);
-                    const int e = min(10 + 127 - static_cast<int>(max(mx & 0xffffu, mx >> 16) >> 7), 120);
-                    const float f = pow2f(e);
-#pragma unroll 4
-                    for (int c = 0; c < 16; ++c) {
-                        uint4 *p = reinterpret_cast<uint4 *>(row + (c >> 3) * kTHalf + (((c & 7) ^ (r & 7)) << 4));
-                        *p = bf16_to_f16(*p, f);
+                        mx[c & 1] = max_mag(*part(c), mx[c & 1]);
+                    mx[0] = fmaxf(mx[0], mx[1]);
+                    if (exponent_of(mx[0]) == 255) {
+                        mx[0] = 0.f;
+#pragma unroll 1
+                        for (int c = 0; c < 16; ++c)
+                            mx[0] = max_finite(*part(c), mx[0]);
                     }
+                    const int e = min(10 + 127 - exponent_of(mx[0]), 120);
+                    const float f = pow2f(e);
+                    asm volatile("" ::: "memory");       // (read again, not kept)
+#pragma unroll 8
+                    for (int c = 0; c < 16; ++c)
+                        *part(c) = bf16_to_f16(*part(c), f);
                     cs = a.scale_log2 * pow2f(-e);
                 }
                 if (!two)
@@ -1426,6 +1444,43 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
 }
 
 // ------------------------------------------------------------ kernels
+// A barrier a lane and step, by its place among them.
+template <class Smem>
+__device__ __forceinline__ void tree_barriers(Smem &sm, int lane)
+{
+    constexpr int S = Smem::kStages, C = Smem::kCodes, users = 8 + 3 + (Smem::Q8 ? kTConvWarps : 0);
+    struct Kind {
+        int n, count;
+    };
+    constexpr Kind kinds[] = {
+        {S, Smem::Q8 ? kTConvWarps / 2 : 1},            // full
+        {S, 2},                                         // empty: the product that used it, and the warp that looks V over
+        {C, 1}, {C, kTConvWarps / 2},                   // code_full, code_empty
+        {kTReady, 1},
+        {kTSegs, 1}, {kTSegs, users},
+        {1, 1}, {1, 1},                                 // q_full, q_empty
+        {2, 1}, {2, 4}, {2, 1},                         // s_full, p_full, o_done
+        {1, 1}, {1, 8}, {1, 8}, {1, 2},                 // seg_done, ml_full, o_free, drain
+        {1, 8}, {2, 1}, {2, 4},                         // q_ready, own_full, own_max
+    };
+    constexpr int kAll = static_cast<int>((offsetof(Smem, seg) - offsetof(Smem, full)) / sizeof(uint64_t));
+    static_assert(2 * S + 2 * C + kTReady + 2 * kTSegs + 2 + 6 + 4 + 5 == kAll, "every barrier is set up");
+    for (int i = lane; i < kAll; i += 32) {
+        int count = 1, end = 0;
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(kinds) / sizeof(Kind)); ++k) {
+            count = i >= end ? kinds[k].count : count;
+            end += kinds[k].n;
+        }
+        mbar_init(sm.full + i, count);
+    }
+    if (lane == 0)
+        sm.abort = 0;
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 template <int FMT, bool TWO>
 __global__ void __launch_bounds__(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8, 1)
     tree_attn_kernel(const __grid_constant__ TreeMaps tm, const TreeArgs a)
@@ -1440,63 +1495,34 @@ __global__ void __launch_bounds__(FMT == EA_CACHE_BF16 ? kTThreads : kTThreadsQ8
             raise_error(&a.hdr->error, EA_DEVERR_BOUNDS);
         return;
     }
-    if (warp == 0) {
-        constexpr int users = 8 + 3 + (kQ8 ? kTConvWarps : 0);
-        if (lane < Smem::kStages) {
-            mbar_init(&sm.full[lane], kQ8 ? kTConvWarps / 2 : 1);
-            mbar_init(&sm.empty[lane], 2);
+    // The producer sets the barriers up and goes on to its range and its first copies; the others wait
+    // for that and for TMEM.
+    if (warp == kTProducerWarp) {
+        tree_barriers(sm, lane);
+        if (a.B * a.Hkv <= kTWarpUnits) {
+            griddep_wait();
+            named_bar_arrive(1, blockDim.x);
+            tree_range(a, sm, lane, 1);
+            __syncwarp();
         }
-        if (lane < Smem::kCodes) {
-            mbar_init(&sm.code_full[lane], 1);
-            mbar_init(&sm.code_empty[lane], kTConvWarps / 2);
-        }
-        if (lane < kTReady)
-            mbar_init(&sm.ready[lane], 1);
-        if (lane < kTSegs) {
-            mbar_init(&sm.seg_full[lane], 1);
-            mbar_init(&sm.seg_empty[lane], users);
-        }
-        if (lane < 2) {
-            mbar_init(&sm.s_full[lane], 1);
-            mbar_init(&sm.p_full[lane], 4);
-            mbar_init(&sm.o_done[lane], 1);
-        }
-        if (lane == 0) {
-            mbar_init(&sm.q_full, 1);
-            mbar_init(&sm.q_empty, 1);
-            mbar_init(&sm.seg_done, 1);
-            mbar_init(&sm.ml_full, 8);
-            mbar_init(&sm.o_free, 8);
-            mbar_init(&sm.drain, 2);
-            mbar_init(&sm.q_ready, 8);
-            for (int k = 0; k < 2; ++k) {
-                mbar_init(&sm.own_full[k], 1);
-                mbar_init(&sm.own_max[k], 4);
-            }
-            sm.abort = 0;
-        }
-        fence_barrier_init();
-        fence_proxy_async_smem();
     }
     if (warp == kTQkWarp) {
         tmem_alloc(&sm.tmem_base, 512);
         tmem_relinquish();
     }
-    if (warp == kTProducerWarp && lane == 0) {
-        tma_prefetch_desc(&tm.q);
-        tma_prefetch_desc(&tm.k);
-        tma_prefetch_desc(&tm.v);
-    }
-    griddep_wait();
-    griddep_launch_dependents();
-    if (a.B * a.Hkv > kTWarpUnits)
+    if (a.B * a.Hkv > kTWarpUnits) {
+        griddep_wait();
         tree_range(a, sm, threadIdx.x, blockDim.x / 32);
-    else if (warp == kTProducerWarp)
-        tree_range(a, sm, lane, 1);
-    tc_fence_before();
-    __syncthreads();
+        tc_fence_before();
+        __syncthreads();
+    } else if (warp != kTProducerWarp) {
+        griddep_wait();
+        tc_fence_before();
+        named_bar_sync(1, blockDim.x);
+    }
+    griddep_launch_dependents();
     tc_fence_after();
-    const uint32_t tmem = sm.tmem_base;
+    const uint32_t tmem = warp == kTProducerWarp ? 0u : sm.tmem_base;
 
     // Registers go to the softmax: 256 x 208 + 128 x 88 of the launch's 384 x 168, or, with
     // converting warps, 256 x 128 + 128 x 72 + 256 x 72 of its 640 x 96.
