@@ -339,3 +339,44 @@ def test_a_whole_step(dev):
         now = logical(dict(c, K=h.K.cpu(), V=h.V.cpu()))
         for b in range(B):                               # the accepted ones alone, with the bits that attended
             assert np.array_equal(now[0][b, : lens[b]], Kc[b, : lens[b]]) and np.array_equal(now[1][b, : lens[b]], Vc[b, : lens[b]])
+
+
+def test_two_calls_at_once(dev):
+    """Two streams, each with a workspace of its own, over one cache and shared pages."""
+    B, T, Hq, Hkv = 2, 20, 16, 2
+    c = make_cache(1, 512, Hkv, BF16, 64, 64, 4)
+    table = c["table"].repeat(B, 1).contiguous()          # both sequences read the same pages, a row each
+    h = ea.KVCache(c["K"].to(dev), c["V"].to(dev), block_table=table.to(dev))
+    Q, K, V = (x.to(dev) for x in inputs(B, T, Hq, Hkv, 9))
+    depth, mask = (i32(x, dev) for x in plan(random_tree(B, T, 3), [T] * B))
+    m = torch.tensor([[FULL, SSA]] * B, dtype=torch.uint8, device=dev)
+    lens = i32([500, 300], dev)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [ea.tree_workspace(B, T, Hq, Hkv, h.capacity, device=dev) for _ in streams]
+    call = lambda w, s: ea.ea_hybrid_attn_tree(Q, K, V, h, lens, depth, mask, m, sink=4, window=64, workspace=w, stream=s)  # noqa: E731
+    ref = call(ws[0], None)
+    torch.cuda.synchronize()
+    got = [[call(w, s) for w, s in zip(ws, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for o, l in pair:
+            assert torch.equal(o, ref[0]) and torch.equal(l, ref[1])
+    for w in ws:
+        check_no_device_error(w)
+
+
+def test_masks_that_leave_nothing(dev):
+    """No ancestors, no cache: zero and -inf, for some rows and for all."""
+    B, T, Hq = 2, 5, 4
+    Q, K, V = (x.to(dev) for x in inputs(B, T, Hq, 1, 2))
+    depth = torch.zeros(B, T, dtype=torch.int32, device=dev)
+    mask = torch.zeros(B, T, 4, dtype=torch.int32, device=dev)
+    mask[1, 2, 0] = 1 << 4
+    m = torch.zeros(B, 1, dtype=torch.uint8, device=dev)
+    for dtype in (BF16, INT8):
+        c = handle(make_cache(B, 128, 1, dtype, 64, 0, 1), dev)
+        O, LSE = ea.ea_hybrid_attn_tree(Q, K, V, c, i32([0, 0], dev), depth, mask, m, sink=0, window=1)
+        none = torch.ones(B, T, dtype=torch.bool, device=dev)
+        none[1, 2] = False
+        assert not O[none].any() and torch.isneginf(LSE.transpose(1, 2)[none]).all()
+        assert (O[1, 2].float() - V[1, 4, 0].float()).abs().max() <= 2.0 ** -8 * V[1, 4].float().abs().max()

@@ -107,3 +107,60 @@ def test_binding_refuses_host_tensors():
                  lambda: ea.ea_tree_accept(i, i, i), lambda: ea.ea_cache_write_rope(None, x, x, f)):
         with pytest.raises(ValueError):
             call()
+
+
+def _attn(L, c, **kw):
+    a = dict(Q=P, K=P, V=P, O=P, LSE=None, qs=Q4, ks=K4, os=Q4, sl=P, n=None, d=P, mk=P, B=4, T=8, Hq=32, scale=0.1, m=P, sink=4, window=64,
+             bm=None, bs=128, ws=P, wsb=1 << 40)
+    a.update(kw)
+    return L.ea_hybrid_attn_tree(a["Q"], a["K"], a["V"], None if c is None else ctypes.byref(c), a["O"], a["LSE"], a["qs"], a["ks"], a["os"],
+                                 a["sl"], a["n"], a["d"], a["mk"], a["B"], a["T"], a["Hq"], ctypes.c_float(a["scale"]), a["m"], a["sink"],
+                                 a["window"], a["bm"], a["bs"], a["ws"], a["wsb"], None)
+
+
+@pytest.mark.parametrize("make,kw,expect", ALL_BAD)
+def test_attention_refuses_bad_caches(L, make, kw, expect):
+    assert _attn(L, make(**kw)) == expect
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(Q=None), INVALID), (dict(K=None), INVALID), (dict(V=None), INVALID), (dict(O=None), INVALID), (dict(sl=None), INVALID),
+    (dict(d=None), INVALID), (dict(mk=None), INVALID), (dict(mk=P + 8), INVALID), (dict(m=None), INVALID), (dict(qs=None), INVALID),
+    (dict(ks=None), INVALID), (dict(os=None), INVALID), (dict(B=0), INVALID), (dict(B=3), INVALID), (dict(T=0), INVALID),
+    (dict(Hq=0), INVALID), (dict(Hq=31), INVALID), (dict(sink=-1), INVALID), (dict(window=0), INVALID), (dict(scale=0.0), INVALID),
+    (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(bs=64), INVALID), (dict(Q=P + 8), INVALID),
+    (dict(K=P + 2), INVALID), (dict(O=P + 4), INVALID), (dict(T=129), UNSUPPORTED), (dict(Hq=8 * 65), UNSUPPORTED),
+    (dict(ws=None), WORKSPACE), (dict(ws=P + 128), WORKSPACE), (dict(wsb=1000), WORKSPACE),
+] + [(dict(**{k: s}), INVALID) for s in BAD_STRIDES for k in ("qs", "ks", "os")])
+def test_attention_refuses_bad_arguments(L, kw, expect):
+    assert _attn(L, cache(), **kw) == expect
+
+
+def test_attention_refuses_no_cache_and_pages_of_odd_size(L):
+    assert _attn(L, None) == INVALID
+    assert _attn(L, paged(format=BF16, rows=80, k_scale=None, v_scale=None)) == UNSUPPORTED
+    assert _attn(L, paged(scale_block=32, rows=96, kv_str=_str(96 * 1024, 1024, 128, 1))) == UNSUPPORTED
+    # more tiles than are counted in 32 bits; block masks whose rows are not numbered
+    assert _attn(L, cache(outer=60000, rows=1 << 20), B=60000) == UNSUPPORTED
+    assert _attn(L, cache(rows=128 * 65536), bm=P) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("sizes", [(0, 8, 32, 8, 128, 4096), (4, 0, 32, 8, 128, 4096), (4, 129, 32, 8, 128, 4096), (4, 8, 31, 8, 128, 4096),
+                                   (4, 8, 0, 8, 128, 4096), (4, 8, 32, 0, 128, 4096), (4, 8, 520, 8, 128, 4096), (4, 8, 32, 8, 64, 4096),
+                                   (4, 8, 32, 8, 128, 0), (60000, 8, 32, 8, 128, 1 << 30)])
+def test_attention_workspace_of_bad_sizes(L, sizes):
+    assert L.ea_tree_workspace_size(*sizes) == 0
+
+
+def test_attention_workspace_sizes(L):
+    # the partial results are bounded by the grid, not by the batch or the lengths
+    small, large = (L.ea_tree_workspace_size(*s) for s in ((1, 8, 32, 8, 128, 4096), (64, 8, 32, 8, 128, 131072)))
+    assert 256 < small < large < small + 4 * 64 * 8 * (1024 + 4)
+    assert L.ea_tree_workspace_size(1, 33, 32, 8, 128, 4096) > 1.9 * small          # two M tiles
+
+
+def test_attention_binding_refuses():
+    x = torch.zeros(1, 4, 2, 128, dtype=torch.bfloat16)
+    i = torch.zeros(1, 4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        ea.ea_hybrid_attn_tree(x, x, x, None, i[0], i, i, i, sink=1, window=1)
