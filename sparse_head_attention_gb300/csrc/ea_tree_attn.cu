@@ -11,8 +11,12 @@
 //
 // What bounds it: each kept key's K and V are read once for up to 256 rows (two M tiles
 // share a key tile), 64 KB a tile of bf16, which an SM receives in 1.45 us at the measured
-// HBM rate; two M tiles take 0.55 us of tensor core and 0.5 of the SFU.  So HBM, up to
-// some 500 rows a KV head.
+// HBM rate; two M tiles take 0.55 us of tensor core and 0.5 of the SFU.  So HBM where one M tile
+// does: 16 sequences of 64K with trees of 32 take 0.65 ms, 0.97 of the measured rate.  Two M tiles
+// take 2.0 us a tile (0.88 ms with trees of 64, 1250 TFLOP/s): S = Q K^T, the softmax and O += P V
+// of a tile wait for one another, and TMEM has no room for a second S of each.  An 8-bit cache's
+// tile takes 1.3 us (0.57 ms with trees of 16, 0.55 of the measured rate): the same chain, beside the
+// conversion.
 //
 // Work.  Key tiles of all (sequence, KV head, pair of M tiles) form one line, which is cut
 // into equal ranges, one a CTA: no CTA idles, and at most two ranges of a CTA's begin or
@@ -29,8 +33,7 @@
 //                NaN), and tiles of which some rows keep a key and others do not are searched
 //                for infinities and NaN; such a tile's product is taken by the softmax warps,
 //                key by key
-//   warps 12-19  8-bit caches: codes from HBM to registers, times their scale (exact in bf16),
-//                into the ring
+//   warps 12-19  8-bit caches: tiles of codes, that TMA brought, become f16 ones in the ring
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -667,12 +670,12 @@ __device__ __forceinline__ void tree_pv(const TreeArgs &a, Smem &sm, uint32_t tm
             if (!(flags & kEdge)) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    mma_ts(go, to, tp + (k < 4 ? 8 * k : 32 + 8 * k), vd + k * (2048 >> 4), kIdPV, k ? 1u : more);
+                    mma_ts(go, to, tp + 32 * (k >> 1) + 8 * (k & 1), vd + k * (2048 >> 4), kIdPV, k ? 1u : more);
             } else if (!odd) {
                 const int groups = flags >> kGroups;
 #pragma unroll 1
                 for (int k = 0; k < groups; ++k)
-                    mma_ts(go, to, tp + (k < 4 ? 8 * k : 32 + 8 * k), vd + k * (2048 >> 4), kIdPV, k ? 1u : more);
+                    mma_ts(go, to, tp + 32 * (k >> 1) + 8 * (k & 1), vd + k * (2048 >> 4), kIdPV, k ? 1u : more);
             }
             commit_if(go, &sm.o_done[w]);
             if (!two || w == 1)
@@ -840,6 +843,9 @@ __device__ __forceinline__ uint4 bf16_to_f16(const uint4 &v, float f)
 // codes of either half of eight rows, one row of each 16-key group, so lane i holds the scale of group
 // i.  They become 16 bytes of the row in either half of the tile, swizzled as TMA would (odd rows'
 // lanes take the second half first: two rows' codes then lie in different banks).
+// A row an iteration, the next one's codes under its work: five roles take turns on a scheduler, and
+// what bounded them when their loops were unrolled was instruction fetch (16 sequences of 64K: 680 us
+// with the rows unrolled here and half of the columns in the softmax, 573 now).
 template <bool E4M3, class Smem>
 __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs &a, Smem &sm, int kv, int ct, int lane)
 {
@@ -926,17 +932,8 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                     f = __ldg(reinterpret_cast<const uint32_t *>(scales) +
                               (static_cast<int64_t>(outer) * a.c.Hkv + s.h) * a.c.nsb + (row >> a.c.log2sb));
             }
-            uint2 c[8][2];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                c[i][0] = *reinterpret_cast<const uint2 *>(sm.code[cs] + 2048 * i + in0);
-                c[i][1] = *reinterpret_cast<const uint2 *>(sm.code[cs] + 2048 * i + in1);
-            }
             const int groups = ti.flags >> kGroups;
             const bool absent = ti.outer[lane >> 2 & 1] < 0;
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.code_empty[cs]);
             codes += 2;
             // the exponents, and the largest of them (0: no scale but NaN)
             const uint32_t e = (f & 0x7fffffffu) < 0x7f800000u ? f >> 23 : 0u;
@@ -960,22 +957,28 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                 ok = false;
                 break;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            const uint8_t *src = sm.code[cs];
+            uint2 c0 = *reinterpret_cast<const uint2 *>(src + in0), c1 = *reinterpret_cast<const uint2 *>(src + in1);
+#pragma unroll 1
+            for (int i = 0; i < groups; ++i) {
                 const uint32_t w = __shfl_sync(0xffffffffu, fg, i);
-                if (i < groups) {
-                    const __half2 x = *reinterpret_cast<const __half2 *>(&w);
-                    const __half2 fx = __low2half2(x), gx = __high2half2(x);
-                    const uint2 w0 = codes_scaled<E4M3>(c[i][0].x, fx, gx), w1 = codes_scaled<E4M3>(c[i][0].y, fx, gx);
-                    *reinterpret_cast<uint4 *>(dst + 2048 * i + at0) = make_uint4(w0.x, w0.y, w1.x, w1.y);
-                    const uint2 w2 = codes_scaled<E4M3>(c[i][1].x, fx, gx), w3 = codes_scaled<E4M3>(c[i][1].y, fx, gx);
-                    *reinterpret_cast<uint4 *>(dst + 2048 * i + at1) = make_uint4(w2.x, w2.y, w3.x, w3.y);
-                }
+                const uint32_t nx = 2048 * min(i + 1, 7);
+                const uint2 d0 = *reinterpret_cast<const uint2 *>(src + nx + in0), d1 = *reinterpret_cast<const uint2 *>(src + nx + in1);
+                const __half2 x = *reinterpret_cast<const __half2 *>(&w);
+                const __half2 fx = __low2half2(x), gx = __high2half2(x);
+                const uint2 w0 = codes_scaled<E4M3>(c0.x, fx, gx), w1 = codes_scaled<E4M3>(c0.y, fx, gx);
+                *reinterpret_cast<uint4 *>(dst + 2048 * i + at0) = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                const uint2 w2 = codes_scaled<E4M3>(c1.x, fx, gx), w3 = codes_scaled<E4M3>(c1.y, fx, gx);
+                *reinterpret_cast<uint4 *>(dst + 2048 * i + at1) = make_uint4(w2.x, w2.y, w3.x, w3.y);
+                c0 = d0;
+                c1 = d1;
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
                 mbar_arrive(&sm.full[st]);
+                mbar_arrive(&sm.code_empty[cs]);
+            }
         }
         if (ok)
             tree_done(sm, it);
@@ -1068,20 +1071,19 @@ __device__ __forceinline__ void exp32(const uint32_t (&x)[32], uint64_t c, uint6
     tmem_st16(tp, p);
 }
 
-// A row's 128 scores go through its thread's registers once (bf16 caches).  Beside the
-// converting warps there is room for half of them: the other half is read from TMEM twice.
-// P takes the place of the first half of either half of S.
+// A row's 128 scores go through its thread's registers once (bf16 caches); beside the
+// converting warps there is no room for them, they are read from TMEM twice.  The 32 columns'
+// P takes the place of the first half of their S.
 template <class Smem>
 __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32_t tmem, int warp, int lane)
 {
-    constexpr int kHeld = Smem::Q8 ? 2 : 4;           // chunks of 32 columns held
     constexpr bool TWO = sizeof(sm.q) > kTBytes;
     const float NEG_INF = -__int_as_float(0x7f800000);
     uint32_t *err = &a.hdr->error;
     const int wg = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_base + 128 * wg, to = tmem + lane_base + kTColO;
-    auto place = [&](int c) { return ts + (c < 2 ? 16 * c : 32 + 16 * c); };
+    auto place = [&](int c) { return ts + 32 * c; };
     uint32_t own = 0, tile0 = 0, joined = 0;
     const TreeSeg *sp;
     for (uint32_t it = 0; (sp = tree_take(a, sm, it)) != nullptr; ++it) {
@@ -1204,26 +1206,50 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         }
                     }
                 };
-                if (!edge) {
+                if (Smem::Q8 && !edge) {
+                    // (few registers, and little code: see tree_convert)
                     float mx = NEG_INF;
-                    uint32_t x[kHeld][32];
-                    if constexpr (kHeld == 2) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            tmem_ld32(ts + 32 * c, x[c]);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+                        uint32_t x[2][32];
+                        tmem_ld32(ts + 32 * c, x[0]);
+                        tmem_ld32(ts + 32 * c + 32, x[1]);
                         tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            tie32(x[c]);
-                            mx = max32(x[c], mx);
-                        }
+                        tie32(x[0]);
+                        tie32(x[1]);
+                        mx = max32(x[1], max32(x[0], mx));
                     }
+                    grow(mx);
+                    const float db = dv - (m == NEG_INF ? 0.f : m);
+                    const uint64_t d2 = f2_pack(db, db);
+                    uint64_t sum = 0;
+                    uint32_t x[32], y[32];
+                    tmem_ld32(ts + 96, x);
+#pragma unroll 1
+                    for (int c = 3; c >= 0; --c) {
+                        tmem_wait_ld();
+                        tie32(x);
 #pragma unroll
-                    for (int c = 0; c < kHeld; ++c)
-                        tmem_ld32(ts + 32 * (c + 4 - kHeld), x[c]);
+                        for (int i = 0; i < 32; ++i)
+                            y[i] = x[i];
+                        tie32(y);
+                        tmem_ld32(ts + 32 * max(c - 1, 0), x);       // the next, under this one's work
+                        exp32<Smem::Q8>(y, c2, d2, sum, place(c));
+                    }
+                    tmem_wait_ld();
+                    tie32(x);
+                    float u, v;
+                    f2_unpack(sum, u, v);
+                    l = fmaf(u + v, iv, l);
+                } else if (!edge) {
+                    float mx = NEG_INF;
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tmem_ld32(ts + 32 * c, x[c]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < kHeld; ++c) {
+                    for (int c = 0; c < 4; ++c) {
                         tie32(x[c]);
                         mx = max32(x[c], mx);
                     }
@@ -1232,24 +1258,13 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                     const uint64_t d2 = f2_pack(db, db);
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-                    for (int c = 0; c < kHeld; ++c)
-                        exp32<Smem::Q8>(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c + 4 - kHeld));
-                    if constexpr (kHeld == 2) {
-#pragma unroll
-                        for (int c = 0; c < 2; ++c)
-                            tmem_ld32(ts + 32 * c, x[c]);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            tie32(x[c]);
-                            exp32<Smem::Q8>(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c));
-                        }
-                    }
+                    for (int c = 0; c < 4; ++c)
+                        exp32<Smem::Q8>(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c));
                     float u, v;
                     f2_unpack(f2_add(sum0, sum1), u, v);
                     l = fmaf(u + v, iv, l);
                 } else if (!odd) {
-                    // 32 columns at a time, those that hold keys (P lies behind what is still to be read)
+                    // 32 columns at a time, those that hold keys
                     float mx = NEG_INF;
 #pragma unroll 1
                     for (int c = 0; c < chunks; ++c) {
