@@ -18,8 +18,9 @@
 // the same registers are rounded and stored.  The keys are rounded once, from fp32: a
 // key rotated, rounded to bf16 and then quantised would carry two errors.
 //
-// Only data moves, so HBM bounds long inputs, and the launch and four dependent loads
-// (length, row, page, data) short ones.
+// Only data moves, so HBM bounds long inputs (a 32K prefill into bf16 pages, 805 MB: 128 us,
+// 0.93 of the measured copy rate; an 8K chunk, Q and K alone: 60 us, 0.82), and the launch and
+// four dependent loads (length, row, page, data) short ones (16 drafts of four sequences 3.4 us).
 #include <cuda_runtime.h>
 
 #include "ea_cache.cuh"
