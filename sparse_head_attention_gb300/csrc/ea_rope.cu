@@ -18,8 +18,8 @@
 // the same registers are rounded and stored.  The keys are rounded once, from fp32: a
 // key rotated, rounded to bf16 and then quantised would carry two errors.
 //
-// Only data moves, so HBM bounds long inputs (a 32K prefill into bf16 pages, 805 MB: 128 us,
-// 0.93 of the measured copy rate; an 8K chunk, Q and K alone: 60 us, 0.82), and the launch and
+// Only data moves, so HBM bounds long inputs (a 32K prefill into bf16 pages, 805 MB: 122 us,
+// 0.97 of the measured copy rate; two chunks of 8K, Q and K alone: 55 us, 0.89), and the launch and
 // four dependent loads (length, row, page, data) short ones (16 drafts of four sequences 3.4 us).
 #include <cuda_runtime.h>
 
@@ -70,27 +70,32 @@ __device__ __forceinline__ uint64_t turns_per_position(float f, bool &bad)
 struct Rotation {
     float cs[8], sn[8];
     int a, b;                            // first dims of its two runs
-    bool on, pairs_next;
+    bool on_a, on_b, pairs_next;         // which of them turn
 
     __device__ __forceinline__ void place(int j, int rot, int interleaved)
     {
+        // (the runs of a row's threads lie side by side, so that each access is of whole sectors: with
+        // two neighbouring runs a thread, neighbours and what only moves took 60 and 128 us for 55 and 122)
         const int r16 = rot / 16;
-        on = j < r16;
         pairs_next = interleaved != 0;
-        if (on && !interleaved) {
+        if (pairs_next) {
             a = 8 * j;
-            b = a + rot / 2;
+            b = a + 64;
+            on_a = a < rot;
+            on_b = b < rot;
         } else {
-            a = 16 * j;                  // neighbours, and what lies behind rot
-            b = a + 8;
+            on_a = on_b = j < r16;
+            a = on_a ? 8 * j : rot + 8 * (j - r16);
+            b = a + (on_a ? 8 * r16 : 8 * (8 - r16));
         }
     }
     __device__ __forceinline__ void angles(const float *inv_freq, int j, int pos, float scale)
     {
-        if (!on)
+        if (!on_a)                       // (then not on_b either)
             return;
-        const float4 f0 = *reinterpret_cast<const float4 *>(inv_freq + 8 * j);
-        const float4 f1 = *reinterpret_cast<const float4 *>(inv_freq + 8 * j + 4);
+        const float4 f0 = *reinterpret_cast<const float4 *>(inv_freq + (pairs_next ? 4 : 8) * j);
+        const float4 f1 = pairs_next && !on_b ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                              : *reinterpret_cast<const float4 *>(inv_freq + (pairs_next ? 4 * j + 32 : 8 * j + 4));
         const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -102,21 +107,24 @@ struct Rotation {
             sn[i] = bad ? __uint_as_float(0x7fc00000u) : sn[i] * scale;
         }
     }
+    // Neighbours of one run by four of the angles.
+    __device__ __forceinline__ void turn_next(float (&u)[8], int k) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = u[2 * i], y = u[2 * i + 1];
+            u[2 * i] = fmaf(x, cs[i + k], -(y * sn[i + k]));
+            u[2 * i + 1] = fmaf(y, cs[i + k], x * sn[i + k]);
+        }
+    }
     __device__ __forceinline__ void turn(float (&u)[8], float (&v)[8]) const
     {
-        if (!on)
-            return;
         if (pairs_next) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float x = u[2 * i], y = u[2 * i + 1];
-                u[2 * i] = fmaf(x, cs[i], -(y * sn[i]));
-                u[2 * i + 1] = fmaf(y, cs[i], x * sn[i]);
-                const float z = v[2 * i], w = v[2 * i + 1];
-                v[2 * i] = fmaf(z, cs[i + 4], -(w * sn[i + 4]));
-                v[2 * i + 1] = fmaf(w, cs[i + 4], z * sn[i + 4]);
-            }
-        } else {
+            if (on_a)
+                turn_next(u, 0);
+            if (on_b)
+                turn_next(v, 4);
+        } else if (on_a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float x = u[i], y = v[i];
@@ -148,13 +156,14 @@ __device__ __forceinline__ void rope_rows(const __nv_bfloat16 *src, __nv_bfloat1
 #pragma unroll
         for (int k = 0; k < kRopeHeads; ++k)
             if (h + k < h1) {
-                if (r.on) {
+                if (r.on_a) {
                     float u[8], v[8];
                     unpack8(raw[k][0], u);
                     unpack8(raw[k][1], v);
                     r.turn(u, v);
                     raw[k][0] = pack8(u);
-                    raw[k][1] = pack8(v);
+                    if (r.on_b)          // (what only moves keeps its bits)
+                        raw[k][1] = pack8(v);
                 }
                 *reinterpret_cast<uint4 *>(dst + (h + k) * d_sh + r.a) = raw[k][0];
                 *reinterpret_cast<uint4 *>(dst + (h + k) * d_sh + r.b) = raw[k][1];
