@@ -183,9 +183,15 @@ __device__ __forceinline__ int rope_row(const RopeArgs &a, int b, int i)
     return -1;
 }
 
+// Threads that an SM holds at least, by the registers of one.  With what they need (88 to 90) CTAs of 512
+// threads are alone on an SM: 64 registers (a few spilled) for them, 80 for the smaller ones took a 32K
+// prefill from 162 us (blocks of 64), 148 (of 32), 131 (of 16) to 143, 124, 122.  (bf16: 121 with 88, 128 with 80.)
+template <int SB, int FMT>
+constexpr int kRopeResident = FMT == EA_CACHE_BF16 ? 1 : (SB <= 32 ? 768 : 1024) / (SB * kRopeRowThreads);
+
 // SB: tokens of a CTA (an 8-bit cache's scale block).
 template <int SB, int FMT>
-__global__ void __launch_bounds__(SB * kRopeRowThreads) rope_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(SB * kRopeRowThreads, kRopeResident<SB, FMT>) rope_kernel(const RopeArgs a)
 {
     constexpr bool kQuant = FMT != EA_CACHE_BF16, kE4M3 = FMT == EA_CACHE_E4M3;
     constexpr int kWarps = SB * kRopeRowThreads / 32;
@@ -368,6 +374,21 @@ static bool rope_freq(const float *inv_freq, int rot)
 // fill the GPU about four times over.
 static ea_status rope_launch(RopeArgs &a, int B, int SB, cudaStream_t st)
 {
+    // Many queries beside large scale blocks go first and alone, in CTAs of 16 tokens (a 32K prefill into
+    // blocks of 64: 131 us in two launches, 143 in one; one token: 7.4 in two, 3.7 in one).
+    if (a.has_cache && a.c.format != EA_CACHE_BF16 && SB >= 64 &&
+        ceil_div(a.T, 16) * ceil_div(a.heads[0], 8) * B >= 4 * 152) {
+        RopeArgs q = a;
+        q.c.format = EA_CACHE_BF16;
+        q.heads[1] = 0;
+        q.blocks[0] = static_cast<int>(ceil_div(a.T, 16));
+        q.blocks[1] = 0;
+        a.heads[0] = 0;
+        a.blocks[0] = 0;
+        const ea_status s = rope_launch(q, B, 16, st);
+        if (s != EA_OK)
+            return s;
+    }
     const int tensors = 1 + (a.has_cache ? 1 : 0);       // K (and V)
     int per = 8;
     auto ctas = [&](int p) {

@@ -216,6 +216,28 @@ def test_append_positions_apart_from_rows(dev, dtype, sb, page):
     check_append(dev, dtype, sb, page, 2, 30, [64, 90], [30, 11], positions=pos, Hq=4)
 
 
+@pytest.mark.parametrize("dtype,sb", [(E4M3, 64), (INT8, 128), (INT8, 32)])
+def test_append_long_with_queries(dev, dtype, sb):
+    """Many queries beside an 8-bit cache: the bits of the rotation alone and of the append alone."""
+    B, T, Hq, Hkv, cap = 2, 2500, 16, 2, 2816
+    Q, K, V = (tokens((B, T, h, 128), 20 + i).to(dev) for i, h in enumerate((Hq, Hkv, Hkv)))
+    f = torch.from_numpy(inv_freq(128)).to(dev)
+    start, n = (torch.tensor(v, dtype=torch.int32, device=dev) for v in ([0, 77], [2500, 2311]))
+    pos = start[:, None] + torch.arange(T, dtype=torch.int32, device=dev)
+    a, b = (ea.kv_cache(B, cap, Hkv, dtype=dtype, scale_block=sb, device=dev) for _ in range(2))
+    out, alone = (torch.full(Q.shape, KEEP, dtype=BF16, device=dev) for _ in range(2))
+    ws = ea.cache_workspace(dev)
+    ea.ea_cache_write_rope(a, K, V, f, Q=Q, Q_out=out, start=start, n_new=n, workspace=ws)
+    ea.ea_cache_write_rope(b, K, V, f, start=start, n_new=n, workspace=ws)
+    ea.ea_rope(Q, None, pos, f, n_new=n, Q_out=alone, workspace=ws)
+    check_no_device_error(ws)
+    assert torch.equal(out.view(torch.int16), alone.view(torch.int16))
+    assert (out[1, 2311:].float() == KEEP).all()
+    for x, y in ((a.K, b.K), (a.V, b.V)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert torch.equal(a.k_scale, b.k_scale) and torch.equal(a.v_scale, b.v_scale)
+
+
 def test_append_equals_rope_then_write(dev):
     """A bf16 cache holds the bits that ea_rope gives."""
     B, T, Hkv = 2, 20, 4
