@@ -12,11 +12,13 @@
 //
 // A row of a head is 8 threads.  Each holds two runs of 8 dims: both sides of eight
 // pairs, or (behind `rot`, and V) dims that only move.  A thread keeps its token's
-// eight angles in registers over all the heads of its CTA, so that the angles cost
-// some 10 % of the instructions of 8 heads.  A CTA takes one block of tokens: for an
-// 8-bit cache that is a scale block, whose largest rotated value sets the scale before
-// the same registers are rounded and stored.  The keys are rounded once, from fp32: a
-// key rotated, rounded to bf16 and then quantised would carry two errors.
+// eight angles in registers over up to eight heads, where they cost some 10 % of the
+// instructions.  Where rows stay bf16 a CTA has 16 tokens, or fewer and more heads; for an
+// 8-bit cache it has what is new to one scale block, whose largest rotated value sets the
+// scale before the same registers are rounded and stored.  The keys are rounded once, from
+// fp32: a key rotated, rounded to bf16 and then quantised would carry two errors.
+// (One token of 64 sequences into blocks of 64: 5.4 us; in CTAs of the block's 64 rows,
+// and a head group of Q each, 14.4.)
 //
 // Only data moves, so HBM bounds long inputs (a 32K prefill into bf16 pages, 805 MB: 122 us,
 // 0.97 of the measured copy rate; two chunks of 8K, Q and K alone: 55 us, 0.89), and the launch and
@@ -29,7 +31,6 @@
 namespace ea {
 
 constexpr int kRopeRowThreads = 8;
-constexpr int kRopeHeads = 4;            // heads whose loads a thread has in flight (bf16 rows)
 
 struct RopeArgs {
     CacheDev c;                          // where has_cache
@@ -42,7 +43,8 @@ struct RopeArgs {
     uint32_t *err;
     float scale;
     int T, heads[2];                     // Q, K
-    int per[2], groups[2], blocks[2];    // heads of a CTA, CTAs along the heads, blocks of tokens
+    int per[2], groups[2], blocks[2];    // heads of a thread, CTAs along the heads, blocks of tokens
+    int log2tb;                          // tokens of a CTA where rows stay bf16: few leave room for more heads
     int rot, interleaved, has_cache;
 };
 
@@ -141,20 +143,21 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
                       pack_bf16x2(x[6], x[7]));
 }
 
-// Rows that stay bf16: heads [h0, h1) of one token.
+// Rows that stay bf16: heads [h0, h1) of one token, the loads of N in flight.
+template <int N>
 __device__ __forceinline__ void rope_rows(const __nv_bfloat16 *src, __nv_bfloat16 *dst, int64_t s_sh, int64_t d_sh,
                                           int h0, int h1, const Rotation &r)
 {
-    for (int h = h0; h < h1; h += kRopeHeads) {
-        uint4 raw[kRopeHeads][2];
+    for (int h = h0; h < h1; h += N) {
+        uint4 raw[N][2];
 #pragma unroll
-        for (int k = 0; k < kRopeHeads; ++k)
+        for (int k = 0; k < N; ++k)
             if (h + k < h1) {
                 raw[k][0] = src ? *reinterpret_cast<const uint4 *>(src + (h + k) * s_sh + r.a) : make_uint4(0u, 0u, 0u, 0u);
                 raw[k][1] = src ? *reinterpret_cast<const uint4 *>(src + (h + k) * s_sh + r.b) : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
-        for (int k = 0; k < kRopeHeads; ++k)
+        for (int k = 0; k < N; ++k)
             if (h + k < h1) {
                 if (r.on_a) {
                     float u[8], v[8];
@@ -186,15 +189,15 @@ __device__ __forceinline__ int rope_row(const RopeArgs &a, int b, int i)
 // Threads that an SM holds at least, by the registers of one.  With what they need (88 to 90) CTAs of 512
 // threads are alone on an SM: 64 registers (a few spilled) for them, 80 for the smaller ones took a 32K
 // prefill from 162 us (blocks of 64), 148 (of 32), 131 (of 16) to 143, 124, 122.  (bf16: 121 with 88, 128 with 80.)
-template <int SB, int FMT>
-constexpr int kRopeResident = FMT == EA_CACHE_BF16 ? 1 : (SB <= 32 ? 768 : 1024) / (SB * kRopeRowThreads);
+template <int R, int FMT>
+constexpr int kRopeResident = FMT == EA_CACHE_BF16 ? 1 : (R <= 32 ? 768 : 1024) / (R * kRopeRowThreads);
 
-// SB: tokens of a CTA (an 8-bit cache's scale block).
-template <int SB, int FMT>
-__global__ void __launch_bounds__(SB * kRopeRowThreads, kRopeResident<SB, FMT>) rope_kernel(const RopeArgs a)
+// R: rows of a CTA, as many as a scale block of an 8-bit cache has or as tokens come.
+template <int R, int FMT>
+__global__ void __launch_bounds__(R * kRopeRowThreads, kRopeResident<R, FMT>) rope_kernel(const RopeArgs a)
 {
     constexpr bool kQuant = FMT != EA_CACHE_BF16, kE4M3 = FMT == EA_CACHE_E4M3;
-    constexpr int kWarps = SB * kRopeRowThreads / 32;
+    constexpr int kWarps = R * kRopeRowThreads / 32;
     const int b = blockIdx.y;
     // CTAs: Q's blocks of tokens by groups of heads, then K's, then V's
     int x = blockIdx.x, what = 0;
@@ -208,7 +211,6 @@ __global__ void __launch_bounds__(SB * kRopeRowThreads, kRopeResident<SB, FMT>) 
     }
     const int kind = what ? 1 : 0;
     const int grp = x % a.groups[kind], blk = x / a.groups[kind];
-    const int h0 = grp * a.per[kind], h1 = min(h0 + a.per[kind], a.heads[kind]);
     const int start = a.start ? a.start[b] : 0, n = a.n_new ? a.n_new[b] : a.T;
     if (n < 0 || n > a.T || (a.has_cache && (start < 0 || static_cast<int64_t>(start) + n > a.c.cap))) {
         if (threadIdx.x == 0 && blockIdx.x == 0)
@@ -216,16 +218,18 @@ __global__ void __launch_bounds__(SB * kRopeRowThreads, kRopeResident<SB, FMT>) 
         return;
     }
     const int r = threadIdx.x / kRopeRowThreads, j = threadIdx.x % kRopeRowThreads;
-    const bool cached = what && a.has_cache;
+    const bool cached = what && a.has_cache, rows = !kQuant || !cached;
+    const int h0 = (rows ? grp * (R >> a.log2tb) + (r >> a.log2tb) : grp) * a.per[kind];
+    const int h1 = min(h0 + a.per[kind], a.heads[kind]);
     Rotation rt;
     rt.place(j, what == 2 ? 0 : a.rot, a.interleaved);
     auto position = [&](int i, int t) {
         return a.positions ? (t >= 0 ? a.positions[static_cast<int64_t>(b) * a.T + t] : 0) : start + i;
     };
 
-    if (!kQuant || !cached) {
-        const int i = blk * SB + r;
-        if (i >= n)
+    if (rows) {
+        const int i = (blk << a.log2tb) + (r & ((1 << a.log2tb) - 1));
+        if (i >= n || h0 >= h1)
             return;
         const int t = what ? rope_row(a, b, i) : i;
         __nv_bfloat16 *dst;
@@ -241,28 +245,29 @@ __global__ void __launch_bounds__(SB * kRopeRowThreads, kRopeResident<SB, FMT>) 
             d_sh = a.oh[what];
         }
         rt.angles(a.inv_freq, j, position(i, t), a.scale);
-        rope_rows(t >= 0 ? a.x[what] + b * a.sb[what] + t * a.st[what] : nullptr, dst, a.sh[what], d_sh, h0, h1, rt);
+        // (two where few registers are left, see kRopeResident; four else: a 32K prefill takes 143 us with two)
+        rope_rows<kQuant && R >= 64 ? 2 : 4>(t >= 0 ? a.x[what] + b * a.sb[what] + t * a.st[what] : nullptr, dst, a.sh[what], d_sh, h0, h1, rt);
         return;
     }
 
     if constexpr (kQuant) {
         __shared__ uint32_t red[2][32];
-        const int p0 = (start / SB + blk) * SB;          // the block's first row
-        const int lo = max(start, p0), hi = min(start + n, p0 + SB);
+        const int p0 = ((start >> a.c.log2sb) + blk) << a.c.log2sb;      // the block's first row
+        const int lo = max(start, p0), hi = min(start + n, p0 + (1 << a.c.log2sb));
         if (lo >= hi)
             return;
         int outer, row0;
         if (!locate(a.c, b, p0, outer, row0, a.err))
             return;
-        const int p = p0 + r;
-        const bool fresh = p >= lo && p < hi, held = p < lo;
+        const int p = lo + r;                            // (no more than R tokens are new to a block)
+        const bool fresh = p < hi;
         const int t = fresh ? rope_row(a, b, p - start) : -1;
         const __nv_bfloat16 *src = a.x[what] + b * a.sb[what] + (t >= 0 ? t : 0) * a.st[what];
         if (fresh)
             rt.angles(a.inv_freq, j, position(p - start, t), a.scale);
         uint8_t *dst = static_cast<uint8_t *>(a.c.code[what - 1]) + outer * a.c.s_outer +
-                       (row0 + r) * a.c.s_row;
-        float *sp = a.c.scale[what - 1] + static_cast<int64_t>(outer) * a.c.Hkv * a.c.nsb + row0 / SB;
+                       row0 * a.c.s_row;
+        float *sp = a.c.scale[what - 1] + static_cast<int64_t>(outer) * a.c.Hkv * a.c.nsb + (row0 >> a.c.log2sb);
         uint4 next[2];
         float was_next = 0.f;
         auto load = [&](int h) {
@@ -297,16 +302,18 @@ __global__ void __launch_bounds__(SB * kRopeRowThreads, kRopeResident<SB, FMT>) 
                 // the block already holds rows p0 .. lo - 1
                 if (!(was <= s)) {
                     s = isnan(s) ? s : was;              // larger, or NaN: it stays
-                } else if (was < s && held) {
+                } else if (was < s) {
                     const __half2 f = __float2half2_rn(was / s);      // below 1
+#pragma unroll 1
+                    for (int q = p0 + r; q < lo; q += R)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint2 *w = reinterpret_cast<uint2 *>(at + 8 * (2 * j + k));
-                        uint32_t c[4];
-                        codes_f16<kE4M3>(w->x, c[0], c[1]);
-                        codes_f16<kE4M3>(w->y, c[2], c[3]);
-                        *w = make_uint2(encode4_f16<kE4M3>(c[0], c[1], f), encode4_f16<kE4M3>(c[2], c[3], f));
-                    }
+                        for (int k = 0; k < 2; ++k) {
+                            uint2 *w = reinterpret_cast<uint2 *>(at + (q - p0) * a.c.s_row + 8 * (2 * j + k));
+                            uint32_t c[4];
+                            codes_f16<kE4M3>(w->x, c[0], c[1]);
+                            codes_f16<kE4M3>(w->y, c[2], c[3]);
+                            *w = make_uint2(encode4_f16<kE4M3>(c[0], c[1], f), encode4_f16<kE4M3>(c[2], c[3], f));
+                        }
                 }
             }
             if (threadIdx.x == 0)
@@ -321,6 +328,7 @@ __global__ void __launch_bounds__(SB * kRopeRowThreads, kRopeResident<SB, FMT>) 
                     w1 = make_uint2(encode4<kE4M3>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
                                     encode4<kE4M3>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
                 }
+                at += (p - p0) * a.c.s_row;
                 *reinterpret_cast<uint2 *>(at + rt.a) = w0;
                 *reinterpret_cast<uint2 *>(at + rt.b) = w1;
             }
@@ -329,13 +337,13 @@ __global__ void __launch_bounds__(SB * kRopeRowThreads, kRopeResident<SB, FMT>) 
 }
 
 // ------------------------------------------------------------ launches
-template <int SB>
+template <int R>
 static void launch_rope_q8(const RopeArgs &a, dim3 grid, cudaStream_t st)
 {
     if (a.c.format == EA_CACHE_E4M3)
-        rope_kernel<SB, EA_CACHE_E4M3><<<grid, SB * kRopeRowThreads, 0, st>>>(a);
+        rope_kernel<R, EA_CACHE_E4M3><<<grid, R * kRopeRowThreads, 0, st>>>(a);
     else
-        rope_kernel<SB, EA_CACHE_INT8><<<grid, SB * kRopeRowThreads, 0, st>>>(a);
+        rope_kernel<R, EA_CACHE_INT8><<<grid, R * kRopeRowThreads, 0, st>>>(a);
 }
 
 static bool rope_tensor(const void *p, const int64_t *str)
@@ -370,50 +378,60 @@ static bool rope_freq(const float *inv_freq, int rot)
            rot % 16 == 0;
 }
 
-// Heads of a CTA: up to 8 share a thread's angles, fewer while the CTAs would not
-// fill the GPU about four times over.
-static ea_status rope_launch(RopeArgs &a, int B, int SB, cudaStream_t st)
+// A launch of CTAs of R rows.  A thread's angles serve up to 8 heads, fewer while the threads
+// would not fill half of the GPU.  An 8-bit cache's heads follow one another, a barrier each: as few
+// of them in a CTA as one wave of CTAs allows (32 accepted paths, e4m3, blocks of 64: 8.0 us with four heads,
+// 9.3 with one in three waves).
+static ea_status rope_launch(RopeArgs &a, int B, int R, cudaStream_t st)
 {
+    const bool wide = !a.has_cache || a.c.format == EA_CACHE_BF16;
     // Many queries beside large scale blocks go first and alone, in CTAs of 16 tokens (a 32K prefill into
     // blocks of 64: 131 us in two launches, 143 in one; one token: 7.4 in two, 3.7 in one).
-    if (a.has_cache && a.c.format != EA_CACHE_BF16 && SB >= 64 &&
-        ceil_div(a.T, 16) * ceil_div(a.heads[0], 8) * B >= 4 * 152) {
+    if (!wide && R >= 64 && ceil_div(a.T, 16) * ceil_div(a.heads[0], 8) * B >= 4 * 152) {
         RopeArgs q = a;
         q.c.format = EA_CACHE_BF16;
         q.heads[1] = 0;
-        q.blocks[0] = static_cast<int>(ceil_div(a.T, 16));
-        q.blocks[1] = 0;
         a.heads[0] = 0;
-        a.blocks[0] = 0;
         const ea_status s = rope_launch(q, B, 16, st);
         if (s != EA_OK)
             return s;
     }
-    const int tensors = 1 + (a.has_cache ? 1 : 0);       // K (and V)
+    const int tensors = a.has_cache ? 2 : 1;             // K (and V)
+    while ((R >> (a.log2tb + 1)) > 0 && (1 << a.log2tb) < a.T)
+        ++a.log2tb;
+    const int sub = R >> a.log2tb;
+    auto rows = [&](int k, int p) { return static_cast<int64_t>(a.T) * ceil_div(a.heads[k], p) * B; };
     int per = 8;
-    auto ctas = [&](int p) {
-        return static_cast<int64_t>(a.blocks[0]) * ceil_div(a.heads[0], p) +
-               static_cast<int64_t>(a.blocks[1]) * ceil_div(a.heads[1], p) * tensors;
-    };
-    while (per > 1 && ctas(per) * B < 4 * 152)
+    while (per > 1 && rows(0, per) + rows(1, per) * tensors < 64 * 152)
         per /= 2;
-    for (int k = 0; k < 2; ++k) {
-        a.per[k] = per;
-        a.groups[k] = static_cast<int>(ceil_div(a.heads[k], per));
-        if (a.groups[k] == 0)
-            a.groups[k] = 1;
+    a.per[0] = a.per[1] = per;
+    a.blocks[0] = a.heads[0] > 0 ? static_cast<int>(ceil_div(a.T, int64_t(1) << a.log2tb)) : 0;
+    a.groups[0] = a.heads[0] > 0 ? static_cast<int>(ceil_div(a.heads[0], per * sub)) : 1;
+    a.blocks[1] = a.heads[1] > 0 ? static_cast<int>(ceil_div(a.T, int64_t(1) << a.log2tb)) : 0;
+    a.groups[1] = a.heads[1] > 0 ? static_cast<int>(ceil_div(a.heads[1], per * sub)) : 1;
+    if (!wide) {
+        // new tokens of any length start at any row of a scale block
+        const int sb = 1 << a.c.log2sb;
+        a.blocks[1] = static_cast<int>((static_cast<int64_t>(a.T) + 2 * sb - 2) / sb);
+        const int64_t wave = 152 * (R <= 32 ? 768 : 1024) / (R * kRopeRowThreads);
+        per = 1;
+        while (per < 8 && a.blocks[1] * ceil_div(a.heads[1], per) * tensors * B > wave)
+            per *= 2;
+        a.per[1] = per;
+        a.groups[1] = static_cast<int>(ceil_div(a.heads[1], per));
     }
-    const int64_t gx = ctas(per);
+    const int64_t gx = static_cast<int64_t>(a.blocks[0]) * a.groups[0] +
+                       static_cast<int64_t>(a.blocks[1]) * a.groups[1] * tensors;
     if (gx >= (int64_t(1) << 31) || B > 65535)
         return EA_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(B));
-    if (!a.has_cache || a.c.format == EA_CACHE_BF16)
+    if (wide)
         rope_kernel<16, EA_CACHE_BF16><<<grid, 16 * kRopeRowThreads, 0, st>>>(a);
-    else if (SB == 16)
+    else if (R == 16)
         launch_rope_q8<16>(a, grid, st);
-    else if (SB == 32)
+    else if (R == 32)
         launch_rope_q8<32>(a, grid, st);
-    else if (SB == 64)
+    else if (R == 64)
         launch_rope_q8<64>(a, grid, st);
     else
         launch_rope_q8<128>(a, grid, st);
@@ -461,8 +479,6 @@ extern "C" ea_status ea_rope(const void *Q, void *Q_out, const int64_t q_str[4],
     a.T = T;
     a.heads[0] = Hq;
     a.heads[1] = Hkv;
-    a.blocks[0] = Hq > 0 ? static_cast<int>(ceil_div(T, 16)) : 0;
-    a.blocks[1] = Hkv > 0 ? static_cast<int>(ceil_div(T, 16)) : 0;
     a.rot = rot;
     a.interleaved = interleaved != 0;
     return rope_launch(a, B, 16, static_cast<cudaStream_t>(stream));
@@ -489,7 +505,8 @@ extern "C" ea_status ea_cache_write_rope(const ea_cache *c, const void *K_new, c
     if (!rope_ws_ok(workspace, ws_bytes))
         return EA_ERR_WORKSPACE;
     const bool wide = c->format == EA_CACHE_BF16;
-    const int sb = wide ? 16 : 1 << a.c.log2sb;
+    // 16 tokens at most (a decode step's, a path's) take CTAs of 16 rows whatever the block
+    const int R = wide || T <= 16 ? 16 : 1 << a.c.log2sb;
     rope_input(a, 1, K_new, n_str);
     rope_input(a, 2, V_new, n_str);
     if (Hq > 0) {
@@ -506,11 +523,8 @@ extern "C" ea_status ea_cache_write_rope(const ea_cache *c, const void *K_new, c
     a.T = T;
     a.heads[0] = Hq;
     a.heads[1] = a.c.Hkv;
-    a.blocks[0] = Hq > 0 ? static_cast<int>(ceil_div(T, sb)) : 0;
-    // new tokens of any length start at any row of a scale block
-    a.blocks[1] = static_cast<int>(wide ? ceil_div(T, sb) : (static_cast<int64_t>(T) + 2 * sb - 2) / sb);
     a.rot = rot;
     a.interleaved = interleaved != 0;
     a.has_cache = 1;
-    return rope_launch(a, B, sb, static_cast<cudaStream_t>(stream));
+    return rope_launch(a, B, R, static_cast<cudaStream_t>(stream));
 }

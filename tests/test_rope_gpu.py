@@ -216,6 +216,13 @@ def test_append_positions_apart_from_rows(dev, dtype, sb, page):
     check_append(dev, dtype, sb, page, 2, 30, [64, 90], [30, 11], positions=pos, Hq=4)
 
 
+@pytest.mark.parametrize("dtype,sb,page", [(E4M3, 64, 0), (INT8, 128, 128), (E4M3, 32, 64), (BF16, 64, 64)])
+def test_append_few_tokens_into_begun_blocks(dev, dtype, sb, page):
+    # up to 16: whole blocks of rows before them, a block's end among them, none
+    check_append(dev, dtype, sb, page, 3, 16, [0, 37, 120, 127, 250, 63], [16, 16, 16, 1, 11, 0], Hq=40, seed=30)
+    check_append(dev, dtype, sb, page, 9, 3, [126, 31, 64], [3, 2, 3], Hq=18, seed=31)
+
+
 @pytest.mark.parametrize("dtype,sb", [(E4M3, 64), (INT8, 128), (INT8, 32)])
 def test_append_long_with_queries(dev, dtype, sb):
     """Many queries beside an 8-bit cache: the bits of the rotation alone and of the append alone."""
