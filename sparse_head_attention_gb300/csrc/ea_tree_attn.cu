@@ -1005,9 +1005,10 @@ __device__ __forceinline__ void tree_keep(const TreeArgs &a, const TreeSeg &s, c
             if (ssa || blk)
                 for (uint32_t left = k; left; left &= left - 1) {
                     const int j = 32 * c + __ffs(left) - 1;
-                    const int dj = a.depth[static_cast<int64_t>(s.b) * a.T + j], pos = s.L + dj;
-                    const bool in = ssa ? pos < a.sink || d - dj < a.window
-                                        : dj >= 0 && pos / EA_TILE < a.nBm && a.block_mask[mrow * a.nBm + pos / EA_TILE] != 0;
+                    // the nearest valid depth, as for the node itself: the position stays below L + n, the block
+                    // below nBm (tree_unit)
+                    const int dj = min(max(a.depth[static_cast<int64_t>(s.b) * a.T + j], 0), s.n - 1), pos = s.L + dj;
+                    const bool in = ssa ? pos < a.sink || d - dj < a.window : a.block_mask[mrow * a.nBm + pos / EA_TILE] != 0;
                     if (!in)
                         k &= ~(left & (0u - left));
                 }

@@ -1,0 +1,154 @@
+"""Attention of a tree of drafted tokens where its arithmetic or its bounds can go wrong:
+depths out of range, drafted values of zero, values of any size in places that a row
+does not keep, few kept keys, the widest windows."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_head_attention_gb300 as ea
+from cache_reference import logical, make_cache, tokens, value_scales, write_ref
+from gpu_helpers import bf16_half_ulp, check_no_device_error, gpu_device
+from test_tree_attn_gpu import KEEP, handle, i32, inputs, out
+from tree_reference import plan, random_tree
+
+pytestmark = pytest.mark.gpu
+E4M3, INT8, BF16 = torch.float8_e4m3fn, torch.int8, torch.bfloat16
+FULL, SSA, BLOCK = ea.FULL, ea.SSA, ea.BLOCK
+SCALE = 128 ** -0.5
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return gpu_device()
+
+
+def unit(x):
+    """What a drafted row's f16 numbers of an 8-bit cache's step stand for: the power of two that puts the row's largest
+    finite magnitude into [2^14, 2^15), that magnitude taken as 2^-64 at least.  x float64 [..., 128]."""
+    top = np.where(np.isfinite(x), np.abs(x), 0.0).max(-1)
+    return 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(top, 2.0 ** -126))), -64) - 14)
+
+
+def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, bm=None, vscale=None, few=False):
+    """The operator in 64 bits, over the keys that a row keeps alone, and how far it may be off:
+      logits: 2^-17 of sum |q k| (128 fp32 terms), and 2^-17 for the exponent's multiply-add and exponential; over 8 bits q's
+      elements are f16, off by 2^-36 of their row's largest, and a drafted key's by 2^-39 of its own row's;
+      probabilities: bf16, half a step 2^-8; `few`: in two parts, 2^-16; f16 (8-bit caches) 2^-11, and 2^-25 where below
+      2^-14, in units of 2^-7 of the largest kept weight times unit (vscale: of the cache's V): at most
+      2^-32 max(u) sum |v| / u, u the units of the kept keys alone; a drafted value 2^-39 of its own row's largest, or
+      2^-103 (half of f16's least step at the smallest unit);
+      sums and joins: 2^-16.
+    The output's own rounding, half a bf16 step, is left to the caller."""
+    B, T, Hq, D = Q.shape
+    Hkv = K.shape[2]
+    g = Hq // Hkv
+    O, LSE = np.zeros((B, T, Hq, D)), np.full((B, Hq, T), -np.inf)
+    tO, tL = np.zeros((B, T, Hq, D)), np.zeros((B, Hq, T))
+    for b in range(B):
+        L, nb = lens[b], n[b]
+        pos = L + depth[b, :nb].astype(np.int64)
+        at = np.concatenate([np.arange(L), pos])
+        up = ((mask[b, :nb].view(np.uint32)[:, :, None] >> np.arange(32, dtype=np.uint32)) & 1).reshape(nb, 128)[:, :nb].astype(bool)
+        for h in range(Hkv):
+            k, v = np.concatenate([Kc[b, :L, h], K[b, :nb, h]]), np.concatenate([Vc[b, :L, h], V[b, :nb, h]])
+            keep = np.concatenate([np.ones((nb, L), bool), up], 1)
+            if modes[b][h] == SSA:
+                keep &= (at[None] < sink) | (pos[:, None] - at[None] < window)
+            elif modes[b][h] == BLOCK:
+                keep &= bm[b, h][pos // 128][:, at // 128] != 0
+            for t in range(nb):
+                j = np.flatnonzero(keep[t])
+                if not len(j):
+                    continue
+                q, hs = Q[b, t, h * g : (h + 1) * g], slice(h * g, (h + 1) * g)
+                x = q @ k[j].T * SCALE
+                e = (np.abs(q) @ np.abs(k[j]).T * SCALE).max(1) * 2.0 ** -17 + 2.0 ** -17
+                if vscale is not None:
+                    own = j[j >= L]
+                    e += 2.0 ** -36 * np.abs(q).max(1) * np.abs(k[j]).sum(1).max() * SCALE
+                    if len(own):
+                        e += 2.0 ** -39 * np.abs(q).sum(1) * np.maximum(np.abs(k[own]).max(), 2.0 ** -64) * SCALE
+                top = x.max(1, keepdims=True)
+                p = np.exp(x - top)
+                s = p.sum(1, keepdims=True)
+                p /= s
+                O[b, t, hs], LSE[b, hs, t] = p @ v[j], (top + np.log(s))[:, 0]
+                part = 2.0 ** -11 if vscale is not None else 2.0 ** -16 if few else 2.0 ** -8
+                tO[b, t, hs] = (p @ np.abs(v[j])) * (part + 2.0 ** -16 + 2 * e[:, None])
+                if vscale is not None:
+                    u = np.concatenate([vscale[b, :L, h] / 64, unit(v[L:])])[j]
+                    tO[b, t, hs] += 2.0 ** -32 * u.max() * (np.abs(v[j]) / u[:, None]).sum(0)
+                    if len(own):
+                        tO[b, t, hs] += 2.0 ** -39 * np.maximum(np.abs(v[own]).max(), 2.0 ** -64)
+                tL[b, hs, t] = e + np.abs(LSE[b, hs, t]) * 2.0 ** -20
+    return O, LSE, tO, tL
+
+
+def check(dev, c, Q, K, V, lens, n, parents, modes, sink=16, window=100, bm=None, few=False, rows=None):
+    """One call against the above; rows: the (sequence, node) pairs that are compared (all)."""
+    B, T, Hq, _ = Q.shape
+    depth, mask = plan(parents, n)
+    q8 = c["ks"] is not None
+    ref = attend(*(x.double().numpy() for x in (Q, K, V)), *logical(c), lens, n, depth, mask, modes, sink, window, bm,
+                 value_scales(c) if q8 else None, few)
+    h = handle(c, dev)
+    ws = ea.tree_workspace(B, T, Hq, K.shape[2], h.capacity, device=dev)
+    O, LSE = out(B, T, Hq, dev)
+    ea.ea_hybrid_attn_tree(*(x.to(dev) for x in (Q, K, V)), h, i32(lens, dev), i32(depth, dev), i32(mask, dev),
+                           torch.tensor(modes, dtype=torch.uint8, device=dev), sink=sink, window=window, n_nodes=i32(n, dev),
+                           block_mask=None if bm is None else torch.as_tensor(bm).to(dev), O=O, LSE=LSE, workspace=ws)
+    check_no_device_error(ws)
+    O, LSE = O.float().cpu().numpy().astype(np.float64), LSE.cpu().numpy().astype(np.float64)
+    for b, t in rows or [(b, t) for b in range(B) for t in range(n[b])]:
+        o, l = O[b, t], LSE[b, :, t]
+        assert np.array_equal(np.isneginf(l), np.isneginf(ref[1][b, :, t])), (b, t, "empty rows")
+        some = ~np.isneginf(l)
+        bad = ~(np.abs(l - ref[1][b, :, t]) <= ref[3][b, :, t]) & some
+        assert not bad.any(), (b, t, "LSE", l[bad][:4], ref[1][b, :, t][bad][:4])
+        err = np.abs(o - ref[0][b, t])
+        bad = ~(err <= bf16_half_ulp(np.maximum(np.abs(o), np.abs(ref[0][b, t]))) + ref[2][b, t] + 2.0 ** -130)
+        assert not bad.any(), (b, t, "O", int(bad.sum()), o[bad][:4], ref[0][b, t][bad][:4], err[bad].max())
+
+
+def _depths(dev, mode, L, sink, window, bm, given, nearest):
+    """The call with the depths `given` reports them and equals the one with the nearest valid ones, whose error word is clear."""
+    B, T, Hq, Hkv = 1, 6, 4, 1
+    Q, K, V = (x.to(dev) for x in inputs(B, T, Hq, Hkv, 5))
+    _, mask = plan(random_tree(B, T, 0, "chain"), [T])
+    h = handle(make_cache(B, 512, Hkv, BF16, 64, 0, 7), dev)
+    ws = ea.tree_workspace(B, T, Hq, Hkv, 512, device=dev)
+    got = []
+    for d, status in ((given, 6), (nearest, 0)):
+        got.append(ea.ea_hybrid_attn_tree(Q, K, V, h, i32([L], dev), i32([d], dev), i32(mask, dev), torch.tensor([[mode]], dtype=torch.uint8, device=dev),
+                                          sink=sink, window=window, block_mask=None if bm is None else torch.as_tensor(bm).to(dev), workspace=ws))
+        assert ea.ea_check_errors(ws) == status
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def _block_rows():
+    bm = np.zeros((1, 1, 4, 4), np.uint8)
+    bm[0, 0, 1, 1] = bm[0, 0, 2, 2] = bm[0, 0, 2, 0] = 1
+    return bm
+
+
+def test_depths_just_outside_their_range(dev):
+    """An ancestor's depth counts as the nearest valid one, as a node's own does."""
+    # -1 would lie below the sink's end, 0 does not
+    _depths(dev, SSA, 100, 100, 2, None, [-1, 1, 2, 3, 4, 5], [0, 1, 2, 3, 4, 5])
+    _depths(dev, SSA, 100, 0, 2, None, [0, 1, 2, 3, 6, 5], [0, 1, 2, 3, 5, 5])
+    # positions 250 to 255: block 1, whose row keeps it; 256 would be in block 2
+    _depths(dev, BLOCK, 250, 0, 1, _block_rows(), [-1, 1, 2, 3, 4, 5], [0, 1, 2, 3, 4, 5])
+    _depths(dev, BLOCK, 250, 0, 1, _block_rows(), [0, 1, 6, 3, 4, 5], [0, 1, 5, 3, 4, 5])
+
+
+@pytest.mark.parametrize("far", [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 200, -1000000])
+def test_depths_far_outside_their_range(dev, far):
+    """No sum with such a depth leaves 32 bits, nor the block mask."""
+    near = 5 if far > 0 else 0
+    _depths(dev, SSA, 100, 100, 2, None, [0, far, 2, 3, 4, 5], [0, near, 2, 3, 4, 5])
+    _depths(dev, BLOCK, 250, 0, 1, _block_rows(), [0, far, 2, 3, 4, 5], [0, near, 2, 3, 4, 5])
+
+
