@@ -897,7 +897,8 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     top = max(top, static_cast<int>(sm.own_exp[own & 1][kv][i]));
-                const int e = min(14 + 127 - top, 120);
+                // (2^-64 at least, as a cache's scales: sums of weights over v's unit stay finite where V is zero)
+                const int e = min(14 + 127 - top, 14 + 64);
                 const float f = pow2f(e);
                 if (ct < rows)
 #pragma unroll 8

@@ -152,3 +152,20 @@ def test_depths_far_outside_their_range(dev, far):
     _depths(dev, BLOCK, 250, 0, 1, _block_rows(), [0, far, 2, 3, 4, 5], [0, near, 2, 3, 4, 5])
 
 
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+@pytest.mark.parametrize("value", [0.0, 2.0 ** -120, math.inf])
+def test_drafted_values_of_nothing(dev, dtype, value):
+    """One head's drafted values are all zero (or next to nothing, or, on a node that no other keeps, infinite): the sums stay
+    finite, over no cache, over a tile of it, and where a range of tiles begins or ends at the tree's own."""
+    T, Hq, Hkv = 6, 8, 2
+    p = np.array([[-1, 0, 1, 1, 0, 4]], np.int32)
+    for lens in ([0, 100], [128, 1], [20000, 20100], [20161, 20050], [3000, 2900]):
+        B = len(lens)
+        Q, K, V = inputs(B, T, Hq, Hkv, 3)
+        V[:, :, 1] = 0.0 if math.isinf(value) else value
+        if math.isinf(value):
+            V[:, 5, 1, 7] = value
+        rows = [(b, t) for b in range(B) for t in range(T) if not (math.isinf(value) and t == 5)]
+        check(dev, make_cache(B, max(lens) + 64, Hkv, dtype, 64, 0, 5), Q, K, V, lens, [T] * B, p.repeat(B, 0), [[FULL] * Hkv] * B, rows=rows)
+
+
