@@ -840,7 +840,11 @@ size_t ea_tree_workspace_size(int B, int T, int Hq, int Hkv, int d, int Lmax);
  * so that a node's output is the decode's on a cache that holds its path.
  * O[b][t][qh][:] = softmax(scale * q . k) V over the kept keys, LSE[b][qh][t] their
  * natural log-sum-exp; none kept: O = 0, LSE = -inf.  What a row does not keep never
- * reaches it, infinities and NaN among them.
+ * reaches it, infinities and NaN among them.  Over 8-bit caches the products are f16 times
+ * powers of two: an element of a query (of a drafted key or value) counts as zero below
+ * 2^-35 (2^-27) of its own row's largest; the numbers of a block of the smallest scale and
+ * of a drafted row below 2^-63 may count as zero.  128 keys whose scales (drafted rows whose
+ * largest elements) are more than 2^12 apart take some fifty times as long as others.
  *
  *   Q, O         device bf16 [B][T][Hq][d], strides q_str / o_str
  *   K, V         device bf16 [B][T][Hkv][d], strides kv_str (shared): the drafted

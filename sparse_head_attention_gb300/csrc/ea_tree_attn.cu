@@ -58,9 +58,10 @@ constexpr float kTGrow = 8.f;                         // the maximum is followed
 constexpr float kTShift = 7.f;                        // 8-bit caches: p is f16, at most 2^(7 + 8)
 constexpr int kTMinTiles = 2;                         // of a range at least (a power of two)
 constexpr int kTPartTiles = 4;                        // see tree_range
+constexpr int kTSpread = 12;                          // see tree_convert
 constexpr int kTSms = 152;                            // a workspace's size depends on the grid
 
-enum { kEdge = 1, kDraft = 2, kRow0 = 4, kRow1 = 8, kMixed = 16, kGroups = 8 };   // (from bit 8 on: 16-key groups)
+enum { kEdge = 1, kDraft = 2, kRow0 = 4, kRow1 = 8, kMixed = 16, kWide = 32, kGroups = 8 };   // (from bit 8 on: 16-key groups)
 
 struct TreeArgs {
     __nv_bfloat16 *O;
@@ -195,19 +196,22 @@ struct __align__(1024) TreeSmem {
     uint8_t q[TWO ? 2 : 1][kTBytes];
     uint8_t ring[kStages][kTBytes];
     uint8_t code[kCodes][Q8 ? kTBytes / 2 : 16];
-    float2 ml[2][kTTile];                // a warpgroup's maximum and sum of each row; before: the scan
+    float2 ml[Q8 ? 1 : 2][kTTile];       // a warpgroup's maximum and sum of each row; before: the scan
     uint64_t full[kStages], empty[kStages];
     uint64_t code_full[kCodes], code_empty[kCodes];
     uint64_t ready[kTReady];             // V has been looked over
     uint64_t seg_full[kTSegs], seg_empty[kTSegs];
     uint64_t q_full, q_empty;
     uint64_t s_full[2], p_full[2], o_done[2];
-    uint64_t seg_done, ml_full, o_free, drain;
+    uint64_t seg_done, ml_full[2], o_free, drain;
     uint64_t q_ready, own_full[2], own_max[2];   // 8-bit caches: Q in f16; the tree's K and V
     TreeSeg seg[kTSegs];
     TreeTile tile[kTInfos];
-    float k_unit[kTInfos], v_log[kTInfos];       // 8-bit caches: a tile's f16 numbers stand for k_unit, 2^v_log times them
-    uint8_t own_exp[2][2][4];
+    // 8-bit caches: a 16-key group's (K's, V's) and a drafted key's f16 numbers stand for 2^(unit - 127) times them (a
+    // group of the tree's own rows: 0 if those have units of their own)
+    alignas(16) uint8_t group_unit[Q8 ? kTInfos : 1][2][8];
+    uint8_t own_unit[Q8 ? kTSegs : 1][2][Q8 ? kTTile : 1];
+    uint8_t own_exp[2][2][2][4];         // the largest and the least exponent of a warp's drafted rows
     uint8_t odd[kTReady];                // V holds an infinity or a NaN
     TreeUnit unit;                       // this CTA's range: its first unit,
     int u, off, count;                   // where it starts in it, and its tiles
@@ -475,20 +479,43 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
             const int i = (t - s.t0) & 15;
             if (i == 0) {
                 const int tt = t + (lane >> 1);
+                uint32_t hi[2] = {0u, 0u}, lo[2] = {255u, 255u};
                 if (tt < s.t1) {
                     mine = tree_tile(a, x, u, tt);
                     if (!(mine.flags & kDraft)) {
                         tree_place(a, s.b, s.L, mine.key0 + 64 * (lane & 1), outer, row);
                         if (Q8 && row >= 0 && outer >= 0) {
-                            // their scales, which the converting warps will ask for
+                            // how far their scales are apart (and in L1 for the converting warps)
+                            const int64_t at = (static_cast<int64_t>(outer) * a.c.Hkv + s.h) * a.c.nsb;
+                            uint32_t w[2][4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int p = min(row + 16 * i, row + s.L - 1 - (mine.key0 + 64 * (lane & 1))) >> a.c.log2sb;
+#pragma unroll
+                                for (int kv = 0; kv < 2; ++kv)
+                                    w[kv][i] = __ldg(reinterpret_cast<const uint32_t *>(a.c.scale[kv]) + at + p);
+                            }
 #pragma unroll
                             for (int kv = 0; kv < 2; ++kv)
-                                asm volatile("prefetch.global.L1 [%0];" ::"l"(
-                                    a.c.scale[kv] + (static_cast<int64_t>(outer) * a.c.Hkv + s.h) * a.c.nsb + (row >> a.c.log2sb)));
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint32_t e = (w[kv][i] & 0x7fffffffu) >= 0x7f800000u ? 0u : w[kv][i] >> 23;
+                                    hi[kv] = max(hi[kv], e);
+                                    lo[kv] = e > 127u - 64u ? min(lo[kv], e) : lo[kv];
+                                }
                         }
                     }
                 }
                 __syncwarp();
+                if constexpr (Q8) {
+                    // (of both halves)
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t top = max(hi[kv], __shfl_xor_sync(0xffffffffu, hi[kv], 1)), low = min(lo[kv], __shfl_xor_sync(0xffffffffu, lo[kv], 1));
+                        if (top > low + kTSpread)
+                            mine.flags |= kWide;
+                    }
+                }
             }
             TreeTile ti;
             ti.key0 = __shfl_sync(0xffffffffu, mine.key0, 2 * i);
@@ -667,7 +694,7 @@ __device__ __forceinline__ void tree_pv(const TreeArgs &a, Smem &sm, uint32_t tm
                 break;
             ++cnt[w];
             tc_fence_after();
-            if (!(flags & kEdge)) {
+            if (!(flags & kEdge) && !odd) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     mma_ts(go, to, tp + 32 * (k >> 1) + 8 * (k & 1), vd + k * (2048 >> 4), kIdPV, k ? 1u : more);
@@ -745,6 +772,9 @@ __device__ __forceinline__ void tree_fix(const TreeMaps &tm, const TreeArgs &a, 
                 }
                 fence_proxy_async_smem();
             }
+            // (rows with units of their own are taken key by key too)
+            if (Smem::Q8)
+                odd |= (ti.flags & kWide) || sm.group_unit[tile % kTInfos][0][0] == 0 || sm.group_unit[tile % kTInfos][1][0] == 0;
             odd = __any_sync(0xffffffffu, odd);
             if (lane == 0) {
                 sm.odd[tile % kTReady] = odd;
@@ -764,11 +794,16 @@ __device__ __forceinline__ void tree_fix(const TreeMaps &tm, const TreeArgs &a, 
 }
 
 // ------------------------------------------------------------ 8-bit caches
-// A tile of codes becomes f16: a code times 2^(e - E + kTHead), e its block's exponent and E the
-// largest of the tile's, exact while a block's numbers are within 2^24 or so of the tile's largest
-// (smaller ones lose bits that the sums do not see).  The tile's numbers so stand for 2^(E - kTHead)
-// times them, one factor for all of it.  (As bf16, each block with its own scale, a code took four
-// integer operations, and the conversion was what bounded the kernel: 1170 us for 16 sequences of 64K.)
+// A tile of codes becomes f16.  Where its scales lie within 2^kTSpread of one another, a code times 2^(e - E + kTHead), e
+// its block's exponent and E the largest of the tile's, so that one factor, 2^(E - kTHead), says what the tile's numbers
+// stand for.  They are exact, and the softmax's weights, scaled to f16's upper end with the largest scale, lose kTSpread bits
+// of its lower end at most, whatever lies in the tile that a row does not keep.  Else a code times 2^kTHead, a unit each 16
+// keys, and the softmax takes the tile key by key.  (Units of 16 keys in every tile's softmax: 16 sequences of 64K, trees of 16,
+// e4m3 574 -> 630 us; a path of its own for such tiles beside it, which no other tile runs, 592.)  The smallest scale,
+// 2^-64, which a block of zeros has, counts for nothing: beside one above 2^-52 its numbers may become zero (as a drafted
+// row below 2^-63).
+// The tree's own rows, bf16, take one power of two, or, where their largest elements are further than 2^kTSpread apart, each
+// its own, and go key by key too.
 //   e4m3: two codes a conversion, then a multiplication
 //   int8: c + 128 in the fraction of 1024, then (1024 + c + 128) f - 1152 f
 template <bool E4M3>
@@ -868,7 +903,7 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
             const int st = entry % kStages, cs = codes % kCodes;
             uint8_t *dst = sm.ring[st];
             if (t == s.nt - 1) {
-                // the tree's own: from bf16, times one power of two that puts the largest below 2^15
+                // the tree's own: from bf16, a thread a row, times the power of two that puts its largest below 2^15
                 if (!mbar_wait_warp(&sm.empty[st], ((entry / kStages) & 1) ^ 1, &sm.abort, err)) {
                     ok = false;
                     break;
@@ -876,44 +911,50 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                 if (ct == 0)
                     tree_load_own(tm, dst, kv, s, &sm.own_full[kv]);
                 __syncwarp();
-                const bool got = mbar_wait_warp(&sm.own_full[kv], own & 1, &sm.abort, err);
-                const int rows = (s.n + 15) & ~15;
-                float mx = 0.f;
-                if (got && ct < s.n)
-#pragma unroll 8
-                    for (int c = 0; c < 16; ++c)
-                        mx = max_finite(*reinterpret_cast<const uint4 *>(dst + (c >> 3) * kTHalf + ct * 128 + (((c & 7) ^ (ct & 7)) << 4)), mx);
-                const int ex = __reduce_max_sync(0xffffffffu, exponent_of(mx));
-                if (lane == 0) {
-                    sm.own_exp[own & 1][kv][ct / 32] = static_cast<uint8_t>(ex);
-                    mbar_arrive(&sm.own_max[kv]);
-                }
-                __syncwarp();
-                if (!got || !mbar_wait_warp(&sm.own_max[kv], own & 1, &sm.abort, err)) {
+                if (!mbar_wait_warp(&sm.own_full[kv], own & 1, &sm.abort, err)) {
                     ok = false;
                     break;
                 }
-                int top = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top = max(top, static_cast<int>(sm.own_exp[own & 1][kv][i]));
-                // (2^-64 at least, as a cache's scales: sums of weights over v's unit stay finite where V is zero)
-                const int e = min(14 + 127 - top, 14 + 64);
-                const float f = pow2f(e);
-                if (ct < rows)
+                auto part = [&](int c) { return reinterpret_cast<uint4 *>(dst + (c >> 3) * kTHalf + ct * 128 + (((c & 7) ^ (ct & 7)) << 4)); };
+                float mx = 0.f;
+                if (ct < s.n)
 #pragma unroll 8
-                    for (int c = 0; c < 16; ++c) {
-                        uint4 *p = reinterpret_cast<uint4 *>(dst + (c >> 3) * kTHalf + ct * 128 + (((c & 7) ^ (ct & 7)) << 4));
-                        *p = bf16_to_f16(*p, f);
-                    }
-                if (ct == 0) {
-                    if (kv == 0) {
-                        sm.tile[tile % kTInfos] = tree_own_tile(s.L, s.n);
-                        sm.k_unit[tile % kTInfos] = pow2f(-e);
-                    } else {
-                        sm.v_log[tile % kTInfos] = static_cast<float>(-e);
-                    }
+                    for (int c = 0; c < 16; ++c)
+                        mx = max_finite(*part(c), mx);
+                // (a row's largest counts as 2^-64 at least, a cache's smallest scale: sums of weights over V's unit stay
+                // finite where V is zero)
+                const int ex = max(exponent_of(mx), 127 - 64);
+                const int hi = __reduce_max_sync(0xffffffffu, ct < s.n ? ex : 0), lo = __reduce_min_sync(0xffffffffu, ct < s.n && ex > 127 - 64 ? ex : 255);
+                if (lane == 0) {
+                    sm.own_exp[own & 1][kv][0][ct / 32] = static_cast<uint8_t>(hi);
+                    sm.own_exp[own & 1][kv][1][ct / 32] = static_cast<uint8_t>(lo);
+                    mbar_arrive(&sm.own_max[kv]);
                 }
+                __syncwarp();
+                if (!mbar_wait_warp(&sm.own_max[kv], own & 1, &sm.abort, err)) {
+                    ok = false;
+                    break;
+                }
+                int top = 0, low = 255;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    top = max(top, static_cast<int>(sm.own_exp[own & 1][kv][0][i]));
+                    low = min(low, static_cast<int>(sm.own_exp[own & 1][kv][1][i]));
+                }
+                const bool wide = top - low > kTSpread;
+                const int unit = (wide ? ex : top) - 14;
+                // (the slot's last user was the part three before, that all are through with)
+                sm.own_unit[it % kTSegs][kv][ct] = static_cast<uint8_t>(unit);
+                if (ct < 8)
+                    sm.group_unit[tile % kTInfos][kv][ct] = static_cast<uint8_t>(wide ? 0 : unit);
+                const float f = pow2f(127 - unit);
+                asm volatile("" ::: "memory");           // (read again, not kept)
+                if (ct < ((s.n + 15) & ~15))
+#pragma unroll 8
+                    for (int c = 0; c < 16; ++c)
+                        *part(c) = bf16_to_f16(*part(c), f);
+                if (ct == 0 && kv == 0)
+                    sm.tile[tile % kTInfos] = tree_own_tile(s.L, s.n);
                 ++own;
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -926,7 +967,7 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                 break;
             }
             const TreeTile &ti = sm.tile[tile % kTInfos];
-            uint32_t f = 0x7fc00000u;                  // a group's scale; NaN as well where there is none
+            uint32_t f = 0u;                           // a group's scale; none behind the end or outside the cache
             {
                 const int i = lane & 7, hf = i >> 2, outer = ti.outer[hf], row = ti.row[hf] + 16 * (i & 3);
                 if (lane < (kv ? 8 : 16) && outer >= 0 && ti.key0 + 16 * i < s.L)
@@ -934,25 +975,26 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                               (static_cast<int64_t>(outer) * a.c.Hkv + s.h) * a.c.nsb + (row >> a.c.log2sb));
             }
             const int groups = ti.flags >> kGroups;
-            const bool absent = ti.outer[lane >> 2 & 1] < 0;
             codes += 2;
-            // the exponents, and the largest of them (0: no scale but NaN)
-            const uint32_t e = (f & 0x7fffffffu) < 0x7f800000u ? f >> 23 : 0u;
-            const uint32_t E = __reduce_max_sync(0xffffffffu, lane < 8 ? e : 0u);
+            // the exponents (lanes 0 - 7, and V's in K's warps) and the largest
+            const bool nan = (f & 0x7fffffffu) >= 0x7f800000u;
+            const int e = nan ? 0 : static_cast<int>(f >> 23);
+            int E = __reduce_max_sync(0xffffffffu, lane < 8 ? e : 0);
+            const bool wide = (ti.flags & kWide) != 0;
+            const int x = max(wide ? 0 : e - E, -100) + kTHead<E4M3>;
             if (kv == 0) {
-                const uint32_t EV = __reduce_max_sync(0xffffffffu, lane >= 8 && lane < 16 ? e : 0u);
-                if (ct == 0) {
-                    sm.k_unit[tile % kTInfos] = pow2f((E ? static_cast<int>(E) - 127 : 0) - kTHead<E4M3>);
-                    sm.v_log[tile % kTInfos] = static_cast<float>((EV ? static_cast<int>(EV) - 127 : 0) - kTHead<E4M3>);
-                }
+                const int EV = __reduce_max_sync(0xffffffffu, lane >= 8 ? e : 0);
+                E = lane < 8 ? E : EV;
+                if (ct < 16)
+                    sm.group_unit[tile % kTInfos][ct >> 3][ct & 7] =
+                        static_cast<uint8_t>(max(wide ? e : E, 127 - 64) - kTHead<E4M3>);
             }
             // (a page outside the cache reads zeros, a block of a NaN scale NaN)
             uint32_t fg;
             {
-                const __half x = e ? __float2half_rn(pow2f(max(static_cast<int>(e) - static_cast<int>(E) + kTHead<E4M3>, -126)))
-                                   : absent ? __ushort_as_half(0) : __ushort_as_half(0x7e00);
-                fg = static_cast<uint32_t>(__half_as_ushort(x)) |
-                     static_cast<uint32_t>(__half_as_ushort(__hmul(x, __float2half_rn(-1152.f)))) << 16;
+                const __half h = nan ? __ushort_as_half(0x7e00) : __float2half_rn(e ? pow2f(x) : 0.f);
+                fg = static_cast<uint32_t>(__half_as_ushort(h)) |
+                     static_cast<uint32_t>(__half_as_ushort(__hmul(h, __float2half_rn(-1152.f)))) << 16;
             }
             if (!mbar_wait_warp(&sm.empty[st], ((entry / kStages) & 1) ^ 1, &sm.abort, err)) {
                 ok = false;
@@ -1038,6 +1080,24 @@ __device__ __forceinline__ void mask32(uint32_t (&x)[32], uint32_t keep)
 #pragma unroll
     for (int i = 0; i < 32; ++i)
         x[i] = (keep >> i) & 1u ? x[i] : 0xff800000u;
+}
+
+// 8-bit caches: a key's number in S to its logit (cs: what the row's queries stand for, and the call's scale), and
+// log2 of what its numbers of V stand for, + 127, which joins it: p = 2^(x unit + v + shift - m) is what multiplies those
+// numbers, and p times `inv`, shifted, the softmax's weight.  (Not zero: a masked -inf stays one.)
+__device__ __forceinline__ float key_unit(float cs, uint32_t u)
+{
+    return fmaxf(cs * __uint_as_float(u << 23), 1e-37f);
+}
+
+__device__ __forceinline__ float val_log(uint32_t u)
+{
+    return static_cast<float>(u);
+}
+
+__device__ __forceinline__ float val_inv(uint32_t u)
+{
+    return __uint_as_float((254u - u) << 23);
 }
 
 __device__ __forceinline__ float max32(const uint32_t (&x)[32], float m)
@@ -1162,30 +1222,24 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                 const int chunks = ((flags >> kGroups) + 1) / 2;     // of 32 columns, that hold keys
                 uint32_t keep[4];
                 bool odd = false;
-                if (edge) {
+                const bool wide = Smem::Q8 && (flags & kWide);
+                if (edge || wide) {
                     tree_keep(a, s, sm.tile[tile % kTInfos], d, up, keep);
-                    if (flags & kMixed) {
+                    if ((flags & kMixed) || wide) {
                         if (!mbar_wait_warp(&sm.ready[tile % kTReady], (tile / kTReady) & 1, &sm.abort, err))
                             return;
                         odd = sm.odd[tile % kTReady] != 0;
                     }
                 }
                 __syncwarp();
-                // p = 2^(unit x + dv - m): unit and dv hold what the tile's numbers of K and V stand for
-                float unit = a.scale_log2, dv = 0.f, iv = 1.f;
                 if constexpr (Smem::Q8) {
                     if (!have)
                         cs = sm.ml[0][r].x;
                     have = true;
-                    unit = fmaxf(cs * sm.k_unit[tile % kTInfos], 1e-37f);
-                    dv = sm.v_log[tile % kTInfos];
-                    iv = pow2f(-static_cast<int>(dv));
-                    dv += kTShift;
                 }
-                const uint64_t c2 = f2_pack(unit, unit);
+                const uint8_t (&units)[2][8] = sm.group_unit[Smem::Q8 ? tile % kTInfos : 0];
                 // (O's product of this warpgroup's step before is over: its S is issued behind that.)
-                auto grow = [&](float x) {
-                    const float mx = x == NEG_INF ? NEG_INF : fmaf(x, unit, Smem::Q8 ? dv - kTShift : 0.f);
+                auto grow = [&](float mx) {
                     const bool grew = mx > m + kTGrow;
                     if (__any_sync(0xffffffffu, grew)) {
                         const float f = grew && m != NEG_INF ? ex2(m - mx) : 1.f;
@@ -1208,8 +1262,10 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         }
                     }
                 };
-                if (Smem::Q8 && !edge) {
+                if (Smem::Q8 && !edge && !wide) {
                     // (few registers, and little code: see tree_convert)
+                    const uint32_t v0 = units[1][0];
+                    const float unit = key_unit(cs, units[0][0]), v = val_log(v0);
                     float mx = NEG_INF;
 #pragma unroll 1
                     for (int c = 0; c < 4; c += 2) {
@@ -1221,9 +1277,9 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         tie32(x[1]);
                         mx = max32(x[1], max32(x[0], mx));
                     }
-                    grow(mx);
-                    const float db = dv - (m == NEG_INF ? 0.f : m);
-                    const uint64_t d2 = f2_pack(db, db);
+                    grow(fmaf(mx, unit, v));
+                    const float db = v + kTShift - (m == NEG_INF ? 0.f : m);
+                    const uint64_t c2 = f2_pack(unit, unit), d2 = f2_pack(db, db);
                     uint64_t sum = 0;
                     uint32_t x[32], y[32];
                     tmem_ld32(ts + 96, x);
@@ -1236,14 +1292,14 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                             y[i] = x[i];
                         tie32(y);
                         tmem_ld32(ts + 32 * max(c - 1, 0), x);       // the next, under this one's work
-                        exp32<Smem::Q8>(y, c2, d2, sum, place(c));
+                        exp32<true>(y, c2, d2, sum, place(c));
                     }
                     tmem_wait_ld();
                     tie32(x);
-                    float u, v;
-                    f2_unpack(sum, u, v);
-                    l = fmaf(u + v, iv, l);
-                } else if (!edge) {
+                    float p0, p1;
+                    f2_unpack(sum, p0, p1);
+                    l = fmaf(p0 + p1, val_inv(v0), l);
+                } else if (!Smem::Q8 && !edge) {
                     float mx = NEG_INF;
                     uint32_t x[4][32];
 #pragma unroll
@@ -1255,18 +1311,19 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         tie32(x[c]);
                         mx = max32(x[c], mx);
                     }
-                    grow(mx);
-                    const float db = dv - (m == NEG_INF ? 0.f : m);
-                    const uint64_t d2 = f2_pack(db, db);
+                    grow(mx * a.scale_log2);
+                    const float db = m == NEG_INF ? 0.f : -m;
+                    const uint64_t c2 = f2_pack(a.scale_log2, a.scale_log2), d2 = f2_pack(db, db);
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        exp32<Smem::Q8>(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c));
+                        exp32<false>(x[c], c2, d2, c & 1 ? sum1 : sum0, place(c));
                     float u, v;
                     f2_unpack(f2_add(sum0, sum1), u, v);
-                    l = fmaf(u + v, iv, l);
+                    l += u + v;
                 } else if (!odd) {
                     // 32 columns at a time, those that hold keys
+                    const float unit = Smem::Q8 ? key_unit(cs, units[0][0]) : a.scale_log2, v = Smem::Q8 ? val_log(units[1][0]) : 0.f;
                     float mx = NEG_INF;
 #pragma unroll 1
                     for (int c = 0; c < chunks; ++c) {
@@ -1277,9 +1334,9 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         mask32(x, c == 0 ? keep[0] : c == 1 ? keep[1] : c == 2 ? keep[2] : keep[3]);
                         mx = max32(x, mx);
                     }
-                    grow(mx);
-                    const float db = dv - (m == NEG_INF ? 0.f : m);
-                    const uint64_t d2 = f2_pack(db, db);
+                    grow(fmaf(mx, unit, v));
+                    const float db = v + (Smem::Q8 ? kTShift : 0.f) - (m == NEG_INF ? 0.f : m);
+                    const uint64_t c2 = f2_pack(unit, unit), d2 = f2_pack(db, db);
                     uint64_t sum = 0;
 #pragma unroll 1
                     for (int c = 0; c < chunks; ++c) {
@@ -1290,27 +1347,32 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         mask32(x, c == 0 ? keep[0] : c == 1 ? keep[1] : c == 2 ? keep[2] : keep[3]);
                         exp32<Smem::Q8>(x, c2, d2, sum, place(c));
                     }
-                    float u, v;
-                    f2_unpack(sum, u, v);
-                    l = fmaf(u + v, iv, l);
+                    float p0, p1;
+                    f2_unpack(sum, p0, p1);
+                    l = fmaf(p0 + p1, Smem::Q8 ? val_inv(units[1][0]) : 1.f, l);
                 } else {
-                    // V holds infinities or NaN in a tile that rows keep differently: the kept keys
-                    // one by one, so that none reaches a row that does not keep it (the first ones of
+                    // V holds infinities or NaN in a tile that rows keep differently, or keys have units of
+                    // their own: the kept ones one by one, so that none reaches a row that does not keep it (the first ones of
                     // a range write O, once nobody reads the last range's)
                     if (steps == 0 && it > 0 && !mbar_wait_warp(&sm.o_free, (it - 1) & 1, &sm.abort, err))
                         return;
                     const uint8_t *v0 = sm.ring[(2 * tile + 1) % Smem::kStages];
                     float mx = NEG_INF, sum = 0.f;
+                    // a key's units
+                    auto ku = [&](int k) {
+                        return !Smem::Q8 ? a.scale_log2 : key_unit(cs, flags & kDraft ? sm.own_unit[it % kTSegs][0][k] : units[0][k >> 4]);
+                    };
+                    auto vu = [&](int k) -> uint32_t { return flags & kDraft ? sm.own_unit[it % kTSegs][1][k] : units[1][k >> 4]; };
 #pragma unroll 1
                     for (int k = 0; k < 16 * (flags >> kGroups); ++k) {
                         uint32_t sk = tmem_ld1(ts + k);
                         tmem_wait_ld();
                         asm volatile("" : "+r"(sk));
                         const uint32_t kw = k < 32 ? keep[0] : k < 64 ? keep[1] : k < 96 ? keep[2] : keep[3];
-                        mx = (kw >> (k & 31)) & 1u ? fmaxf(mx, __uint_as_float(sk)) : mx;
+                        mx = (kw >> (k & 31)) & 1u ? fmaxf(mx, fmaf(__uint_as_float(sk), ku(k), Smem::Q8 ? val_log(vu(k)) : 0.f)) : mx;
                     }
                     grow(mx);
-                    const float db = dv - (m == NEG_INF ? 0.f : m);
+                    const float db = (Smem::Q8 ? kTShift : 0.f) - (m == NEG_INF ? 0.f : m);
 #pragma unroll 1
                     for (int dc = 0; dc < 8; ++dc) {              // 16 dims at a time
                         uint32_t raw[16];
@@ -1332,8 +1394,8 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                             asm volatile("" : "+r"(sk));
                             const uint32_t kw = k < 32 ? keep[0] : k < 64 ? keep[1] : k < 96 ? keep[2] : keep[3];
                             if ((kw >> (k & 31)) & 1u) {
-                                const float p = ex2(fmaf(__uint_as_float(sk), unit, db));
-                                sum += dc == 0 ? p : 0.f;
+                                const float p = ex2(fmaf(__uint_as_float(sk), ku(k), (Smem::Q8 ? val_log(vu(k)) : 0.f) + db));
+                                sum += dc > 0 ? 0.f : Smem::Q8 ? p * val_inv(vu(k)) : p;
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
                                     const uint4 v = *reinterpret_cast<const uint4 *>(
@@ -1356,7 +1418,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                             raw[i] = __float_as_uint(o[i]);
                         tmem_st16(to + 128 * wg + 16 * dc, raw);
                     }
-                    l = fmaf(sum, iv, l);
+                    l += sum;
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1375,13 +1437,36 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
         bool both = false;
         float M = m;
         if (!two) {
-            sm.ml[wg][r] = make_float2(M, l);
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&sm.ml_full);
-            if (!mbar_wait_warp(&sm.ml_full, joined++ & 1, &sm.abort, err))
-                return;
-            const float2 x0 = sm.ml[0][r], x1 = sm.ml[1][r];
+            float2 x0 = make_float2(M, l), x1 = x0;
+            if constexpr (Smem::Q8) {
+                // (one place a row, there is no room for two: the second warpgroup's, then the first's)
+                if (wg == 0) {
+                    if (!mbar_wait_warp(&sm.ml_full[0], joined & 1, &sm.abort, err))
+                        return;
+                    x1 = sm.ml[0][r];
+                    sm.ml[0][r] = x0;
+                } else {
+                    sm.ml[0][r] = x1;
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.ml_full[wg ^ 1]);
+                if (wg == 1) {
+                    if (!mbar_wait_warp(&sm.ml_full[1], joined & 1, &sm.abort, err))
+                        return;
+                    x0 = sm.ml[0][r];
+                }
+            } else {
+                sm.ml[wg][r] = x0;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&sm.ml_full[0]);
+                if (!mbar_wait_warp(&sm.ml_full[0], joined & 1, &sm.abort, err))
+                    return;
+                x0 = sm.ml[0][r];
+                x1 = sm.ml[1][r];
+            }
+            ++joined;
             M = fmaxf(x0.x, x1.x);
             // 1 where nothing but NaN (or no key) was met, so that a NaN stays
             f0 = x0.x == NEG_INF ? 1.f : ex2(x0.x - M);
@@ -1443,7 +1528,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                 }
             }
             if (valid && (two || wg == 0)) {
-                const float l2 = none ? NEG_INF : (M == NEG_INF ? 0.f : M) - (Smem::Q8 ? kTShift : 0.f) + tree_lg2(l);
+                const float l2 = none ? NEG_INF : (M == NEG_INF ? 0.f : M) - (Smem::Q8 ? kTShift + 127.f : 0.f) + tree_lg2(l);
                 if (!whole) {
                     if (in_bounds(prow, 2 * static_cast<int64_t>(gridDim.x) * a.rows_slot, err))
                         a.part_lse[prow] = l2;
@@ -1477,11 +1562,11 @@ __device__ __forceinline__ void tree_barriers(Smem &sm, int lane)
         {kTSegs, 1}, {kTSegs, users},
         {1, 1}, {1, 1},                                 // q_full, q_empty
         {2, 1}, {2, 4}, {2, 1},                         // s_full, p_full, o_done
-        {1, 1}, {1, 8}, {1, 8}, {1, 2},                 // seg_done, ml_full, o_free, drain
+        {1, 1}, {2, Smem::Q8 ? 4 : 8}, {1, 8}, {1, 2},  // seg_done, ml_full, o_free, drain
         {1, 8}, {2, 1}, {2, 4},                         // q_ready, own_full, own_max
     };
     constexpr int kAll = static_cast<int>((offsetof(Smem, seg) - offsetof(Smem, full)) / sizeof(uint64_t));
-    static_assert(2 * S + 2 * C + kTReady + 2 * kTSegs + 2 + 6 + 4 + 5 == kAll, "every barrier is set up");
+    static_assert(2 * S + 2 * C + kTReady + 2 * kTSegs + 2 + 6 + 5 + 5 == kAll, "every barrier is set up");
     for (int i = lane; i < kAll; i += 32) {
         int count = 1, end = 0;
 #pragma unroll

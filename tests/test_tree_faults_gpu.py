@@ -34,11 +34,12 @@ def unit(x):
 def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, bm=None, vscale=None, few=False):
     """The operator in 64 bits, over the keys that a row keeps alone, and how far it may be off:
       logits: 2^-17 of sum |q k| (128 fp32 terms), and 2^-17 for the exponent's multiply-add and exponential; over 8 bits q's
-      elements are f16, off by 2^-36 of their row's largest, and a drafted key's by 2^-39 of its own row's;
+      elements are f16, off by 2^-36 of their row's largest, and a drafted key's by 2^-27 of its own row's (half of f16's least
+      step, 2^-25, where the largest of rows within 2^12 of one another is at least 2^14), or of 2^-64;
       probabilities: bf16, half a step 2^-8; `few`: in two parts, 2^-16; f16 (8-bit caches) 2^-11, and 2^-25 where below
-      2^-14, in units of 2^-7 of the largest kept weight times unit (vscale: of the cache's V): at most
-      2^-32 max(u) sum |v| / u, u the units of the kept keys alone; a drafted value 2^-39 of its own row's largest, or
-      2^-103 (half of f16's least step at the smallest unit);
+      2^-14, in units of 2^-7 of the largest kept weight times unit (vscale: of the cache's V), a tile's units standing for
+      the largest within 2^12: at most 2^-20 max(u) sum |v| / u, u the units of the kept keys alone; a drafted value as a
+      drafted key;
       sums and joins: 2^-16.
     The output's own rounding, half a bf16 step, is left to the caller."""
     B, T, Hq, D = Q.shape
@@ -69,7 +70,7 @@ def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, bm=None, 
                     own = j[j >= L]
                     e += 2.0 ** -36 * np.abs(q).max(1) * np.abs(k[j]).sum(1).max() * SCALE
                     if len(own):
-                        e += 2.0 ** -39 * np.abs(q).sum(1) * np.maximum(np.abs(k[own]).max(), 2.0 ** -64) * SCALE
+                        e += 2.0 ** -27 * np.abs(q).sum(1) * np.maximum(np.abs(k[own]).max(), 2.0 ** -64) * SCALE
                 top = x.max(1, keepdims=True)
                 p = np.exp(x - top)
                 s = p.sum(1, keepdims=True)
@@ -79,9 +80,9 @@ def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, bm=None, 
                 tO[b, t, hs] = (p @ np.abs(v[j])) * (part + 2.0 ** -16 + 2 * e[:, None])
                 if vscale is not None:
                     u = np.concatenate([vscale[b, :L, h] / 64, unit(v[L:])])[j]
-                    tO[b, t, hs] += 2.0 ** -32 * u.max() * (np.abs(v[j]) / u[:, None]).sum(0)
+                    tO[b, t, hs] += 2.0 ** -20 * u.max() * (np.abs(v[j]) / u[:, None]).sum(0)
                     if len(own):
-                        tO[b, t, hs] += 2.0 ** -39 * np.maximum(np.abs(v[own]).max(), 2.0 ** -64)
+                        tO[b, t, hs] += 2.0 ** -27 * np.maximum(np.abs(v[own]).max(), 2.0 ** -64)
                 tL[b, hs, t] = e + np.abs(LSE[b, hs, t]) * 2.0 ** -20
     return O, LSE, tO, tL
 
@@ -167,5 +168,76 @@ def test_drafted_values_of_nothing(dev, dtype, value):
             V[:, 5, 1, 7] = value
         rows = [(b, t) for b in range(B) for t in range(T) if not (math.isinf(value) and t == 5)]
         check(dev, make_cache(B, max(lens) + 64, Hkv, dtype, 64, 0, 5), Q, K, V, lens, [T] * B, p.repeat(B, 0), [[FULL] * Hkv] * B, rows=rows)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+def test_some_rows_of_zero(dev, dtype):
+    """Blocks of zeros in the cache and drafted rows of zero among others."""
+    B, T, Hq, Hkv, lens = 2, 6, 8, 2, [500, 33]
+    Q, K, V = inputs(B, T, Hq, Hkv, 3)
+    c = make_cache(B, 512, Hkv, dtype, 16, 0, 5)
+    zero = torch.zeros(B, 48, Hkv, 128, dtype=BF16)
+    for s in (0, 144, 400):
+        write_ref(c, zero, tokens((B, 48, Hkv, 128), s) if s == 144 else zero, [s] * B, [48] * B)
+    K[:, 1], V[:, 1], V[:, 4] = 0.0, 0.0, 0.0
+    check(dev, c, Q, K, V, lens, [T] * B, random_tree(B, T, 1), [[FULL, SSA]] * B)
+
+
+@pytest.mark.parametrize("dtype,sb,page", [(E4M3, 16, 0), (INT8, 16, 64), (BF16, 64, 0)])
+@pytest.mark.parametrize("size", [10, 14, 40, 90, -40])
+def test_values_of_another_size_in_places_not_kept(dev, dtype, sb, page, size):
+    """Keys and values 2^size times the others', in rows that no node keeps and on a node that keeps its own alone: the others'
+    results are as if they were not there.  (-40: the others are the large ones.)"""
+    B, T, Hq, Hkv, lens = 2, 6, 8, 2, [500, 0]
+    p = np.array([[-1, 0, 1, 1, 0, 4]] * B, np.int32)
+    Q, K, V = inputs(B, T, Hq, Hkv, 3)
+    c = make_cache(B, 512, Hkv, dtype, sb, page, 4)
+    big, small = 2.0 ** max(size, 0), 2.0 ** min(size, 0)
+    # a window's end inside a tile, a sink's end inside another: the rows between are kept by none
+    kn, vn = tokens((B, 512, Hkv, 128), 50).float(), tokens((B, 512, Hkv, 128), 51).float()
+    write_ref(c, (kn * small).to(BF16), (vn * small).to(BF16), [0] * B, [512] * B)
+    for s in (256, 16):
+        write_ref(c, (kn[:, :32] * big).to(BF16), (vn[:, :32] * big).to(BF16), [s] * B, [32] * B)
+    for x in (K, V):
+        x.mul_(small)
+        x[:, 3] *= big / small
+    rows = [(b, t) for b in range(B) for t in range(T) if t != 3]
+    check(dev, c, (Q.float() / small).clamp(max=2.0 ** 100).to(BF16) if size < 0 else Q, K, V, lens, [T] * B, p, [[SSA, SSA], [FULL, SSA]], sink=10, window=200, rows=rows)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+def test_large_values_kept_with_others(dev, dtype):
+    """Blocks of different scales in a tile and drafted rows of different size, all kept: each within the bits of its own weight."""
+    B, T, Hq, Hkv, lens = 2, 9, 4, 1, [300, 40]
+    Q, K, V = inputs(B, T, Hq, Hkv, 3)
+    c = make_cache(B, 320, Hkv, dtype, 16, 0, 4)
+    r = np.random.RandomState(0)
+    for s in range(0, 320, 16):
+        x = [tokens((B, 16, Hkv, 128), 60 + s + i).float() * 2.0 ** float(r.randint(-6, 7)) * (1.0 if i else 0.25) for i in range(2)]
+        write_ref(c, *(y.to(BF16) for y in x), [s] * B, [16] * B)
+    V *= torch.from_numpy(2.0 ** r.randint(-6, 7, (B, T, 1, 1))).to(BF16)
+    check(dev, c, Q, K, V, lens, [T] * B, random_tree(B, T, 2), [[FULL]] * B)
+
+
+@pytest.mark.parametrize("dtype", [E4M3, INT8])
+def test_single_token_is_the_8bit_decode(dev, dtype):
+    """T = 1 equals the 8-bit decode over the cache with that token in it, outputs and log-sum-exps, where the token's numbers
+    are 8-bit ones at the scale of the block that it begins."""
+    B, Hq, Hkv, L = 3, 8, 2, [192, 64, 128]
+    c = make_cache(B, 256, Hkv, dtype, 64, 0, 7)
+    Kc, Vc = logical(c)
+    Q = inputs(B, 1, Hq, Hkv, 1)[0]
+    K, V = (torch.from_numpy(np.stack([x[b, L[b] - 1][None] for b in range(B)])).to(BF16) for x in (Kc, Vc))
+    depth, mask = plan(np.full((B, 1), -1, np.int32), [1] * B)
+    modes = [[FULL, SSA]] * B
+    ref = attend(*(x.double().numpy() for x in (Q, K, V)), Kc, Vc, L, [1] * B, depth, mask, modes, 4, 30, vscale=value_scales(c))
+    h = handle(c, dev)
+    m = torch.tensor(modes, dtype=torch.uint8, device=dev)
+    O, LSE = ea.ea_hybrid_attn_tree(Q.to(dev), K.to(dev), V.to(dev), h, i32(L, dev), i32(depth, dev), i32(mask, dev), m, sink=4, window=30)
+    ea.ea_cache_write(h, K.to(dev), V.to(dev), start=i32(L, dev))
+    o, lse = ea.ea_hybrid_attn_decode_q8(Q[:, 0].to(dev), h, i32(np.array(L) + 1, dev), m, sink=4, window=30)
+    a, b = O[:, 0].double().cpu().numpy(), o.double().cpu().numpy()
+    assert (np.abs(a - b) <= 2 * (bf16_half_ulp(np.maximum(np.abs(a), np.abs(b))) + ref[2][:, 0])).all()
+    assert (np.abs(LSE[:, :, 0].double().cpu().numpy() - lse.double().cpu().numpy()) <= 2 * ref[3][:, :, 0]).all()
 
 
