@@ -59,6 +59,7 @@ constexpr float kTShift = 7.f;                        // 8-bit caches: p is f16,
 constexpr int kTMinTiles = 2;                         // of a range at least (a power of two)
 constexpr int kTPartTiles = 4;                        // see tree_range
 constexpr int kTSpread = 12;                          // see tree_convert
+constexpr int kTFewKeys = 512;                        // bf16 caches: P V in two parts up to these, see exp32_parts
 constexpr int kTSms = 152;                            // a workspace's size depends on the grid
 
 enum { kEdge = 1, kDraft = 2, kRow0 = 4, kRow1 = 8, kMixed = 16, kWide = 32, kGroups = 8 };   // (from bit 8 on: 16-key groups)
@@ -144,7 +145,8 @@ __device__ __forceinline__ TreeUnit tree_unit(const TreeArgs &a, int u)
 struct TreeSeg {
     int valid;
     int b, h, v;                         // v: unit * pairs + pair
-    int mode, L, n, dead;
+    int mode, L, n;
+    bool dead, few;                      // no key is kept; no row keeps more than kTFewKeys of the cache
     int tok0, two;                       // first node, and whether there are two M tiles
     int t0, t1, nt;                      // tiles [t0, t1) of nt
     int slot;                            // of the partial result
@@ -455,6 +457,11 @@ __device__ __forceinline__ void tree_producer(const TreeMaps &tm, const TreeArgs
         s.L = x.L;
         s.n = x.n;
         s.dead = x.dead;
+        if constexpr (!Q8) {
+            // (the window of depth 0; of a block row's last block one key at least)
+            const int kept = x.mode == EA_FULL ? x.L : x.mode == EA_SSA ? x.n0 + x.L - max(x.n0, x.L - a.window + 1) : (x.nt - 2) * kTTile + 1;
+            s.few = kept <= kTFewKeys;
+        }
         s.tok0 = 2 * pair * a.tpt;
         s.two = s.tok0 + a.tpt < x.n;
         s.t0 = max(from - kTPartTiles, 0);
@@ -674,6 +681,7 @@ __device__ __forceinline__ void tree_pv(const TreeArgs &a, Smem &sm, uint32_t tm
     for (uint32_t it = 0; (sp = tree_take(a, sm, it)) != nullptr; ++it) {
         const int two = TWO ? __shfl_sync(0xffffffffu, sp->two, 0) : 0;
         const int nt = __shfl_sync(0xffffffffu, sp->t1 - sp->t0, 0);
+        const int few = Smem::Q8 ? 0 : __shfl_sync(0xffffffffu, sp->few, 0);
         // (O is still read for the range's part before)
         if (it > 0 && !mbar_wait_warp(&sm.o_free, (it - 1) & 1, abort, err))
             break;
@@ -703,6 +711,13 @@ __device__ __forceinline__ void tree_pv(const TreeArgs &a, Smem &sm, uint32_t tm
 #pragma unroll 1
                 for (int k = 0; k < groups; ++k)
                     mma_ts(go, to, tp + 32 * (k >> 1) + 8 * (k & 1), vd + k * (2048 >> 4), kIdPV, k ? 1u : more);
+            }
+            if (few && !odd) {
+                // P's second part
+                const int groups = flags >> kGroups;
+#pragma unroll 2
+                for (int k = 0; k < groups; ++k)
+                    mma_ts(go, to, tp + 32 * (k >> 1) + 8 * (k & 1) + 16, vd + k * (2048 >> 4), kIdPV, 1u);
             }
             commit_if(go, &sm.o_done[w]);
             if (!two || w == 1)
@@ -1133,6 +1148,31 @@ __device__ __forceinline__ void exp32(const uint32_t (&x)[32], uint64_t c, uint6
     tmem_st16(tp, p);
 }
 
+// The same with p in two bf16 parts, the second one in the other half of the columns: a row that keeps few keys takes
+// one probability's rounding, 2^-8 of it, almost whole (outputs of values in [2.2, 3.8) over 2 to 500 keys were off by up to
+// 0.01 beyond their own rounding).  So do the prefill and the decode, up to the same number.  (256 sequences of 512, trees of 4:
+// 140 us without, 177 with; nothing where more keys are kept.)  The first part is cut, not rounded, and the second 2^-23 p more than what is left,
+// so that both are positive wherever p is: an infinity among the values stays one.
+__device__ __forceinline__ void exp32_parts(const uint32_t (&x)[32], uint64_t c, uint64_t d, uint64_t &sum, uint32_t tp)
+{
+    uint32_t p[32];
+    const uint64_t more = f2_pack(1.f + 0x1p-23f, 1.f + 0x1p-23f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float e0, e1;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c, d), e0, e1);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
+        const uint64_t e = f2_pack(e0, e1);
+        sum = f2_add(sum, e);
+        const uint32_t u0 = __float_as_uint(e0), u1 = __float_as_uint(e1);
+        p[i] = __byte_perm(u0, u1, 0x7632);
+        f2_unpack(f2_fma(e, more, f2_pack(__uint_as_float((u0 & 0xffff0000u) | 0x80000000u), __uint_as_float((u1 & 0xffff0000u) | 0x80000000u))), e0, e1);
+        p[16 + i] = pack_bf16x2(e0, e1);
+    }
+    tmem_st32(tp, p);
+}
+
 // A row's 128 scores go through its thread's registers once (bf16 caches); beside the
 // converting warps there is no room for them, they are read from TMEM twice.  The 32 columns'
 // P takes the place of the first half of their S.
@@ -1299,7 +1339,7 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                     float p0, p1;
                     f2_unpack(sum, p0, p1);
                     l = fmaf(p0 + p1, val_inv(v0), l);
-                } else if (!Smem::Q8 && !edge) {
+                } else if (!Smem::Q8 && !edge && !s.few) {
                     float mx = NEG_INF;
                     uint32_t x[4][32];
 #pragma unroll
@@ -1331,7 +1371,8 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         tmem_ld32(ts + 32 * c, x);
                         tmem_wait_ld();
                         tie32(x);
-                        mask32(x, c == 0 ? keep[0] : c == 1 ? keep[1] : c == 2 ? keep[2] : keep[3]);
+                        if (Smem::Q8 || edge)
+                            mask32(x, c == 0 ? keep[0] : c == 1 ? keep[1] : c == 2 ? keep[2] : keep[3]);
                         mx = max32(x, mx);
                     }
                     grow(fmaf(mx, unit, v));
@@ -1344,8 +1385,12 @@ __device__ __forceinline__ void tree_softmax(const TreeArgs &a, Smem &sm, uint32
                         tmem_ld32(ts + 32 * c, x);
                         tmem_wait_ld();
                         tie32(x);
-                        mask32(x, c == 0 ? keep[0] : c == 1 ? keep[1] : c == 2 ? keep[2] : keep[3]);
-                        exp32<Smem::Q8>(x, c2, d2, sum, place(c));
+                        if (Smem::Q8 || edge)
+                            mask32(x, c == 0 ? keep[0] : c == 1 ? keep[1] : c == 2 ? keep[2] : keep[3]);
+                        if (!Smem::Q8 && s.few)
+                            exp32_parts(x, c2, d2, sum, place(c));
+                        else
+                            exp32<Smem::Q8>(x, c2, d2, sum, place(c));
                     }
                     float p0, p1;
                     f2_unpack(sum, p0, p1);

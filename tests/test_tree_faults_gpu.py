@@ -36,7 +36,7 @@ def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, bm=None, 
       logits: 2^-17 of sum |q k| (128 fp32 terms), and 2^-17 for the exponent's multiply-add and exponential; over 8 bits q's
       elements are f16, off by 2^-36 of their row's largest, and a drafted key's by 2^-27 of its own row's (half of f16's least
       step, 2^-25, where the largest of rows within 2^12 of one another is at least 2^14), or of 2^-64;
-      probabilities: bf16, half a step 2^-8; `few`: in two parts, 2^-16; f16 (8-bit caches) 2^-11, and 2^-25 where below
+      probabilities: bf16, half a step 2^-8; `few`: in two parts, the second less than 2^-7 of it, half a step 2^-15; f16 (8-bit caches) 2^-11, and 2^-25 where below
       2^-14, in units of 2^-7 of the largest kept weight times unit (vscale: of the cache's V), a tile's units standing for
       the largest within 2^12: at most 2^-20 max(u) sum |v| / u, u the units of the kept keys alone; a drafted value as a
       drafted key;
@@ -76,7 +76,7 @@ def attend(Q, K, V, Kc, Vc, lens, n, depth, mask, modes, sink, window, bm=None, 
                 s = p.sum(1, keepdims=True)
                 p /= s
                 O[b, t, hs], LSE[b, hs, t] = p @ v[j], (top + np.log(s))[:, 0]
-                part = 2.0 ** -11 if vscale is not None else 2.0 ** -16 if few else 2.0 ** -8
+                part = 2.0 ** -11 if vscale is not None else 2.0 ** -15 if few else 2.0 ** -8
                 tO[b, t, hs] = (p @ np.abs(v[j])) * (part + 2.0 ** -16 + 2 * e[:, None])
                 if vscale is not None:
                     u = np.concatenate([vscale[b, :L, h] / 64, unit(v[L:])])[j]
@@ -239,5 +239,38 @@ def test_single_token_is_the_8bit_decode(dev, dtype):
     a, b = O[:, 0].double().cpu().numpy(), o.double().cpu().numpy()
     assert (np.abs(a - b) <= 2 * (bf16_half_ulp(np.maximum(np.abs(a), np.abs(b))) + ref[2][:, 0])).all()
     assert (np.abs(LSE[:, :, 0].double().cpu().numpy() - lse.double().cpu().numpy()) <= 2 * ref[3][:, :, 0]).all()
+
+
+@pytest.mark.parametrize("page", [0, 64])
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 8, 2), (5, 4, 2), (24, 16, 2)])
+def test_few_kept_keys(dev, T, Hq, Hkv, page):
+    """bf16 caches, rows that keep at most 512 keys of the cache: probabilities in two parts, as the decode has them, so that
+    little but the output's own rounding is left.  Values of one sign and a large offset, which each probability's error enters whole."""
+    lens = [0, 2, 5, 60, 130, 300, 500, 5000]
+    B = len(lens)
+    c = make_cache(B, 5056, Hkv, BF16, 64, page, 3)
+    g = torch.Generator().manual_seed(1)
+    sign = torch.where(torch.rand(128, generator=g) < 0.5, -1.0, 1.0)
+    offset = lambda *s: ((2.2 + 1.6 * torch.rand(*s, 128, generator=g)) * sign).to(BF16)  # noqa: E731
+    write_ref(c, tokens((B, 5056, Hkv, 128), 9), offset(B, 5056, Hkv), [0] * B, [5056] * B)
+    Q, K, _ = inputs(B, T, Hq, Hkv, 3)
+    modes = [[FULL, SSA]] * (B - 1) + [[SSA, SSA]]
+    check(dev, c, Q, K, offset(B, T, Hkv), lens, [T] * B, random_tree(B, T, 4, "chain" if T == 24 else "tree"), modes, sink=16, window=128, few=True)
+
+
+def test_infinite_values_over_few_keys(dev):
+    """An infinity among values that all rows keep stays one, whatever its probability's parts are."""
+    B, T, Hq, lens = 2, 4, 4, [64, 300]
+    Q, K, V = inputs(B, T, Hq, 1, 3)
+    c = make_cache(B, 320, 1, BF16, 64, 0, 2)
+    c["K"][:] = 0.0                                       # equal weights: powers of two, or not
+    K.zero_()
+    c["V"][0, 5, 0, 17], c["V"][1, 7, 0, 19] = math.inf, -math.inf
+    depth, mask = (i32(x, dev) for x in plan(random_tree(B, T, 3, "chain"), [T] * B))
+    O, _ = ea.ea_hybrid_attn_tree(*(x.to(dev) for x in (Q, K, V)), handle(c, dev), i32(lens, dev), depth, mask,
+                                  torch.zeros(B, 1, dtype=torch.uint8, device=dev), sink=0, window=1)
+    assert torch.isposinf(O[0, :, :, 17]).all() and torch.isneginf(O[1, :, :, 19]).all()
+    O[0, :, :, 17], O[1, :, :, 19] = 0.0, 0.0
+    assert torch.isfinite(O).all()
 
 
