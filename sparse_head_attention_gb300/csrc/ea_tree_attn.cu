@@ -1990,9 +1990,9 @@ extern "C" ea_status ea_hybrid_attn_tree(const void *Q, const void *K, const voi
     a.pairs = w.pairs;
     a.rows_slot = w.rows_slot;
     a.nBm = static_cast<int>(nBm);
-    // positions stay below 2^31 - 128: larger limits say the same
+    // positions stay below 2^31 - 128: larger limits say the same (and the window's first column, less 96, stays in 32 bits)
     a.sink = sink < (1 << 30) ? sink : 0x7fffffff;
-    a.window = window;
+    a.window = window < 0x7fffffff - 128 ? window : 0x7fffffff - 128;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.inv_Hkv = 1.f / static_cast<float>(Hkv);
     a.inv_g = 1.f / static_cast<float>(a.g);

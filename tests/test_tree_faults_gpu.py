@@ -274,3 +274,18 @@ def test_infinite_values_over_few_keys(dev):
     assert torch.isfinite(O).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, INT8])
+def test_the_widest_window_and_sink(dev, dtype):
+    """Windows and sinks up to 2^31 - 1 keep what any larger than the cache keeps."""
+    B, T, Hq = 3, 20, 4
+    Q, K, V = (x.to(dev) for x in inputs(B, T, Hq, 1, 2))
+    h = handle(make_cache(B, 320, 1, dtype, 64, 0, 1), dev)
+    depth, mask = (i32(x, dev) for x in plan(random_tree(B, T, 3, "chain"), [T] * B))
+    m = torch.full((B, 1), SSA, dtype=torch.uint8, device=dev)
+    call = lambda s, w: ea.ea_hybrid_attn_tree(Q, K, V, h, i32([300, 0, 1], dev), depth, mask, m, sink=s, window=w)  # noqa: E731
+    ref = call(0, 1000)
+    for s, w in ((0, 2 ** 31 - 1), (2 ** 31 - 1, 1), (2 ** 31 - 1, 2 ** 31 - 1), (0, 2 ** 30)):
+        got = call(s, w)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
