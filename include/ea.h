@@ -756,8 +756,9 @@ ea_status ea_key_weights(const void *Q, const void *K, const float *LSE, const i
  * a = p * inv_freq[i]:
  *   out_i = rope_scale * (x_i cos a - x_j sin a)
  *   out_j = rope_scale * (x_j cos a + x_i sin a)
- * and the dims from rot on are copied.  Angles are exact to 2^-31 of a turn at every
- * position; products and sums are fp32, rounded once.
+ * and the dims from rot on are copied.  Angles are off by 2^-26 of a turn at most (fp32's
+ * own rounding, and 2^-31 besides) at every position; products and sums are fp32, rounded
+ * once.
  *
  *   Q, Q_out     device bf16 [B][T][Hq][d], strides q_str / qo_str; Hq = 0: none
  *   K, K_out     device bf16 [B][T][Hkv][d], strides k_str / ko_str; Hkv = 0: none
