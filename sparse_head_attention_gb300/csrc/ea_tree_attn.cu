@@ -11,12 +11,12 @@
 //
 // What bounds it: each kept key's K and V are read once for up to 256 rows (two M tiles
 // share a key tile), 64 KB a tile of bf16, which an SM receives in 1.45 us at the measured
-// HBM rate; two M tiles take 0.55 us of tensor core and 0.5 of the SFU.  So HBM where one M tile
-// does: 16 sequences of 64K with trees of 32 take 0.65 ms, 0.97 of the measured rate.  Two M tiles
-// take 2.0 us a tile (0.88 ms with trees of 64, 1250 TFLOP/s): S = Q K^T, the softmax and O += P V
-// of a tile wait for one another, and TMEM has no room for a second S of each.  An 8-bit cache's
-// tile takes 1.3 us (0.57 ms with trees of 16, 0.55 of the measured rate): the same chain, beside the
-// conversion.
+// HBM rate; an M tile takes 0.66 us of tensor core (at the measured bf16 rate) and 0.25 of the SFU.
+// So HBM where one M tile does: 16 sequences of 64K with trees of 32 take 0.63 - 0.66 ms by GPU, 0.97 - 1.0 of
+// the measured rate.  Two M tiles take 2.0 us a tile (0.87 - 0.89 ms with trees of 64, 1250 TFLOP/s), 1.3 of it tensor core:
+// S = Q K^T, the softmax and O += P V of a tile wait for one another, and TMEM has no room for a
+// second S of each.  An 8-bit cache's tile takes 1.3 us (0.59 ms with trees of 16, 0.54 of the
+// measured rate): the same chain, beside the conversion.
 //
 // Work.  Key tiles of all (sequence, KV head, pair of M tiles) form one line, which is cut
 // into equal ranges, one a CTA: no CTA idles, and at most two ranges of a CTA's begin or
@@ -32,7 +32,7 @@
 //   warp 11      Q, and V's rows that no query row keeps are zeroed before the product (0 * NaN is
 //                NaN), and tiles of which some rows keep a key and others do not are searched
 //                for infinities and NaN; such a tile's product is taken by the softmax warps,
-//                key by key
+//                key by key, as are 8-bit tiles whose scales are far apart (tree_convert)
 //   warps 12-19  8-bit caches: tiles of codes, that TMA brought, become f16 ones in the ring
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -895,7 +895,7 @@ __device__ __forceinline__ uint4 bf16_to_f16(const uint4 &v, float f)
 // lanes take the second half first: two rows' codes then lie in different banks).
 // A row an iteration, the next one's codes under its work: five roles take turns on a scheduler, and
 // what bounded them when their loops were unrolled was instruction fetch (16 sequences of 64K: 680 us
-// with the rows unrolled here and half of the columns in the softmax, 573 now).
+// with the rows unrolled here and half of the columns in the softmax, 587 now).
 template <bool E4M3, class Smem>
 __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs &a, Smem &sm, int kv, int ct, int lane)
 {
