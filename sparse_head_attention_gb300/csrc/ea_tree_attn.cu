@@ -752,7 +752,7 @@ __device__ __forceinline__ void tree_fix(const TreeMaps &tm, const TreeArgs &a, 
         const TreeSeg &s = *sp;
         // the queries
         if (!mbar_wait_warp(&sm.q_empty, (it & 1) ^ 1, &sm.abort, err))
-            return;
+            break;
         if (lane == 0) {
             const int tiles = sizeof(sm.q) > kTBytes && s.two ? 2 : 1;
             mbar_arrive_expect_tx(&sm.q_full, static_cast<uint32_t>(tiles * a.g * a.tpt) * 256u);
@@ -902,7 +902,7 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
     constexpr int kStages = Smem::kStages, kCodes = Smem::kCodes;
     static_assert(kStages % 2 == 0 && kCodes % 2 == 0, "a stage belongs to K or to V");
     uint32_t *err = &a.hdr->error;
-    uint32_t entry = kv, codes = kv, tile = 0, own = 0;
+    uint32_t entry = kv, codes = kv, tile = 0, own = 1;          // (own: one more than loads issued)
     const int piece = ct & 7, r0 = ct >> 3, flip = r0 & 1;
     const uint32_t in0 = r0 * 128 + 64 * flip + 8 * piece, in1 = in0 ^ 64u;
     const uint32_t at0 = flip * kTHalf + r0 * 128 + ((piece ^ (r0 & 7)) << 4), at1 = at0 ^ static_cast<uint32_t>(kTHalf);
@@ -925,6 +925,7 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                 }
                 if (ct == 0)
                     tree_load_own(tm, dst, kv, s, &sm.own_full[kv]);
+                ++own;
                 __syncwarp();
                 if (!mbar_wait_warp(&sm.own_full[kv], own & 1, &sm.abort, err)) {
                     ok = false;
@@ -970,7 +971,6 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
                         *part(c) = bf16_to_f16(*part(c), f);
                 if (ct == 0 && kv == 0)
                     sm.tile[tile % kTInfos] = tree_own_tile(s.L, s.n);
-                ++own;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
@@ -1042,9 +1042,9 @@ __device__ __forceinline__ void tree_convert(const TreeMaps &tm, const TreeArgs 
             tree_done(sm, it);
     }
     // Before leaving on an abort, let the copies already issued land.
-    if (ct < 32 && own > 0 && __any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
+    if (ct < 32 && own > 1 && __any_sync(0xffffffffu, *static_cast<volatile int *>(&sm.abort))) {
         volatile int no_abort = 0;
-        mbar_wait_warp(&sm.own_full[kv], (own - 1) & 1, &no_abort, nullptr);
+        mbar_wait_warp(&sm.own_full[kv], own & 1, &no_abort, nullptr);
     }
 }
 
